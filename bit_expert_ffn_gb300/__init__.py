@@ -23,8 +23,10 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE = 0, 1, 2, 3
 MOE_ERR_CUDA, MOE_ERR_TIMEOUT, MOE_ERR_NONFINITE, MOE_ERR_BOUNDS = 4, 5, 6, 7
 MOE_ERR_RANGE = 8
 MOE_ID_NOT_LOCAL = -1
-MOE_F32, MOE_BF16 = 0, 1
+MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
 MOE_PATH_AUTO, MOE_PATH_DECODE, MOE_PATH_PREFILL, MOE_PATH_PREFILL_FP8 = 0, 1, 2, 3
+MOE_MX4_PLAIN, MOE_MX4_SWIGLU = 0, 1
+MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GATE_CHANNEL = 0, 1, 2
 RMS_EPS = 1e-6  # normalisation in front of each stacked layer
 
 _lock = threading.Lock()
@@ -102,6 +104,19 @@ _SIGS = {
                               ctypes.POINTER(moe_decode_options), _P, _P, _P, _SZ, _P, _P],
     "moe_rms_norm_bf16": [_P, _P, _I32, _I32, ctypes.c_float, _P],
     "moe_selftest_barrier": [ctypes.c_uint, _I32, _P, _SZ, _P, _P],
+    "moe_dispatch": [_P, _I32, _I64, _I32, _I32, _I32, _I32, _P, _P, _P, _P],
+    "moe_dispatch_backward": [_P, _I32, _I32, _I32, _I32, _P, _P, _P],
+    "moe_combine": [_P, _I32, _I32, _I32, _I32, _P, _P, _P, _I32, _I32, _P],
+    "moe_combine_backward": [_P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P],
+    "moe_mx4_size": [_I64, _I64, _PSZ, _PSZ],
+    "moe_mx4_quantise": [_P, _I32, _I64, _I64, _I64, _P, _P, _P, _P],
+    "moe_mx4_dequantise": [_P, _P, _I64, _I64, _P, _I32, _P],
+    "moe_mx4_matmul": [_P, _P, _I32, _I32, _I32, _P, _P, _I32, _P, _P, _I32, _I32, _P, _P],
+    "moe_block_norm": [_P, _I32, _I64, _P, _I32, _I64, _I32, _I32, _P, _P, _P, _I32, ctypes.c_float, ctypes.c_float, _P,
+                       _P, _P],
+    "moe_block_norm_backward_workspace_size": [_I32, _I32, _I32, _PSZ],
+    "moe_block_norm_backward": [_P, _I32, _I64, _P, _I32, _I64, _I32, _I32, _P, _P, _P, _I32, ctypes.c_float,
+                                ctypes.c_float, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P],
 }
 
 
@@ -165,6 +180,30 @@ def _ptr(t):
     return t.data_ptr() if t.numel() else None
 
 
+_BYTES = {MOE_F32: 4, MOE_BF16: 2, MOE_F16: 2}
+
+
+def _packed(t, name, n, size):
+    """The pointer of a packed buffer of at least n elements of `size` bytes (a tensor), or of a raw address."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_contiguous() or t.element_size() != size or t.numel() < n:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{name} must be a packed tensor of at least {n} elements of {size} bytes "
+                                            f"(got {tuple(t.shape)}, strides {t.stride()}, {t.dtype})")
+    return t.data_ptr() if n else None
+
+
+def _rows(t, name, n, cols, dtype):
+    """Pointer and row stride of n rows of `cols` elements: a packed tensor, a 2D one whose rows are packed (stride 0
+    repeats one row), or a raw address of packed rows."""
+    if t is None or isinstance(t, int):
+        return t, cols
+    if t.dim() == 2 and t.element_size() == _BYTES.get(dtype) and t.shape[0] >= n and t.shape[1] == cols and (
+            t.stride(1) == 1 or cols == 1):
+        return (t.data_ptr(), t.stride(0) if n > 1 else cols) if n else (None, cols)
+    return _packed(t, name, n * cols, _BYTES.get(dtype, 0)), cols
+
+
 def _stream(stream=None):
     """The stream handle: an int, a torch stream, or the current torch stream."""
     if isinstance(stream, int):
@@ -172,7 +211,7 @@ def _stream(stream=None):
     if stream is None:
         import torch
 
-        if not torch.cuda.is_available():  # host-side argument checks still run
+        if not (torch.cuda.is_initialized() or torch.cuda.is_available()):  # host-side argument checks still run
             return ctypes.c_void_p(0)
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
@@ -313,6 +352,116 @@ def moe_rms_norm_bf16(x, out, T, H, eps=None, stream=None):
 def moe_selftest_barrier(extra_arrivals, timeout_ms, ws, ws_bytes, dev_status=None, stream=None):
     _check(lib().moe_selftest_barrier(extra_arrivals, timeout_ms, _ptr(ws), ws_bytes, _ptr(dev_status),
                                       _stream(stream)), "moe_selftest_barrier")
+
+
+# ----------------------------------------------------------------- rows to their experts and back
+
+def moe_dispatch(x, dtype, T, H, k, E, offsets, inv_perm, out, stream=None):
+    """out[inv_perm[t, j]] = x[t]; rows of no pair are zero.  x: [T][H], packed rows at any row stride."""
+    xp, xs = _rows(x, "x", T, H, dtype)
+    _check(lib().moe_dispatch(xp, dtype, xs, T, H, k, E, _packed(offsets, "offsets", E + 1, 4),
+                              _packed(inv_perm, "inv_perm", T * k, 4), _packed(out, "out", T * k * H, _BYTES.get(dtype, 0)),
+                              _stream(stream)), "moe_dispatch")
+
+
+def moe_dispatch_backward(drows, dtype, T, H, k, inv_perm, dx, stream=None):
+    """dx[t] = sum_j drows[inv_perm[t, j]]."""
+    b = _BYTES.get(dtype, 0)
+    _check(lib().moe_dispatch_backward(_packed(drows, "drows", T * k * H, b), dtype, T, H, k,
+                                       _packed(inv_perm, "inv_perm", T * k, 4), _packed(dx, "dx", T * H, b),
+                                       _stream(stream)), "moe_dispatch_backward")
+
+
+def moe_combine(y, dtype, T, H, k, w, inv_perm, out, out_dtype=MOE_F32, accumulate=False, stream=None):
+    """out[t] (+)= sum_j w[t, j] * y[inv_perm[t, j]]."""
+    _check(lib().moe_combine(_packed(y, "y", T * k * H, _BYTES.get(dtype, 0)), dtype, T, H, k, _packed(w, "w", T * k, 4),
+                             _packed(inv_perm, "inv_perm", T * k, 4),
+                             _packed(out, "out", T * H, _BYTES.get(out_dtype, 0)), out_dtype, int(accumulate),
+                             _stream(stream)), "moe_combine")
+
+
+def moe_combine_backward(dout, y, dtype, T, H, k, E, offsets, w, inv_perm, dy, dw, stream=None):
+    """dy[inv_perm[t, j]] = w[t, j] * dout[t], dw[t, j] = <dout[t], y[inv_perm[t, j]]>."""
+    b = _BYTES.get(dtype, 0)
+    _check(lib().moe_combine_backward(_packed(dout, "dout", T * H, b), _packed(y, "y", T * k * H, b), dtype, T, H, k, E,
+                                      _packed(offsets, "offsets", E + 1, 4), _packed(w, "w", T * k, 4),
+                                      _packed(inv_perm, "inv_perm", T * k, 4), _packed(dy, "dy", T * k * H, b),
+                                      _packed(dw, "dw", T * k, 4), _stream(stream)), "moe_combine_backward")
+
+
+# ----------------------------------------------------------------- 4-bit floating point matrices
+
+def moe_mx4_size(rows: int, cols: int):
+    """(bytes of codes, bytes of scales) of a [rows][cols] matrix; cols a multiple of 32."""
+    cb, sb = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(lib().moe_mx4_size(rows, cols, ctypes.byref(cb), ctypes.byref(sb)), "moe_mx4_size")
+    return cb.value, sb.value
+
+
+def _mx4(codes, scales, name, rows, cols):
+    return (_packed(codes, name + "codes", rows * (cols // 2), 1),
+            _packed(scales, name + "scales", rows * ((cols + 255) // 256) * 8, 1))
+
+
+def moe_mx4_quantise(x, dtype, rows, cols, codes, scales, dev_status=None, stream=None):
+    """x [rows][cols] (rows packed, any row stride) to e2m1 codes and e8m0 scales (uint8 tensors of moe_mx4_size)."""
+    if not isinstance(x, int) and x is not None and x.dim() > 2 and x.is_contiguous():
+        x = x.view(-1, cols) if x.shape[-1] == cols else x
+    xp, xs = _rows(x, "x", rows, cols, dtype)
+    cp, sp = _mx4(codes, scales, "", rows, cols)
+    _check(lib().moe_mx4_quantise(xp, dtype, xs, rows, cols, cp, sp, _ptr(dev_status), _stream(stream)),
+           "moe_mx4_quantise")
+
+
+def moe_mx4_dequantise(codes, scales, rows, cols, out, dtype=MOE_BF16, stream=None):
+    """The values that codes and scales stand for."""
+    cp, sp = _mx4(codes, scales, "", rows, cols)
+    _check(lib().moe_mx4_dequantise(cp, sp, rows, cols, _packed(out, "out", rows * cols, _BYTES.get(dtype, 0)), dtype,
+                                    _stream(stream)), "moe_mx4_dequantise")
+
+
+def moe_mx4_matmul(w_codes, w_scales, E, N, K, x_codes, x_scales, rows, offsets, out, out_dtype=MOE_F32,
+                   epilogue=MOE_MX4_PLAIN, dev_status=None, stream=None):
+    """out[p] = x[p] W_e^T (or silu(gate) * up of it) for the rows p of each group e; offsets None: one group (E = 1)."""
+    wc, ws = _mx4(w_codes, w_scales, "w_", E * N * (2 if epilogue == MOE_MX4_SWIGLU else 1), K)
+    xc, xs = _mx4(x_codes, x_scales, "x_", rows, K)
+    _check(lib().moe_mx4_matmul(wc, ws, E, N, K, xc, xs, rows, _packed(offsets, "offsets", E + 1, 4),
+                                _packed(out, "out", rows * N, _BYTES.get(out_dtype, 0)), out_dtype, epilogue,
+                                _ptr(dev_status), _stream(stream)), "moe_mx4_matmul")
+
+
+# ----------------------------------------------------------------- norms around a block
+
+def _gate_size(gate_kind, T, H):
+    return T if gate_kind == MOE_GATE_TOKEN else H
+
+
+def moe_block_norm(x, res_dtype, b, dtype, T, H, w_post, w_pre, gate, gate_kind, alpha, eps, y, u, stream=None):
+    """y = x + alpha * gate * w_post * rmsnorm(b), u = w_pre * rmsnorm(y).  x and b: packed rows at any row stride."""
+    xp, xs = _rows(x, "x", T, H, res_dtype)
+    bp, bs = _rows(b, "b", T, H, dtype)
+    _check(lib().moe_block_norm(xp, res_dtype, xs, bp, dtype, bs, T, H, _packed(w_post, "w_post", H, 4),
+                                _packed(w_pre, "w_pre", H, 4), _packed(gate, "gate", _gate_size(gate_kind, T, H), 4),
+                                gate_kind, alpha, eps, _packed(y, "y", T * H, _BYTES.get(res_dtype, 0)),
+                                _packed(u, "u", T * H, _BYTES.get(dtype, 0)), _stream(stream)), "moe_block_norm")
+
+
+def moe_block_norm_backward_workspace_size(T, H, gate_kind=MOE_GATE_NONE):
+    return _size(lib().moe_block_norm_backward_workspace_size, T, H, gate_kind)
+
+
+def moe_block_norm_backward(x, res_dtype, b, dtype, T, H, w_post, w_pre, gate, gate_kind, alpha, eps, dy, du, dx, db,
+                            dw_post=None, dw_pre=None, dgate=None, ws=None, ws_bytes=0, stream=None):
+    """Gradients of moe_block_norm for dy and du (either may be None)."""
+    xp, xs = _rows(x, "x", T, H, res_dtype)
+    bp, bs = _rows(b, "b", T, H, dtype)
+    rb, ab, n = _BYTES.get(res_dtype, 0), _BYTES.get(dtype, 0), _gate_size(gate_kind, T, H)
+    _check(lib().moe_block_norm_backward(
+        xp, res_dtype, xs, bp, dtype, bs, T, H, _packed(w_post, "w_post", H, 4), _packed(w_pre, "w_pre", H, 4),
+        _packed(gate, "gate", n, 4), gate_kind, alpha, eps, _packed(dy, "dy", T * H, rb), _packed(du, "du", T * H, ab),
+        _packed(dx, "dx", T * H, rb), _packed(db, "db", T * H, ab), _packed(dw_post, "dw_post", H, 4),
+        _packed(dw_pre, "dw_pre", H, 4), _packed(dgate, "dgate", n, 4), _ptr(ws), ws_bytes, _stream(stream)),
+        "moe_block_norm_backward")
 
 
 def header_functions():

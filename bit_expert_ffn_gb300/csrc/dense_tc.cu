@@ -331,6 +331,26 @@ moe_status make_tmap_2d(CUtensorMap *map, const void *base, CUtensorMapDataType 
     return MOE_OK;
 }
 
+moe_status make_tmap_bytes_3d(CUtensorMap *map, const void *base, int64_t mats, int64_t rows, int64_t row_bytes,
+                              int box_rows)
+{
+    EncodeTiled enc;
+    moe_status st = encode_fn(&enc);
+    if (st != MOE_OK) return st;
+    if (mats < 1 || rows < 1 || row_bytes < 1 || !aligned16(base) || row_bytes % 16 != 0)
+        return fail(MOE_ERR_INVALID_ARG, "tensor map: %lld x %lld rows of %lld bytes at %p", (long long)mats,
+                    (long long)rows, (long long)row_bytes, base);
+    cuuint64_t dims[3] = {(cuuint64_t)row_bytes, (cuuint64_t)rows, (cuuint64_t)mats};
+    cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)(rows * row_bytes)};
+    cuuint32_t box[3] = {128, (cuuint32_t)box_rows, 1};
+    cuuint32_t elem[3] = {1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, elem,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return MOE_OK;
+}
+
 bool dense_tc_supported(const DenseGemm &g, DenseEpi epi)
 {
     if (g.M < 1 || g.N < 1 || g.K < 64 || g.K % 64 || g.a_cols % 64 || g.b_cols % 64) return false;

@@ -52,4 +52,10 @@ moe_status make_tmap_2d(CUtensorMap *map, const void *base, CUtensorMapDataType 
                         int64_t cols, int box_cols, int box_rows,
                         CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
+// Tensor map of [mats][rows][row_bytes] with boxes of 128 bytes x box_rows x 1
+// (128-byte swizzle): rows past a matrix's last read as zeros, not as the next
+// matrix's.
+moe_status make_tmap_bytes_3d(CUtensorMap *map, const void *base, int64_t mats, int64_t rows, int64_t row_bytes,
+                              int box_rows);
+
 }  // namespace moe

@@ -1,0 +1,306 @@
+// rows.cu -- moe_dispatch, moe_combine and their gradients: token rows copied
+// to their pairs' places in expert order, and the pairs' rows summed back.
+//
+// All four are bound by memory: a pair row crosses HBM once (written by
+// dispatch, read by combine), a token row once.  The kernels walk tokens, not
+// pairs: a warp takes one piece of one token's row and all k of its pairs, so
+// the token's bytes are read (or summed) once and no atomics are needed.
+#include "rows.cuh"
+
+namespace moe {
+
+constexpr int kRowThreads = 256;
+constexpr int kMaxK = 16;
+
+// inv_perm of a token's slot (lane j of the warp), -1 for left-out pairs; an
+// entry outside [0, n_pairs) counts as left out.
+__device__ __forceinline__ int32_t pair_row(const int32_t *inv, int64_t t, int k, int64_t n_pairs, int lane)
+{
+    int32_t p = lane < k ? inv[t * k + lane] : -1;
+    return p >= 0 && p < n_pairs ? p : -1;
+}
+
+__device__ __forceinline__ int64_t first_tail_row(const int32_t *offsets, int E, int64_t n_pairs)
+{
+    int64_t n = offsets[E];
+    return n < 0 ? 0 : (n > n_pairs ? n_pairs : n);
+}
+
+// ---------------------------------------------------------------- dispatch
+// A copy, whatever the type: V is the widest unit that row bytes and pointers
+// allow.  Unit of work: kUnroll * 32 V's of one token's row, to its k places.
+template <class V, int kUnroll>
+__global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const V *__restrict__ x, int64_t x_stride, int64_t T,
+                                                               int row, int k, int E,
+                                                               const int32_t *__restrict__ offsets,
+                                                               const int32_t *__restrict__ inv, V *__restrict__ out)
+{
+    const int lane = lane_id();
+    const int pieces = (row + 32 * kUnroll - 1) / (32 * kUnroll);
+    const int64_t n_pairs = T * k, units = T * pieces;
+    const int64_t w0 = (int64_t)blockIdx.x * (kRowThreads / 32) + warp_id(), wn = (int64_t)gridDim.x * (kRowThreads / 32);
+    for (int64_t u = w0; u < units; u += wn) {
+        const int64_t t = u / pieces;
+        const int c0 = (int)(u % pieces) * 32 * kUnroll + lane;
+        const int32_t p = pair_row(inv, t, k, n_pairs, lane);
+        V v[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; i++)
+            if (c0 + 32 * i < row) v[i] = x[t * x_stride + c0 + 32 * i];
+        for (int j = 0; j < k; j++) {
+            const int32_t r = __shfl_sync(0xffffffffu, p, j);
+            if (r < 0) continue;
+#pragma unroll
+            for (int i = 0; i < kUnroll; i++)
+                if (c0 + 32 * i < row) out[(int64_t)r * row + c0 + 32 * i] = v[i];
+        }
+    }
+    // rows of no pair
+    const int64_t z0 = first_tail_row(offsets, E, n_pairs);
+    const int64_t zn = (n_pairs - z0) * pieces;
+    for (int64_t u = w0; u < zn; u += wn) {
+        const int64_t r = z0 + u / pieces;
+        const int c0 = (int)(u % pieces) * 32 * kUnroll + lane;
+#pragma unroll
+        for (int i = 0; i < kUnroll; i++)
+            if (c0 + 32 * i < row) out[r * row + c0 + 32 * i] = V{};
+    }
+}
+
+// ---------------------------------------------------------------- combine
+// out[t] = (out[t]) + sum_j w[t][j] y[inv[t][j]] in slot order, fp32 sums,
+// one rounding at the end.  Unit of work: 256 columns of one token (eight per
+// lane; scalar columns where rows are not 16-byte aligned).
+template <class A, class O, bool kVec>
+__global__ void __launch_bounds__(kRowThreads) combine_kernel(const typename A::T *__restrict__ y, int64_t T, int H,
+                                                              int k, const float *__restrict__ w,
+                                                              const int32_t *__restrict__ inv,
+                                                              typename O::T *__restrict__ out, int accumulate)
+{
+    const int lane = lane_id();
+    const int pieces = (H + 255) / 256;
+    const int64_t n_pairs = T * k, units = T * pieces;
+    const int64_t w0 = (int64_t)blockIdx.x * (kRowThreads / 32) + warp_id(), wn = (int64_t)gridDim.x * (kRowThreads / 32);
+    for (int64_t u = w0; u < units; u += wn) {
+        const int64_t t = u / pieces;
+        const int32_t p = pair_row(inv, t, k, n_pairs, lane);
+        const float f = w && lane < k ? w[t * k + lane] : 1.0f;
+        const int c0 = (int)(u % pieces) * 256;
+        float acc[8] = {};
+        typename O::T *o = out + t * H;
+        if (kVec) {
+            const int c = c0 + lane * 8;
+            if (accumulate && c < H) O::load8(o + c, acc);
+            for (int j = 0; j < k; j++) {
+                const int32_t r = __shfl_sync(0xffffffffu, p, j);
+                const float g = __shfl_sync(0xffffffffu, f, j);
+                if (r < 0 || c >= H) continue;
+                float v[8];
+                A::load8(y + (int64_t)r * H + c, v);
+#pragma unroll
+                for (int i = 0; i < 8; i++) acc[i] = fmaf(g, v[i], acc[i]);
+            }
+            if (c < H) O::store8(o + c, acc);
+        } else {
+            const int c = c0 + lane;
+            if (accumulate) {
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    if (c + 32 * i < H) acc[i] = O::load(o + c + 32 * i);
+            }
+            for (int j = 0; j < k; j++) {
+                const int32_t r = __shfl_sync(0xffffffffu, p, j);
+                const float g = __shfl_sync(0xffffffffu, f, j);
+                if (r < 0) continue;
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    if (c + 32 * i < H) acc[i] = fmaf(g, A::load(y + (int64_t)r * H + c + 32 * i), acc[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (c + 32 * i < H) O::store(o + c + 32 * i, acc[i]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- combine's gradients
+// One warp per (token, slot): dy[inv] = w dout[t] and dw = <dout[t], y[inv]>,
+// the dot product in fp32 (lane sums over strided pieces, then a fixed tree).
+template <class A, bool kVec>
+__global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(
+    const typename A::T *__restrict__ dout, const typename A::T *__restrict__ y, int64_t T, int H, int k, int E,
+    const int32_t *__restrict__ offsets, const float *__restrict__ w, const int32_t *__restrict__ inv,
+    typename A::T *__restrict__ dy, float *__restrict__ dw)
+{
+    const int lane = lane_id();
+    const int64_t n_pairs = T * k;
+    const int64_t w0 = (int64_t)blockIdx.x * (kRowThreads / 32) + warp_id(), wn = (int64_t)gridDim.x * (kRowThreads / 32);
+    for (int64_t q = w0; q < n_pairs; q += wn) {
+        const int32_t r = inv[q];
+        if (r < 0 || r >= n_pairs) {
+            if (lane == 0) dw[q] = 0.f;
+            continue;
+        }
+        const float f = w[q];
+        const typename A::T *d = dout + q / k * H, *yr = y + (int64_t)r * H;
+        typename A::T *o = dy + (int64_t)r * H;
+        float sum = 0.f;
+        if (kVec) {
+#pragma unroll 4
+            for (int c = lane * 8; c < H; c += 256) {
+                float a[8], b[8];
+                A::load8(d + c, a);
+                A::load8(yr + c, b);
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    sum = fmaf(a[i], b[i], sum);
+                    a[i] *= f;
+                }
+                A::store8(o + c, a);
+            }
+        } else {
+#pragma unroll 4
+            for (int c = lane; c < H; c += 32) {
+                const float a = A::load(d + c);
+                sum = fmaf(a, A::load(yr + c), sum);
+                A::store(o + c, a * f);
+            }
+        }
+#pragma unroll
+        for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        if (lane == 0) dw[q] = sum;
+    }
+    const int64_t z0 = first_tail_row(offsets, E, n_pairs);
+    for (int64_t r = z0 + w0; r < n_pairs; r += wn) {
+        for (int c = lane; c < H; c += 32) A::store(dy + r * H + c, 0.f);
+    }
+}
+
+static unsigned row_grid(int64_t warps)
+{
+    const int64_t blocks = (warps + kRowThreads / 32 - 1) / (kRowThreads / 32);
+    return (unsigned)std::max<int64_t>(1, std::min<int64_t>(blocks, (int64_t)sm_count() * 8));
+}
+
+// 16-byte accesses of eight (or four) elements need aligned rows.
+static bool vec_rows(moe_dtype t, int H, const void *p) { return aligned16(p) && H % 8 == 0 && dtype_ok(t); }
+
+static moe_status check_rows(int T, int H, int k, moe_dtype dtype)
+{
+    MOE_REQUIRE(T >= 0 && H >= 1 && k >= 1 && k <= kMaxK, "T >= 0, H >= 1 and 1 <= k <= %d (got T=%d H=%d k=%d)", kMaxK,
+                T, H, k);
+    MOE_REQUIRE((int64_t)T * k <= INT32_MAX, "T*k too large (T=%d k=%d)", T, k);
+    MOE_REQUIRE(dtype_ok(dtype), "dtype must be MOE_F32, MOE_BF16 or MOE_F16 (got %d)", (int)dtype);
+    return MOE_OK;
+}
+
+template <class V>
+static void launch_dispatch(const void *x, int64_t stride_bytes, int T, int64_t row_bytes, int k, int E,
+                            const int32_t *offsets, const int32_t *inv, void *out, cudaStream_t s)
+{
+    const int row = (int)(row_bytes / (int64_t)sizeof(V));
+    const int64_t units = (int64_t)T * ((row + 127) / 128);
+    dispatch_kernel<V, 4><<<row_grid(units), kRowThreads, 0, s>>>(static_cast<const V *>(x),
+                                                                  stride_bytes / (int64_t)sizeof(V), T, row, k, E,
+                                                                  offsets, inv, static_cast<V *>(out));
+}
+
+static moe_status combine_any(const void *y, moe_dtype dtype, int T, int H, int k, const float *w,
+                              const int32_t *inv, void *out, moe_dtype out_dtype, int accumulate, cudaStream_t s,
+                              const char *what)
+{
+    const unsigned grid = row_grid((int64_t)T * ((H + 255) / 256));
+    const bool vec = vec_rows(dtype, H, y) && vec_rows(out_dtype, H, out);
+    return with_dtype(dtype, [&](auto a) {
+        using A = decltype(a);
+        auto go = [&](auto o) {
+            using O = decltype(o);
+            auto *yp = static_cast<const typename A::T *>(y);
+            auto *op = static_cast<typename O::T *>(out);
+            if (vec)
+                combine_kernel<A, O, true><<<grid, kRowThreads, 0, s>>>(yp, T, H, k, w, inv, op, accumulate);
+            else
+                combine_kernel<A, O, false><<<grid, kRowThreads, 0, s>>>(yp, T, H, k, w, inv, op, accumulate);
+            return check_launch(what);
+        };
+        return out_dtype == dtype ? go(a) : go(F32{});
+    });
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_dispatch(const void *x, moe_dtype dtype, int64_t x_stride, int T, int H, int k, int E,
+                                   const int32_t *offsets, const int32_t *inv_perm, void *out, moe_stream_t stream)
+{
+    moe_status st = check_rows(T, H, k, dtype);
+    if (st != MOE_OK) return st;
+    MOE_REQUIRE(E >= 1 && E <= 1024, "E must be in [1, 1024] (got %d)", E);
+    MOE_REQUIRE(x_stride == 0 || x_stride >= H, "x_stride must be 0 (one row for every token) or >= H (got %lld, H=%d)",
+                (long long)x_stride, H);
+    if (T == 0) return MOE_OK;
+    MOE_REQUIRE(x && offsets && inv_perm && out, "NULL pointer");
+    const int b = dtype_bytes(dtype);
+    const int64_t rb = (int64_t)H * b, sb = x_stride * b;
+    MOE_REQUIRE(aligned_to(x, b) && aligned_to(out, b), "x and out must be aligned to their type");
+    cudaStream_t s = to_cuda(stream);
+    if (rb % 16 == 0 && sb % 16 == 0 && aligned16(x) && aligned16(out))
+        launch_dispatch<uint4>(x, sb, T, rb, k, E, offsets, inv_perm, out, s);
+    else if (rb % 4 == 0 && sb % 4 == 0 && aligned_to(x, 4) && aligned_to(out, 4))
+        launch_dispatch<uint32_t>(x, sb, T, rb, k, E, offsets, inv_perm, out, s);
+    else
+        launch_dispatch<uint16_t>(x, sb, T, rb, k, E, offsets, inv_perm, out, s);
+    return check_launch("dispatch");
+}
+
+extern "C" moe_status moe_dispatch_backward(const void *drows, moe_dtype dtype, int T, int H, int k,
+                                            const int32_t *inv_perm, void *dx, moe_stream_t stream)
+{
+    moe_status st = check_rows(T, H, k, dtype);
+    if (st != MOE_OK) return st;
+    if (T == 0) return MOE_OK;
+    MOE_REQUIRE(drows && inv_perm && dx, "NULL pointer");
+    MOE_REQUIRE(aligned_to(drows, dtype_bytes(dtype)) && aligned_to(dx, dtype_bytes(dtype)),
+                "drows and dx must be aligned to their type");
+    return combine_any(drows, dtype, T, H, k, nullptr, inv_perm, dx, dtype, 0, to_cuda(stream), "dispatch_backward");
+}
+
+extern "C" moe_status moe_combine(const void *y, moe_dtype dtype, int T, int H, int k, const float *w,
+                                  const int32_t *inv_perm, void *out, moe_dtype out_dtype, int accumulate,
+                                  moe_stream_t stream)
+{
+    moe_status st = check_rows(T, H, k, dtype);
+    if (st != MOE_OK) return st;
+    MOE_REQUIRE(out_dtype == dtype || out_dtype == MOE_F32, "out_dtype must be MOE_F32 or the rows' type (got %d, %d)",
+                (int)out_dtype, (int)dtype);
+    if (T == 0) return MOE_OK;
+    MOE_REQUIRE(y && w && inv_perm && out, "NULL pointer");
+    MOE_REQUIRE(aligned_to(y, dtype_bytes(dtype)) && aligned_to(out, dtype_bytes(out_dtype)),
+                "y and out must be aligned to their type");
+    return combine_any(y, dtype, T, H, k, w, inv_perm, out, out_dtype, accumulate, to_cuda(stream), "combine");
+}
+
+extern "C" moe_status moe_combine_backward(const void *dout, const void *y, moe_dtype dtype, int T, int H, int k, int E,
+                                           const int32_t *offsets, const float *w, const int32_t *inv_perm, void *dy,
+                                           float *dw, moe_stream_t stream)
+{
+    moe_status st = check_rows(T, H, k, dtype);
+    if (st != MOE_OK) return st;
+    MOE_REQUIRE(E >= 1 && E <= 1024, "E must be in [1, 1024] (got %d)", E);
+    if (T == 0) return MOE_OK;
+    MOE_REQUIRE(dout && y && offsets && w && inv_perm && dy && dw, "NULL pointer");
+    MOE_REQUIRE(aligned_to(dout, dtype_bytes(dtype)) && aligned_to(y, dtype_bytes(dtype)) &&
+                    aligned_to(dy, dtype_bytes(dtype)),
+                "dout, y and dy must be aligned to their type");
+    const unsigned grid = row_grid((int64_t)T * k);
+    const bool vec = vec_rows(dtype, H, dout) && vec_rows(dtype, H, y) && vec_rows(dtype, H, dy);
+    return with_dtype(dtype, [&](auto a) {
+        using A = decltype(a);
+        using E1 = typename A::T;
+        auto fn = vec ? combine_backward_kernel<A, true> : combine_backward_kernel<A, false>;
+        fn<<<grid, kRowThreads, 0, to_cuda(stream)>>>(static_cast<const E1 *>(dout), static_cast<const E1 *>(y), T, H, k,
+                                                      E, offsets, w, inv_perm, static_cast<E1 *>(dy), dw);
+        return check_launch("combine_backward");
+    });
+}

@@ -1,0 +1,91 @@
+// rows.cuh -- element types of activation rows: fp32, bf16 and fp16 values to
+// and from fp32 registers, one at a time or eight (16 or 32 bytes) at once.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+struct F32 {
+    using T = float;
+    static constexpr int kBytes = 4;
+    __device__ static float load(const T *p) { return *p; }
+    __device__ static void store(T *p, float v) { *p = v; }
+    __device__ static void load8(const T *p, float (&v)[8])
+    {
+        const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+    __device__ static void store8(T *p, const float (&v)[8])
+    {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+};
+
+struct Bf16 {
+    using T = uint16_t;
+    static constexpr int kBytes = 2;
+    __device__ static float load(const T *p) { return bf16_to_f32(*p); }
+    __device__ static void store(T *p, float v) { *p = f32_to_bf16(v); }
+    __device__ static void unpack8(uint4 q, float (&v)[8])
+    {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    __device__ static uint4 pack8(const float (&v)[8])
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++)  // one rounding, to nearest even
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ static void load8(const T *p, float (&v)[8]) { unpack8(*reinterpret_cast<const uint4 *>(p), v); }
+    __device__ static void store8(T *p, const float (&v)[8]) { *reinterpret_cast<uint4 *>(p) = pack8(v); }
+};
+
+struct Fp16 {
+    using T = uint16_t;
+    static constexpr int kBytes = 2;
+    __device__ static float load(const T *p) { return fp16_to_f32(*p); }
+    __device__ static void store(T *p, float v) { *p = __half_as_ushort(__float2half_rn(v)); }
+    __device__ static void unpack8(uint4 q, float (&v)[8])
+    {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            v[2 * i] = fp16_to_f32((uint16_t)(w[i] & 0xffffu));
+            v[2 * i + 1] = fp16_to_f32((uint16_t)(w[i] >> 16));
+        }
+    }
+    __device__ static uint4 pack8(const float (&v)[8])
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ static void load8(const T *p, float (&v)[8]) { unpack8(*reinterpret_cast<const uint4 *>(p), v); }
+    __device__ static void store8(T *p, const float (&v)[8]) { *reinterpret_cast<uint4 *>(p) = pack8(v); }
+};
+
+inline bool dtype_ok(moe_dtype t) { return t == MOE_F32 || t == MOE_BF16 || t == MOE_F16; }
+inline int dtype_bytes(moe_dtype t) { return t == MOE_F32 ? 4 : 2; }
+inline bool aligned_to(const void *p, int n) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(n - 1)) == 0; }
+
+// Calls F<A>() with the element type of `t`.
+template <class F>
+moe_status with_dtype(moe_dtype t, F f)
+{
+    if (t == MOE_F32) return f(F32{});
+    if (t == MOE_BF16) return f(Bf16{});
+    return f(Fp16{});
+}
+
+}  // namespace moe

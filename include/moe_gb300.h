@@ -81,7 +81,11 @@ typedef enum moe_status {
                                 moe_expert_forward, moe_decode_forward) */
 } moe_status;
 
-typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
+typedef enum moe_dtype {
+    MOE_F32 = 0,
+    MOE_BF16 = 1,
+    MOE_F16 = 2 /* the row, 4-bit and norm calls only */
+} moe_dtype;
 
 typedef enum moe_path {
     MOE_PATH_AUTO = 0,        /* DECODE for T <= 8, PREFILL otherwise (never FP8) */
@@ -486,6 +490,141 @@ moe_status moe_f32_to_bf16(const float *in_f32, uint16_t *out_bf16, int64_t n, m
  * of every layer.
  */
 moe_status moe_rms_norm_bf16(const float *x, uint16_t *out, int T, int H, float eps, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Rows to their experts and back                                           */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * The movement of activation rows around a layer's experts, for experts that
+ * are not this library's 2-/3-bit ones (moe_expert_forward does it inside),
+ * and its gradients.  offsets and inv_perm are moe_permute's: pair (t, j) is
+ * row inv_perm[t*k + j] of the T*k sorted rows, or none (-1, a left-out pair).
+ * An inv_perm entry outside [0, T*k) counts as left out.  Rows are fp32, bf16
+ * or fp16; sums and dot products are fp32 and rounded once; nothing is added
+ * with atomics, so the same call gives the same bits.  1 <= k <= 16, any
+ * H >= 1 (rows of 16-byte multiples move fastest).  T = 0 is a no-op.
+ *
+ * moe_dispatch: out[inv_perm[t*k + j]] = x[t]; rows at and past offsets[E] are
+ * set to zero.  Row t of x starts at x + t * x_stride elements (x_stride >= H,
+ * or 0: the same row for every token).
+ * moe_dispatch_backward: dx[t] = sum_j drows[inv_perm[t*k + j]], in slot order.
+ */
+moe_status moe_dispatch(const void *x, moe_dtype dtype, int64_t x_stride, int T, int H, int k, int E,
+                        const int32_t *offsets, const int32_t *inv_perm, void *out, moe_stream_t stream);
+moe_status moe_dispatch_backward(const void *drows, moe_dtype dtype, int T, int H, int k,
+                                 const int32_t *inv_perm, void *dx, moe_stream_t stream);
+
+/*
+ * out[t] = (accumulate ? out[t] : 0) + sum_j w[t][j] * y[inv_perm[t*k + j]],
+ * in slot order; a token all of whose pairs are left out gets 0 (or keeps its
+ * value).  out_dtype: the rows' type or MOE_F32.
+ * moe_combine_backward: dy[inv_perm[t*k + j]] = w[t][j] * dout[t] and
+ * dw[t][j] = <dout[t], y[inv_perm[t*k + j]]> (fp32; 0 for a left-out pair);
+ * rows of dy at and past offsets[E] are set to zero.  The gradient of an
+ * accumulated out is dout itself.
+ */
+moe_status moe_combine(const void *y, moe_dtype dtype, int T, int H, int k, const float *w,
+                       const int32_t *inv_perm, void *out, moe_dtype out_dtype, int accumulate,
+                       moe_stream_t stream);
+moe_status moe_combine_backward(const void *dout, const void *y, moe_dtype dtype, int T, int H, int k, int E,
+                                const int32_t *offsets, const float *w, const int32_t *inv_perm, void *dy,
+                                float *dw, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* 4-bit floating point matrices (MXFP4)                                    */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * A matrix [rows][cols], cols a multiple of 32, in the OCP microscaling format
+ * MXFP4 (Open Compute Project, "Microscaling Formats (MX) Specification" 1.0):
+ *   codes:  [rows][cols/2] bytes, value i of a row in the low (i even) or high
+ *           (i odd) half of byte i/2: an e2m1 number, sign at bit 3, magnitude
+ *           0, 0.5, 1, 1.5, 2, 3, 4 or 6 for codes 0..7;
+ *   scales: [rows][8 * ceil(cols/256)] bytes, byte b of a row the exponent
+ *           (e8m0, 2^(byte - 127), 255 = NaN) of values 32b .. 32b+31; bytes
+ *           past cols/32 are 0.
+ * Both are 16-byte aligned.
+ *
+ * moe_mx4_quantise: per block of 32, with m its largest magnitude,
+ * e = max(floor(log2 m) - 2, -127) and code = e2m1(x 2^-e), to nearest, ties
+ * to even, magnitudes above 6 to 6 (the specification's conversion; m = 0
+ * gives byte 0).  A block that holds an infinity or a NaN gets the scale NaN
+ * and zero codes, and sets *dev_status = MOE_ERR_NONFINITE.  Row r starts at
+ * x + r * x_stride elements (x_stride >= cols, or 0).
+ * moe_mx4_dequantise: out = code * 2^(byte - 127), exact in fp32 and bf16, one
+ * rounding to fp16; NaN for a block of scale NaN.
+ */
+moe_status moe_mx4_size(int64_t rows, int64_t cols, size_t *code_bytes, size_t *scale_bytes);
+moe_status moe_mx4_quantise(const void *x, moe_dtype dtype, int64_t x_stride, int64_t rows, int64_t cols,
+                            uint8_t *codes, uint8_t *scales, int32_t *dev_status, moe_stream_t stream);
+moe_status moe_mx4_dequantise(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols,
+                              void *out, moe_dtype dtype, moe_stream_t stream);
+
+typedef enum moe_mx4_epilogue {
+    MOE_MX4_PLAIN = 0, /* out = x W^T, W [E][N][K]                               */
+    MOE_MX4_SWIGLU = 1 /* out = silu(x Wg^T) * (x Wu^T), W [E][2N][K]: rows 0..N-1
+                          of an expert gate, N..2N-1 up                         */
+} moe_mx4_epilogue;
+
+/*
+ * Products of quantised rows with their expert's quantised weights, on the
+ * tensor cores (products exact, fp32 sums, one rounding to out_dtype):
+ *   out[p][n] = sum_k x[p][k] W_e[n][k],  e the group with offsets[e] <= p <
+ *   offsets[e+1]
+ * x is a [rows][K] and W one [E * N (or 2N)][K] matrix of the format above;
+ * offsets [E+1] as moe_permute gives them, or NULL when E = 1 (all rows).  Rows
+ * at and past offsets[E] are set to zero.  out [rows][N], any N >= 1.  Offsets
+ * that decrease or leave [0, rows] set *dev_status = MOE_ERR_BOUNDS and are
+ * clipped; a wait that runs out (about 2 s) sets MOE_ERR_TIMEOUT.  E <= 1024.
+ */
+moe_status moe_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_scales, int E, int N, int K,
+                          const uint8_t *x_codes, const uint8_t *x_scales, int rows, const int32_t *offsets,
+                          void *out, moe_dtype out_dtype, moe_mx4_epilogue epilogue, int32_t *dev_status,
+                          moe_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Norms around a block                                                     */
+/* ------------------------------------------------------------------------ */
+
+typedef enum moe_gate {
+    MOE_GATE_NONE = 0,
+    MOE_GATE_TOKEN = 1,  /* gate [T]: one factor per token    */
+    MOE_GATE_CHANNEL = 2 /* gate [H]: one factor per channel  */
+} moe_gate;
+
+/*
+ * The end of one block and the start of the next, in one pass: with b the
+ * block's output and x the residual stream,
+ *   v = w_post * b / sqrt(mean(b^2) + eps)
+ *   y = x + alpha * gate * v
+ *   u = w_pre * y / sqrt(mean(y^2) + eps)
+ * The residual stream (x, y) is fp32 or of the type of b and u (fp32, bf16,
+ * fp16); w_post, w_pre (NULL: ones) and gate are fp32.  All arithmetic is
+ * fp32; u comes from y before its rounding.  y may be x and u may be b (packed
+ * rows).  Rows of x and b start every x_stride and b_stride elements (>= H, or
+ * 0: the same row for every token).  1 <= H <= 16384; T = 0 is a no-op.
+ */
+moe_status moe_block_norm(const void *x, moe_dtype res_dtype, int64_t x_stride, const void *b,
+                          moe_dtype dtype, int64_t b_stride, int T, int H, const float *w_post,
+                          const float *w_pre, const float *gate, moe_gate gate_kind, float alpha, float eps,
+                          void *y, void *u, moe_stream_t stream);
+
+/*
+ * Gradients of moe_block_norm for dy and du, the gradients of y and u (NULL:
+ * zero): dx [T][H] (residual type), db [T][H] (the block's type), and the fp32
+ * sums dw_post [H], dw_pre [H] and dgate ([T] or [H] like gate), each of which
+ * may be NULL.  dx may be dy and db may be du.  The statistics are recomputed
+ * from x and b.  With T = 0 the sums over tokens are set to zero.  Sums over
+ * tokens are taken in a fixed order.
+ */
+moe_status moe_block_norm_backward_workspace_size(int T, int H, moe_gate gate_kind, size_t *bytes);
+moe_status moe_block_norm_backward(const void *x, moe_dtype res_dtype, int64_t x_stride, const void *b,
+                                   moe_dtype dtype, int64_t b_stride, int T, int H, const float *w_post,
+                                   const float *w_pre, const float *gate, moe_gate gate_kind, float alpha,
+                                   float eps, const void *dy, const void *du, void *dx, void *db,
+                                   float *dw_post, float *dw_pre, float *dgate, void *ws, size_t ws_bytes,
+                                   moe_stream_t stream);
 
 #ifdef __cplusplus
 }
