@@ -33,6 +33,8 @@
 #include "rows.cuh"
 #include "tc.cuh"
 
+#include <type_traits>
+
 namespace moe {
 namespace mx {
 
@@ -46,6 +48,7 @@ constexpr int SF_COL = 2 * MAX_BN;           // tensor memory columns of the sca
 constexpr int THREADS = 256;
 constexpr int EPI_WARP0 = 4;
 constexpr int MAX_E = 1024;
+constexpr int STAGE_PITCH = 80;  // 32 16-bit columns and 16 bytes, so that eight rows fall into different banks
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
 struct Params {
@@ -56,18 +59,21 @@ struct Params {
     const uint8_t *w_scales, *x_scales;
     int pitch;                   // bytes of scales per row
     void *out;
-    int out_type;
+    int vec;  // rows of out are 16-byte pieces
     int32_t *status;
 };
 
 struct Shared {
     uint64_t full[MAX_STAGES], empty[MAX_STAGES];
     uint64_t acc_full[2], acc_empty[2];
+    uint64_t turn[2];  // the scale warps' hand-over
     uint64_t mma_done;
     uint32_t tmem;
     volatile int abort;
     int warp_tot[THREADS / 32];
     int tile0[MAX_E + 1];  // row tiles before expert e
+    int start[MAX_E], count[MAX_E];
+    alignas(16) char stage[4][32 * STAGE_PITCH];  // epilogue warps: 32 rows on their way out
 };
 
 struct Item {
@@ -89,27 +95,30 @@ __device__ __forceinline__ void group_of(const Params &p, int e, int &p0, int &c
     cnt = max(0, b - a);
 }
 
+// The whole warp finds the last expert with tile0 <= tt: 32 ranges, then one.
 __device__ __forceinline__ Item item_of(const Params &p, const Shared &S, int item, int split)
 {
     Item it;
-    const int tt = item / p.n_tiles;
-    it.n0 = (item % p.n_tiles) * (p.swiglu ? BM / 2 : BM);
-    int lo = 0, hi = p.E - 1;  // the last expert with tile0 <= tt
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (S.tile0[mid] <= tt) lo = mid;
-        else hi = mid - 1;
-    }
-    it.e = lo;
-    int p0, cnt;
-    group_of(p, lo, p0, cnt);
-    const int nt = S.tile0[lo + 1] - S.tile0[lo], j = tt - S.tile0[lo];
-    const int w = ((cnt + nt - 1) / nt + 15) & ~15;
-    it.p0 = p0 + j * w;
+    const int lane = lane_id(), tt = item / p.n_tiles;
+    it.n0 = (item - tt * p.n_tiles) * (p.swiglu ? BM / 2 : BM);
+    int e = __popc(__ballot_sync(0xffffffffu, lane * 32 < p.E && S.tile0[min(lane * 32, p.E)] <= tt)) - 1;
+    e *= 32;
+    e += __popc(__ballot_sync(0xffffffffu, e + lane < p.E && S.tile0[min(e + lane, p.E)] <= tt)) - 1;
+    it.e = e;
+    const int cnt = S.count[e], j = tt - S.tile0[e], nt = S.tile0[e + 1] - S.tile0[e];
+    const int w = nt == 1 ? cnt : ((cnt + nt - 1) / nt + 15) & ~15;
+    it.p0 = S.start[e] + j * w;
     it.cnt = min(w, cnt - j * w);
     it.kb0 = p.nk * split / p.splits;
     it.kb1 = p.nk * (split + 1) / p.splits;
     return it;
+}
+
+// A whole warp waits; false for all of it when the time is up or the CTA stops.
+__device__ __forceinline__ bool warp_wait(Shared &S, uint64_t *bar, uint32_t parity)
+{
+    const bool ok = tc::mbar_wait(bar, parity, kWaitNs);
+    return __all_sync(0xffffffffu, ok && !S.abort);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -172,36 +181,121 @@ __device__ __forceinline__ uint32_t idesc_mxf4(int n, uint32_t id)
            (id << 29);
 }
 
-__device__ __forceinline__ void store_out(const Params &p, int64_t i, float v)
+__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+// 16 lanes x 32 columns: thread t gets lanes t/4 and t/4 + 8, of each group j of
+// eight columns 2 (t%4) and the next: r[4j], r[4j+1] and r[4j+2], r[4j+3].
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, float (&r)[16])
 {
-    if (p.out_type == MOE_F32) static_cast<float *>(p.out)[i] = v;
-    else if (p.out_type == MOE_BF16) Bf16::store(static_cast<uint16_t *>(p.out) + i, v);
-    else Fp16::store(static_cast<uint16_t *>(p.out) + i, v);
+    uint32_t u[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 16; i++) r[i] = __uint_as_float(u[i]);
 }
 
-// Lane `lane` of quadrant q holds columns c .. c+31 of a tile's sums.
-__device__ __forceinline__ void write_columns(const Params &p, const Item &it, int q, int lane, int c, const float (&v)[32])
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
-    if (!p.swiglu) {
-        const int n = it.n0 + q * 32 + lane;
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
+
+template <class O>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    uint32_t w;
+    if (std::is_same<O, Bf16>::value) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    return w;
+}
+
+// Rows c .. c+31 of a tile, whose sums lie in columns of tensor memory from
+// `taddr` on, a weight row per lane: this warp's 32 (SwiGLU: 16) output
+// columns.  16-bit outputs are transposed in shared memory (stmatrix) and leave
+// in pieces of 16 bytes; fp32 ones leave from the registers.
+template <class O, bool kSwiglu>
+__device__ __forceinline__ void write_rows(const Params &p, const Item &m, int q, int lane, uint32_t taddr, int c, char *stage)
+{
+    constexpr int W = kSwiglu ? 16 : 32;  // output columns of the warp
+    using T = typename O::T;
+    const int n0 = m.n0 + q * W, rows = m.cnt - c;
+    T *out = static_cast<T *>(p.out) + (int64_t)(m.p0 + c) * p.N;
+    __syncwarp();
+    if (!kSwiglu && O::kBytes == 4) {
+        uint32_t r[32];
+        tc::tmem_ld_32x32b_x32(taddr, r);
+        tc::tmem_ld_wait();
+        const int in = n0 + lane < p.N ? rows : 0;
+        T *o = out + n0 + lane;
 #pragma unroll
-        for (int i = 0; i < 32; i++)
-            if (n < p.N && c + i < it.cnt) store_out(p, (int64_t)(it.p0 + c + i) * p.N + n, v[i]);
+        for (int i = 0; i < 32; i++, o += p.N)
+            if (i < in) O::store(o, __uint_as_float(r[i]));
         return;
     }
-    // lanes 0..15: gate, 16..31: the same columns' up.  Each pair of lanes
-    // swaps one value, and then has both of one row.
-    const bool up = lane >= 16;
-    const int n = it.n0 + q * 16 + (lane & 15);
+    float a[16], b[16];
+    tmem_ld_16x256b_x4(taddr, a);
+    tmem_ld_16x256b_x4(taddr + (16u << 16), b);
+    tc::tmem_ld_wait();
+    if (kSwiglu) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-        const float got = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 1], 16);
-        const float g = up ? got : v[i], u = up ? v[i + 1] : got;
-        const int r = c + i + (up ? 1 : 0);
-        if (n < p.N && r < it.cnt) store_out(p, (int64_t)(it.p0 + r) * p.N + n, g / (1.0f + expf(-g)) * u);
+        for (int i = 0; i < 16; i++) a[i] = swiglu(a[i], b[i]);
+    }
+    if (O::kBytes == 4) {
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+            const int row = (i >> 2) * 8 + 2 * (lane & 3) + (i & 1), n = n0 + lane / 4 + (i & 2) * 4;
+            if (row < rows && n < p.N) O::store(out + (int64_t)row * p.N + n, a[i]);
+        }
+        return;
+    }
+    constexpr int P = kSwiglu ? 48 : STAGE_PITCH;
+    const uint32_t base = tc::smem_u32(stage) + ((lane >> 4) * 8 + (lane & 7)) * P + ((lane >> 3) & 1) * 16;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+        stmatrix_x4_trans(base + j * 8 * P, pack2<O>(a[4 * j], a[4 * j + 1]), pack2<O>(a[4 * j + 2], a[4 * j + 3]),
+                          pack2<O>(a[4 * j + 4], a[4 * j + 5]), pack2<O>(a[4 * j + 6], a[4 * j + 7]));
+        if (!kSwiglu)
+            stmatrix_x4_trans(base + j * 8 * P + 32, pack2<O>(b[4 * j], b[4 * j + 1]), pack2<O>(b[4 * j + 2], b[4 * j + 3]),
+                              pack2<O>(b[4 * j + 4], b[4 * j + 5]), pack2<O>(b[4 * j + 6], b[4 * j + 7]));
+    }
+    __syncwarp();
+    if (p.vec && n0 + W <= p.N) {
+        constexpr int L = W / 8;  // lanes per row
+        const int row0 = lane / L, part = lane % L;
+        T *o = out + (int64_t)row0 * p.N + n0 + part * 8;
+#pragma unroll
+        for (int i = 0; i < L; i++, o += (int64_t)(32 / L) * p.N) {
+            const int row = row0 + i * (32 / L);
+            if (row < rows) *reinterpret_cast<uint4 *>(o) = *reinterpret_cast<const uint4 *>(stage + row * P + part * 16);
+        }
+    } else if (lane < W && n0 + lane < p.N) {
+        T *o = out + n0 + lane;
+        for (int i = 0; i < min(rows, 32); i++, o += p.N) *o = *reinterpret_cast<const T *>(stage + i * P + lane * 2);
     }
 }
 
+// One row's sums of this warp's lanes (the parts of a cluster, added up).
+template <class O, bool kSwiglu>
+__device__ __forceinline__ void write_row(const Params &p, const Item &m, int q, int lane, int row, float v)
+{
+    typename O::T *out = static_cast<typename O::T *>(p.out) + (int64_t)(m.p0 + row) * p.N;
+    if (!kSwiglu) {
+        const int n = m.n0 + q * 32 + lane;
+        if (n < p.N) O::store(out + n, v);
+        return;
+    }
+    const float u = __shfl_down_sync(0xffffffffu, v, 16);  // lanes 0..15: gate, 16..31: the same columns' up
+    const int n = m.n0 + q * 16 + lane;
+    if (lane < 16 && n < p.N) O::store(out + n, swiglu(v, u));
+}
+
+template <class O, bool kSwiglu>
 __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_constant__ Params p,
                                                                 const __grid_constant__ CUtensorMap mw,
                                                                 const __grid_constant__ CUtensorMap mx)
@@ -221,13 +315,17 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
 #pragma unroll
         for (int i = 0; i < MAX_E / THREADS; i++) {
             const int e = threadIdx.x * (MAX_E / THREADS) + i;
-            int p0, cnt = 0;
+            int p0 = 0, cnt = 0;
             if (e < p.E) {
                 group_of(p, e, p0, cnt);
                 if (p.offsets && blockIdx.x == 0) {
                     const int a = p.offsets[e], b = p.offsets[e + 1];
                     if (a < 0 || b < a || b > p.rows) set_status(p.status, MOE_ERR_BOUNDS);
                 }
+            }
+            if (e < p.E) {
+                S.start[e] = p0;
+                S.count[e] = cnt;
             }
             n[i] = sum;
             sum += (cnt + p.bn - 1) / p.bn;
@@ -258,6 +356,8 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
             tc::mbar_init(&S.acc_full[i], 1);
             tc::mbar_init(&S.acc_empty[i], 4);
         }
+        tc::mbar_init(&S.turn[0], 1);
+        tc::mbar_init(&S.turn[1], 1);
         tc::mbar_init(&S.mma_done, 1);
         S.abort = 0;
         tc::fence_mbar_init();
@@ -273,23 +373,22 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
     const int total = p.splits > 1 ? min(S.tile0[p.E] * p.n_tiles, step) : S.tile0[p.E] * p.n_tiles;
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ---------------- codes
-            int it = 0;
-            for (int item = first; item < total && !S.abort; item += step) {
-                const Item m = item_of(p, S, item, split);
-                const int boxes = (m.cnt + 31) / 32;
-                for (int kb = m.kb0; kb < m.kb1; kb++, it++) {
-                    const int s = it % p.stages, u = it / p.stages;
-                    if (u > 0 && !tc::mbar_wait(&S.empty[s], (u - 1) & 1, kWaitNs)) {
-                        set_status(p.status, MOE_ERR_TIMEOUT);
-                        S.abort = 1;
-                        break;
-                    }
+        // ---------------- codes
+        int it = 0;
+        bool ok = true;
+        for (int item = first; item < total && ok; item += step) {
+            const Item m = item_of(p, S, item, split);
+            const int boxes = (m.cnt + 31) / 32;
+            for (int kb = m.kb0; kb < m.kb1; kb++, it++) {
+                const int s = it % p.stages, u = it / p.stages;
+                if (u > 0) ok = warp_wait(S, &S.empty[s], (u - 1) & 1);
+                if (!ok) break;
+                if (lane == 0) {
                     tc::mbar_arrive_expect_tx(&S.full[s], A_BYTES + boxes * 32 * (BK / 2));
                     char *a = sA + s * A_BYTES, *b = sB + s * b_bytes;
                     const int x = kb * (BK / 2);
-                    if (p.swiglu) {
+                    if (kSwiglu) {
+#pragma unroll
                         for (int i = 0; i < 8; i++)
                             tma_load_3d(a + i * 16 * (BK / 2), &mw, x, (i & 1) * p.N + m.n0 + (i >> 1) * 16, m.e, &S.full[s]);
                     } else {
@@ -299,6 +398,12 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
                         tc::tma_load_2d(b + i * 32 * (BK / 2), &mx, x, m.p0 + i * 32, &S.full[s]);
                 }
             }
+        }
+        if (lane == 0) {
+            if (!ok) {
+                set_status(p.status, MOE_ERR_TIMEOUT);
+                S.abort = 1;
+            }
             // no copy may still be in flight when the CTA leaves (a full
             // barrier that never got its scales' arrival runs out of time)
             for (int s = 0; s < p.stages && s < it; s++) {
@@ -307,28 +412,24 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ---------------- MMA
-            int it = 0, j = 0;
-            bool stop = false;
-            for (int item = first; item < total && !stop; item += step, j++) {
-                const Item m = item_of(p, S, item, split);
-                const int acc = j & 1, v = j >> 1;
-                if (S.abort || (v > 0 && !tc::mbar_wait(&S.acc_empty[acc], (v - 1) & 1, kWaitNs))) {
-                    stop = true;
-                    break;
-                }
+        // ---------------- MMA
+        int it = 0, j = 0;
+        bool ok = true;
+        for (int item = first; item < total && ok; item += step, j++) {
+            const Item m = item_of(p, S, item, split);
+            const int acc = j & 1, v = j >> 1;
+            if (v > 0) ok = warp_wait(S, &S.acc_empty[acc], (v - 1) & 1);
+            if (!ok) break;
+            tc::tc_fence_after();
+            const int n16 = (m.cnt + 15) & ~15;
+            const uint32_t d = tmem + (uint32_t)(acc * MAX_BN);
+            const uint32_t id0 = idesc_mxf4(n16, 0), id2 = idesc_mxf4(n16, 2);
+            for (int kb = m.kb0; kb < m.kb1; kb++, it++) {
+                const int s = it % p.stages, u = it / p.stages;
+                ok = warp_wait(S, &S.full[s], u & 1);
+                if (!ok) break;
                 tc::tc_fence_after();
-                const int n16 = (m.cnt + 15) & ~15;
-                const uint32_t d = tmem + (uint32_t)(acc * MAX_BN);
-                const uint32_t id0 = idesc_mxf4(n16, 0), id2 = idesc_mxf4(n16, 2);
-                for (int kb = m.kb0; kb < m.kb1; kb++, it++) {
-                    const int s = it % p.stages, u = it / p.stages;
-                    if (!tc::mbar_wait(&S.full[s], u & 1, kWaitNs)) {
-                        stop = true;
-                        break;
-                    }
-                    tc::tc_fence_after();
+                if (lane == 0) {
                     const uint32_t sfa = tmem + SF_COL + (it & 1) * 32, sfb = sfa + 8;
                     const uint32_t f = tc::smem_u32(sF + s * SF_BYTES);
 #pragma unroll
@@ -339,15 +440,19 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
                     }
                     const uint64_t da = tc::desc_kmajor_sw128(tc::smem_u32(sA + s * A_BYTES));
                     const uint64_t db = tc::desc_kmajor_sw128(tc::smem_u32(sB + s * b_bytes));
-                    const int nm = min(4, p.n_mma - kb * 4);
-                    for (int i = 0; i < nm; i++)  // 32 bytes of the swizzled rows per MMA
-                        mma_mxf4(d, da + i * 2, db + i * 2, (i & 1) ? id2 : id0, sfa + (i >> 1) * 4, sfb + (i >> 1) * 8,
-                                 (kb > m.kb0 || i > 0) ? 1u : 0u);
+                    const int nm = p.n_mma - kb * 4;
+#pragma unroll
+                    for (int i = 0; i < 4; i++)  // 32 bytes of the swizzled rows per MMA
+                        if (i < nm)
+                            mma_mxf4(d, da + i * 2, db + i * 2, (i & 1) ? id2 : id0, sfa + (i >> 1) * 4, sfb + (i >> 1) * 8,
+                                     (kb > m.kb0 || i > 0) ? 1u : 0u);
                     tc::mma_commit(&S.empty[s]);
+                    if (kb + 1 == m.kb1) tc::mma_commit(&S.acc_full[acc]);
                 }
-                if (!stop) tc::mma_commit(&S.acc_full[acc]);
             }
-            if (stop) {
+        }
+        if (lane == 0) {
+            if (!ok) {
                 set_status(p.status, MOE_ERR_TIMEOUT);
                 S.abort = 1;
             }
@@ -355,22 +460,25 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
             if (!tc::mbar_wait(&S.mma_done, 0, kWaitNs)) set_status(p.status, MOE_ERR_TIMEOUT);
         }
     } else if (warp == 2 || warp == 3) {
-        // ---------------- scales: four steps at a time, the two warps in turn
-        int it = 0, turn = 0;
+        // ---------------- scales: four steps at a time, the two warps in turn.
+        // Both load ahead, but a warp stores its steps only after the other has
+        // stored the ones before: a wait for a stage's parity may be at most one
+        // phase ahead, and steps stored out of order would be two.
+        int it = 0, batch = 0;
         for (int item = first; item < total; item += step) {
             const Item m = item_of(p, S, item, split);
             bool stop = false;
-            for (int kb = m.kb0; kb < m.kb1; kb += 4, turn ^= 1) {
+            for (int kb = m.kb0; kb < m.kb1; kb += 4, batch++) {
                 const int n = min(4, m.kb1 - kb);
-                if (turn == (warp & 1)) {
+                if ((batch & 1) == (warp & 1)) {
                     uint2 wv[4][4], xv[MAX_BN / 32][4];
 #pragma unroll
                     for (int g = 0; g < 4; g++) {
                         const int r = g * 32 + lane;
-                        const int row = p.swiglu ? m.n0 + g * 16 + (lane & 15) : m.n0 + r;
+                        const int row = kSwiglu ? m.n0 + g * 16 + (lane & 15) : m.n0 + r;
                         const bool in = row < p.N;
                         const uint8_t *src =
-                            p.w_scales + ((int64_t)m.e * p.w_rows + (p.swiglu && lane >= 16 ? p.N : 0) + row) * p.pitch + kb * 8;
+                            p.w_scales + ((int64_t)m.e * p.w_rows + (kSwiglu && lane >= 16 ? p.N : 0) + row) * p.pitch + kb * 8;
 #pragma unroll
                         for (int i = 0; i < 4; i++)
                             wv[g][i] = in && i < n ? __ldg(reinterpret_cast<const uint2 *>(src) + i) : make_uint2(0u, 0u);
@@ -383,13 +491,12 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
                         for (int i = 0; i < 4; i++)
                             xv[g][i] = r < m.cnt && i < n ? __ldg(reinterpret_cast<const uint2 *>(src) + i) : make_uint2(0u, 0u);
                     }
+                    if (batch > 0) stop = !warp_wait(S, &S.turn[(batch - 1) & 1], ((batch - 1) >> 1) & 1);
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
                         if (i >= n || stop) break;
                         const int s = (it + i) % p.stages, u = (it + i) / p.stages;
-                        bool ok = true;
-                        if (lane == 0) ok = !S.abort && (u == 0 || tc::mbar_wait(&S.empty[s], (u - 1) & 1, kWaitNs));
-                        if (!__shfl_sync(0xffffffffu, (int)ok, 0)) {
+                        if (u > 0 && !warp_wait(S, &S.empty[s], (u - 1) & 1)) {
                             stop = true;
                             break;
                         }
@@ -410,6 +517,7 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
                         __syncwarp();
                         if (lane == 0) tc::mbar_arrive(&S.full[s]);
                     }
+                    if (lane == 0) tc::mbar_arrive(&S.turn[batch & 1]);
                 }
                 it += n;
                 if (stop) break;
@@ -420,10 +528,10 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
         // ---------------- sums out
         const int q = warp - EPI_WARP0;
         int j = 0;
-        for (int item = first; item < total && !S.abort; item += step, j++) {
+        for (int item = first; item < total; item += step, j++) {
             const Item m = item_of(p, S, item, split);
             const int acc = j & 1, v = j >> 1;
-            if (!tc::mbar_wait(&S.acc_full[acc], v & 1, kWaitNs)) {
+            if (!warp_wait(S, &S.acc_full[acc], v & 1)) {
                 if (lane == 0) set_status(p.status, MOE_ERR_TIMEOUT);
                 S.abort = 1;
                 break;
@@ -431,22 +539,19 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
             tc::tc_fence_after();
             const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * MAX_BN);
             for (int c = 0; c < m.cnt; c += 32) {
+                if (p.splits == 1) {
+                    write_rows<O, kSwiglu>(p, m, q, lane, tbase + c, c, S.stage[q]);
+                    continue;
+                }
                 uint32_t r[32];
                 __syncwarp();
                 tc::tmem_ld_32x32b_x32(tbase + c, r);
                 tc::tmem_ld_wait();
-                float f[32];
+                // every copy of this (only) item has been consumed: its stages hold the part now
+                float *part = reinterpret_cast<float *>(dyn) + c * BM + q * 32 + lane;
 #pragma unroll
-                for (int i = 0; i < 32; i++) f[i] = __uint_as_float(r[i]);
-                if (p.splits > 1) {
-                    // every copy of this (only) item has been consumed: its stages hold the part now
-                    float *part = reinterpret_cast<float *>(dyn) + c * BM + q * 32 + lane;
-#pragma unroll
-                    for (int i = 0; i < 32; i++)
-                        if (c + i < m.cnt) part[i * BM] = f[i];
-                } else {
-                    write_columns(p, m, q, lane, c, f);
-                }
+                for (int i = 0; i < 32; i++)
+                    if (c + i < m.cnt) part[i * BM] = __uint_as_float(r[i]);
             }
             tc::tc_fence_before();
             __syncwarp();
@@ -456,7 +561,7 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
             const int z0 = max(0, min(p.rows, __ldg(p.offsets + p.E)));
             const int64_t n = (int64_t)(p.rows - z0) * p.N;
             for (int64_t i = (int64_t)blockIdx.x * 128 + (threadIdx.x - EPI_WARP0 * 32); i < n; i += (int64_t)gridDim.x * 128)
-                store_out(p, (int64_t)z0 * p.N + i, 0.f);
+                O::store(static_cast<typename O::T *>(p.out) + (int64_t)z0 * p.N + i, 0.f);
         }
     }
     tc::tc_fence_before();
@@ -466,25 +571,18 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
         tc::tmem_dealloc(tmem, 512);
     }
     if (p.splits > 1) {
-        // the cluster's parts, added in order; each CTA takes groups of 32 rows in turn
+        // the cluster's parts, added in order; each CTA takes its share of the rows
         cluster_sync();
         if (warp >= EPI_WARP0 && first < total) {
             const int q = warp - EPI_WARP0;
             const Item m = item_of(p, S, first, split);
             const int per = (m.cnt + p.splits - 1) / p.splits;  // rows of this CTA
             const int c1 = min(m.cnt, (split + 1) * per);
-            for (int c = split * per; c < c1; c += 32) {
-                float f[32];
-#pragma unroll
-                for (int i = 0; i < 32; i++) {
-                    f[i] = 0.f;
-                    if (c + i < c1)
-                        for (int r = 0; r < p.splits; r++)
-                            f[i] += ld_cluster(tc::smem_u32(reinterpret_cast<float *>(dyn) + (c + i) * BM + q * 32 + lane), r);
-                }
-                Item mine = m;
-                mine.cnt = c1;
-                write_columns(p, mine, q, lane, c, f);
+            for (int c = split * per; c < c1; c++) {
+                const uint32_t a = tc::smem_u32(reinterpret_cast<float *>(dyn) + c * BM + q * 32 + lane);
+                float v = 0.f;
+                for (int r = 0; r < p.splits; r++) v += ld_cluster(a, r);
+                write_row<O, kSwiglu>(p, m, q, lane, c, v);
             }
         }
         cluster_sync();  // no CTA leaves while another reads its part
@@ -524,7 +622,7 @@ extern "C" moe_status moe_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_sc
     p.n_tiles = (N + tn - 1) / tn;
     p.swiglu = swiglu;
     p.offsets = offsets, p.w_scales = w_scales, p.x_scales = x_scales, p.pitch = p.nk * 8;
-    p.out = out, p.out_type = out_dtype, p.status = dev_status;
+    p.out = out, p.vec = aligned16(out) && N % 8 == 0, p.status = dev_status;
     // Rows per tile: what one group needs, twice the mean where there are
     // several (the groups' sizes are known on the device only).
     const int64_t groups = std::min(E, rows);
@@ -548,7 +646,6 @@ extern "C" moe_status moe_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_sc
     if (st == MOE_OK)
         st = make_tmap_2d(&mxm, x_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, K / 2, BK / 2, 32);
     if (st != MOE_OK) return st;
-    MOE_CUDA_TRY(cudaFuncSetAttribute(mx4_matmul_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(THREADS);
@@ -560,6 +657,11 @@ extern "C" moe_status moe_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_sc
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = p.splits > 1 ? 1 : 0;
-    MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, mx4_matmul_kernel, p, mw, mxm));
-    return check_launch("mx4_matmul");
+    return with_dtype(out_dtype, [&](auto o) {
+        using O = decltype(o);
+        auto fn = swiglu ? mx4_matmul_kernel<O, true> : mx4_matmul_kernel<O, false>;
+        MOE_CUDA_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+        MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, fn, p, mw, mxm));
+        return check_launch("mx4_matmul");
+    });
 }

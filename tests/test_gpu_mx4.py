@@ -198,6 +198,17 @@ def test_same_bits_every_time(moe):
         assert torch.equal(again, first)
 
 
+def test_many_steps_through_few_stages(moe):
+    """The widest tiles leave four stages, which a long K passes through many times: the same bits every time."""
+    rng = np.random.default_rng(17)
+    for rows, N in ((449, 2501), (1111, 300)):
+        (wc, ws, xc, xs), first = product(rng, 1, N, 4064, None, rows, torch.float32, False)
+        for _ in range(40):
+            again = torch.empty_like(first)
+            m.moe_mx4_matmul(wc, ws, 1, N, 4064, xc, xs, rows, None, again)
+            assert torch.equal(again, first)
+
+
 def test_bad_offsets_are_clipped_and_reported(moe):
     rng = np.random.default_rng(15)
     for bad in ([0, 3, 2, 6], [-4, 2, 3, 6], [0, 2, 3, 1000], [2 ** 31 - 1, -2 ** 31, 0, 6]):
