@@ -73,8 +73,22 @@ struct Shared {
     int warp_tot[THREADS / 32];
     int tile0[MAX_E + 1];  // row tiles before expert e
     int start[MAX_E], count[MAX_E];
-    alignas(16) char stage[4][32 * STAGE_PITCH];  // epilogue warps: 32 rows on their way out
+    alignas(16) char stage[4][16 * STAGE_PITCH];  // epilogue warps: 16 rows on their way out
 };
+
+// The value of lane 0, which the compiler then knows to be the same in the
+// whole warp: descriptors and coordinates stay in uniform registers, which the
+// TMA and tcgen05 instructions take.  (With values that might differ between
+// lanes each such instruction cost 120 to 140 cycles to issue.)
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
 
 struct Item {
     int e, p0, cnt;  // expert, first row, rows
@@ -105,12 +119,23 @@ __device__ __forceinline__ Item item_of(const Params &p, const Shared &S, int it
     e *= 32;
     e += __popc(__ballot_sync(0xffffffffu, e + lane < p.E && S.tile0[min(e + lane, p.E)] <= tt)) - 1;
     it.e = e;
-    const int cnt = S.count[e], j = tt - S.tile0[e], nt = S.tile0[e + 1] - S.tile0[e];
-    const int w = nt == 1 ? cnt : ((cnt + nt - 1) / nt + 15) & ~15;
-    it.p0 = S.start[e] + j * w;
-    it.cnt = min(w, cnt - j * w);
-    it.kb0 = p.nk * split / p.splits;
-    it.kb1 = p.nk * (split + 1) / p.splits;
+    const int cnt = S.count[e], t0 = S.tile0[e], nt = S.tile0[e + 1] - t0;
+    it.p0 = S.start[e];
+    it.cnt = cnt;
+    if (nt > 1) {
+        const int w = ((cnt + nt - 1) / nt + 15) & ~15;
+        it.p0 += (tt - t0) * w;
+        it.cnt = min(w, cnt - (tt - t0) * w);
+    }
+    it.e = uniform(it.e);
+    it.p0 = uniform(it.p0);
+    it.cnt = uniform(it.cnt);
+    it.kb0 = 0;
+    it.kb1 = p.nk;
+    if (p.splits > 1) {
+        it.kb0 = p.nk * split / p.splits;
+        it.kb1 = p.nk * (split + 1) / p.splits;
+    }
     return it;
 }
 
@@ -181,21 +206,26 @@ __device__ __forceinline__ uint32_t idesc_mxf4(int n, uint32_t id)
            (id << 29);
 }
 
-__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
-
-// 16 lanes x 32 columns: thread t gets lanes t/4 and t/4 + 8, of each group j of
-// eight columns 2 (t%4) and the next: r[4j], r[4j+1] and r[4j+2], r[4j+3].
-__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, float (&r)[16])
+// silu(g) u.  With t = e^-|g| <= 1 nothing overflows; 16-bit outputs take the
+// fast exponential and quotient (some 2^-21 relative for |g| < 8).
+template <class O>
+__device__ __forceinline__ float swiglu(float g, float u)
 {
-    uint32_t u[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
-          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
-        : "r"(taddr));
+    if (O::kBytes == 4) return g / (1.0f + expf(-g)) * u;
+    const float t = __expf(-fabsf(g)), r = __fdividef(1.0f, 1.0f + t);
+    return g * (g >= 0.f ? r : t * r) * u;
+}
+
+// 16 lanes x 16 columns: thread t gets lanes t/4 and t/4 + 8, of each group j of
+// eight columns 2 (t%4) and the next: r[4j], r[4j+1] and r[4j+2], r[4j+3].
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, float (&r)[8])
+{
+    uint32_t u[8];
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                 : "r"(taddr));
 #pragma unroll
-    for (int i = 0; i < 16; i++) r[i] = __uint_as_float(u[i]);
+    for (int i = 0; i < 8; i++) r[i] = __uint_as_float(u[i]);
 }
 
 __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
@@ -214,7 +244,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     return w;
 }
 
-// Rows c .. c+31 of a tile, whose sums lie in columns of tensor memory from
+// Rows c .. c+15 of a tile, whose sums lie in columns of tensor memory from
 // `taddr` on, a weight row per lane: this warp's 32 (SwiGLU: 16) output
 // columns.  16-bit outputs are transposed in shared memory (stmatrix) and leave
 // in pieces of 16 bytes; fp32 ones leave from the registers.
@@ -225,58 +255,44 @@ __device__ __forceinline__ void write_rows(const Params &p, const Item &m, int q
     using T = typename O::T;
     const int n0 = m.n0 + q * W, rows = m.cnt - c;
     T *out = static_cast<T *>(p.out) + (int64_t)(m.p0 + c) * p.N;
+    float a[8], b[8];
     __syncwarp();
-    if (!kSwiglu && O::kBytes == 4) {
-        uint32_t r[32];
-        tc::tmem_ld_32x32b_x32(taddr, r);
-        tc::tmem_ld_wait();
-        const int in = n0 + lane < p.N ? rows : 0;
-        T *o = out + n0 + lane;
-#pragma unroll
-        for (int i = 0; i < 32; i++, o += p.N)
-            if (i < in) O::store(o, __uint_as_float(r[i]));
-        return;
-    }
-    float a[16], b[16];
-    tmem_ld_16x256b_x4(taddr, a);
-    tmem_ld_16x256b_x4(taddr + (16u << 16), b);
+    tmem_ld_16x256b_x2(taddr, a);
+    tmem_ld_16x256b_x2(taddr + (16u << 16), b);
     tc::tmem_ld_wait();
     if (kSwiglu) {
 #pragma unroll
-        for (int i = 0; i < 16; i++) a[i] = swiglu(a[i], b[i]);
+        for (int i = 0; i < 8; i++) a[i] = swiglu<O>(a[i], b[i]);
     }
     if (O::kBytes == 4) {
 #pragma unroll
-        for (int i = 0; i < 16; i++) {
+        for (int i = 0; i < 8; i++) {
             const int row = (i >> 2) * 8 + 2 * (lane & 3) + (i & 1), n = n0 + lane / 4 + (i & 2) * 4;
-            if (row < rows && n < p.N) O::store(out + (int64_t)row * p.N + n, a[i]);
+            T *o = out + (int64_t)row * p.N + n;
+            if (row < rows && n < p.N) O::store(o, a[i]);
+            if (!kSwiglu && row < rows && n + 16 < p.N) O::store(o + 16, b[i]);
         }
         return;
     }
     constexpr int P = kSwiglu ? 48 : STAGE_PITCH;
     const uint32_t base = tc::smem_u32(stage) + ((lane >> 4) * 8 + (lane & 7)) * P + ((lane >> 3) & 1) * 16;
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 4; j += 2) {
-        stmatrix_x4_trans(base + j * 8 * P, pack2<O>(a[4 * j], a[4 * j + 1]), pack2<O>(a[4 * j + 2], a[4 * j + 3]),
-                          pack2<O>(a[4 * j + 4], a[4 * j + 5]), pack2<O>(a[4 * j + 6], a[4 * j + 7]));
-        if (!kSwiglu)
-            stmatrix_x4_trans(base + j * 8 * P + 32, pack2<O>(b[4 * j], b[4 * j + 1]), pack2<O>(b[4 * j + 2], b[4 * j + 3]),
-                              pack2<O>(b[4 * j + 4], b[4 * j + 5]), pack2<O>(b[4 * j + 6], b[4 * j + 7]));
-    }
+    stmatrix_x4_trans(base, pack2<O>(a[0], a[1]), pack2<O>(a[2], a[3]), pack2<O>(a[4], a[5]), pack2<O>(a[6], a[7]));
+    if (!kSwiglu)
+        stmatrix_x4_trans(base + 32, pack2<O>(b[0], b[1]), pack2<O>(b[2], b[3]), pack2<O>(b[4], b[5]), pack2<O>(b[6], b[7]));
     __syncwarp();
     if (p.vec && n0 + W <= p.N) {
         constexpr int L = W / 8;  // lanes per row
         const int row0 = lane / L, part = lane % L;
         T *o = out + (int64_t)row0 * p.N + n0 + part * 8;
 #pragma unroll
-        for (int i = 0; i < L; i++, o += (int64_t)(32 / L) * p.N) {
+        for (int i = 0; i < L / 2; i++, o += (int64_t)(32 / L) * p.N) {
             const int row = row0 + i * (32 / L);
             if (row < rows) *reinterpret_cast<uint4 *>(o) = *reinterpret_cast<const uint4 *>(stage + row * P + part * 16);
         }
-    } else if (lane < W && n0 + lane < p.N) {
+    } else {
+        const int in = lane < W && n0 + lane < p.N ? min(rows, 16) : 0;
         T *o = out + n0 + lane;
-        for (int i = 0; i < min(rows, 32); i++, o += p.N) *o = *reinterpret_cast<const T *>(stage + i * P + lane * 2);
+        for (int i = 0; i < in; i++, o += p.N) *o = *reinterpret_cast<const T *>(stage + i * P + lane * 2);
     }
 }
 
@@ -292,7 +308,7 @@ __device__ __forceinline__ void write_row(const Params &p, const Item &m, int q,
     }
     const float u = __shfl_down_sync(0xffffffffu, v, 16);  // lanes 0..15: gate, 16..31: the same columns' up
     const int n = m.n0 + q * 16 + lane;
-    if (lane < 16 && n < p.N) O::store(out + n, swiglu(v, u));
+    if (lane < 16 && n < p.N) O::store(out + n, swiglu<O>(v, u));
 }
 
 template <class O, bool kSwiglu>
@@ -305,7 +321,7 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
     const int b_bytes = (p.bn + 31) / 32 * 32 * (BK / 2);
     char *sA = dyn, *sB = sA + p.stages * A_BYTES, *sF = sB + p.stages * b_bytes;
     __shared__ Shared S;
-    const int warp = warp_id(), lane = lane_id();
+    const int warp = uniform(warp_id()), lane = lane_id();
     const int split = p.splits > 1 ? (int)cluster_rank() : 0;
     const int first = blockIdx.x / p.splits, step = gridDim.x / p.splits;
 
@@ -368,22 +384,23 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    const uint32_t tmem = S.tmem;
+    const uint32_t tmem = (uint32_t)uniform((int)S.tmem);
     // (a cluster that splits K takes one item; the grid holds them all)
-    const int total = p.splits > 1 ? min(S.tile0[p.E] * p.n_tiles, step) : S.tile0[p.E] * p.n_tiles;
+    const int tiles = uniform(S.tile0[p.E]) * p.n_tiles;
+    const int total = p.splits > 1 ? min(tiles, step) : tiles;
 
     if (warp == 0) {
         // ---------------- codes
-        int it = 0;
+        int it = 0, s = 0;
+        uint32_t phase = 1;  // parity of the stage's use before this one
         bool ok = true;
         for (int item = first; item < total && ok; item += step) {
             const Item m = item_of(p, S, item, split);
             const int boxes = (m.cnt + 31) / 32;
             for (int kb = m.kb0; kb < m.kb1; kb++, it++) {
-                const int s = it % p.stages, u = it / p.stages;
-                if (u > 0) ok = warp_wait(S, &S.empty[s], (u - 1) & 1);
+                if (it >= p.stages) ok = warp_wait(S, &S.empty[s], phase);
                 if (!ok) break;
-                if (lane == 0) {
+                if (elect_one()) {
                     tc::mbar_arrive_expect_tx(&S.full[s], A_BYTES + boxes * 32 * (BK / 2));
                     char *a = sA + s * A_BYTES, *b = sB + s * b_bytes;
                     const int x = kb * (BK / 2);
@@ -397,6 +414,8 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
                     for (int i = 0; i < boxes; i++)
                         tc::tma_load_2d(b + i * 32 * (BK / 2), &mx, x, m.p0 + i * 32, &S.full[s]);
                 }
+                __syncwarp();
+                if (++s == p.stages) s = 0, phase ^= 1;
             }
         }
         if (lane == 0) {
@@ -406,14 +425,15 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
             }
             // no copy may still be in flight when the CTA leaves (a full
             // barrier that never got its scales' arrival runs out of time)
-            for (int s = 0; s < p.stages && s < it; s++) {
-                const int u = (it - 1 - s) / p.stages;
-                if (!tc::mbar_wait(&S.full[s], u & 1, kWaitNs)) set_status(p.status, MOE_ERR_TIMEOUT);
+            for (int i = 0; i < p.stages && i < it; i++) {
+                const int u = (it - 1 - i) / p.stages;
+                if (!tc::mbar_wait(&S.full[i], u & 1, kWaitNs)) set_status(p.status, MOE_ERR_TIMEOUT);
             }
         }
     } else if (warp == 1) {
         // ---------------- MMA
-        int it = 0, j = 0;
+        int it = 0, j = 0, s = 0;
+        uint32_t phase = 0;
         bool ok = true;
         for (int item = first; item < total && ok; item += step, j++) {
             const Item m = item_of(p, S, item, split);
@@ -425,11 +445,10 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
             const uint32_t d = tmem + (uint32_t)(acc * MAX_BN);
             const uint32_t id0 = idesc_mxf4(n16, 0), id2 = idesc_mxf4(n16, 2);
             for (int kb = m.kb0; kb < m.kb1; kb++, it++) {
-                const int s = it % p.stages, u = it / p.stages;
-                ok = warp_wait(S, &S.full[s], u & 1);
+                ok = warp_wait(S, &S.full[s], phase);
                 if (!ok) break;
                 tc::tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
                     const uint32_t sfa = tmem + SF_COL + (it & 1) * 32, sfb = sfa + 8;
                     const uint32_t f = tc::smem_u32(sF + s * SF_BYTES);
 #pragma unroll
@@ -449,16 +468,16 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
                     tc::mma_commit(&S.empty[s]);
                     if (kb + 1 == m.kb1) tc::mma_commit(&S.acc_full[acc]);
                 }
+                __syncwarp();
+                if (++s == p.stages) s = 0, phase ^= 1;
             }
         }
-        if (lane == 0) {
-            if (!ok) {
-                set_status(p.status, MOE_ERR_TIMEOUT);
-                S.abort = 1;
-            }
-            tc::mma_commit(&S.mma_done);
-            if (!tc::mbar_wait(&S.mma_done, 0, kWaitNs)) set_status(p.status, MOE_ERR_TIMEOUT);
+        if (!ok && lane == 0) {
+            set_status(p.status, MOE_ERR_TIMEOUT);
+            S.abort = 1;
         }
+        if (elect_one()) tc::mma_commit(&S.mma_done);
+        if (!tc::mbar_wait(&S.mma_done, 0, kWaitNs) && lane == 0) set_status(p.status, MOE_ERR_TIMEOUT);
     } else if (warp == 2 || warp == 3) {
         // ---------------- scales: four steps at a time, the two warps in turn.
         // Both load ahead, but a warp stores its steps only after the other has
@@ -538,11 +557,12 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
             }
             tc::tc_fence_after();
             const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * MAX_BN);
-            for (int c = 0; c < m.cnt; c += 32) {
-                if (p.splits == 1) {
+            if (p.splits == 1) {
+#pragma unroll 1
+                for (int c = 0; c < m.cnt; c += 16)
                     write_rows<O, kSwiglu>(p, m, q, lane, tbase + c, c, S.stage[q]);
-                    continue;
-                }
+            }
+            for (int c = 0; p.splits > 1 && c < m.cnt; c += 32) {
                 uint32_t r[32];
                 __syncwarp();
                 tc::tmem_ld_32x32b_x32(tbase + c, r);
