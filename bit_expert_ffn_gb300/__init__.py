@@ -407,7 +407,7 @@ def moe_mx4_size(rows: int, cols: int):
 
 def _mx4(codes, scales, name, rows, cols):
     return (_packed(codes, name + "codes", rows * (cols // 2), 1),
-            _packed(scales, name + "scales", rows * ((cols + 255) // 256) * 8, 1))
+            _packed(scales, name + "scales", rows * ((cols + 1023) // 1024) * 32, 1))
 
 
 def moe_mx4_quantise(x, dtype, rows, cols, codes, scales, dev_status=None, stream=None):

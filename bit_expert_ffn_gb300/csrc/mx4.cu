@@ -3,13 +3,16 @@
 //
 // Both directions are one pass bound by memory: quantising reads a value once
 // and writes 17/32 byte for it.  A warp takes 256 columns of a row (eight
-// values per lane, a block per four lanes), which is one 8-byte unit of the
-// row's scales, so the scales' padding is written with them.
+// values per lane, a block per four lanes), eight bytes of the row's scales;
+// the last one of a row also clears the scales' padding.
 #include "rows.cuh"
 
 namespace moe {
 
 constexpr int kMxThreads = 256;
+
+// Bytes of a row's scales: 32 for 1024 values, the unit the product loads.
+__host__ __device__ constexpr int64_t mx4_pitch(int64_t cols) { return (cols + 1023) / 1024 * 32; }
 
 // Two fp32 values to e2m1 (nearest, ties to even, saturating at 6): lo in bits 0..3.
 __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi)
@@ -61,7 +64,9 @@ __global__ void __launch_bounds__(kMxThreads) mx4_quantise_kernel(const typename
         }
         if (c < cols) *reinterpret_cast<uint32_t *>(codes + r * (cols / 2) + c / 2) = q;
         if (bad && (lane & 3) == 0) set_status(status, MOE_ERR_NONFINITE);
-        if ((lane & 3) == 0) scales[u * 8 + lane / 4] = bad ? 255 : (uint8_t)byte;
+        uint8_t *sc = scales + r * mx4_pitch(cols);
+        if ((lane & 3) == 0) sc[g * 8 + lane / 4] = bad ? 255 : (uint8_t)byte;
+        if (g == groups - 1 && (groups + lane) * 8 < mx4_pitch(cols)) *reinterpret_cast<uint2 *>(sc + (groups + lane) * 8) = make_uint2(0, 0);
     }
 }
 
@@ -79,7 +84,7 @@ __global__ void __launch_bounds__(kMxThreads) mx4_dequantise_kernel(const uint8_
         const int c = (int)(u % groups) * 256 + lane * 8;
         if (c >= cols) continue;
         const uint32_t q = *reinterpret_cast<const uint32_t *>(codes + r * (cols / 2) + c / 2);
-        const uint32_t byte = scales[u * 8 + lane / 4];
+        const uint32_t byte = scales[r * mx4_pitch(cols) + c / 32];
         const float f = byte == 255u ? __uint_as_float(0x7fffffffu) : byte ? __uint_as_float(byte << 23)
                                                                              : __uint_as_float(0x00400000u);
         float v[8];
@@ -123,7 +128,7 @@ extern "C" moe_status moe_mx4_size(int64_t rows, int64_t cols, size_t *code_byte
     moe_status st = check_mx(rows, cols);
     if (st != MOE_OK) return st;
     if (code_bytes) *code_bytes = (size_t)(rows * (cols / 2));
-    if (scale_bytes) *scale_bytes = (size_t)(rows * ((cols + 255) / 256) * 8);
+    if (scale_bytes) *scale_bytes = (size_t)(rows * mx4_pitch(cols));
     return MOE_OK;
 }
 
@@ -137,7 +142,7 @@ extern "C" moe_status moe_mx4_quantise(const void *x, moe_dtype dtype, int64_t x
                 (long long)x_stride, (long long)cols);
     if (rows == 0) return MOE_OK;
     MOE_REQUIRE(x && codes && scales, "NULL pointer");
-    MOE_REQUIRE(aligned16(codes) && aligned16(scales), "codes and scales must be 16-byte aligned");
+    MOE_REQUIRE(aligned16(codes) && aligned_to(scales, 32), "codes must be 16-byte, scales 32-byte aligned");
     MOE_REQUIRE(aligned_to(x, dtype_bytes(dtype)), "x must be aligned to its type");
     const bool vec = aligned16(x) && (x_stride * dtype_bytes(dtype)) % 16 == 0;
     const unsigned grid = mx_grid(rows * ((cols + 255) / 256));
@@ -158,7 +163,7 @@ extern "C" moe_status moe_mx4_dequantise(const uint8_t *codes, const uint8_t *sc
     MOE_REQUIRE(dtype_ok(dtype), "dtype must be MOE_F32, MOE_BF16 or MOE_F16 (got %d)", (int)dtype);
     if (rows == 0) return MOE_OK;
     MOE_REQUIRE(codes && scales && out, "NULL pointer");
-    MOE_REQUIRE(aligned16(codes) && aligned16(scales), "codes and scales must be 16-byte aligned");
+    MOE_REQUIRE(aligned16(codes) && aligned_to(scales, 32), "codes must be 16-byte, scales 32-byte aligned");
     MOE_REQUIRE(aligned_to(out, dtype_bytes(dtype)), "out must be aligned to its type");
     const unsigned grid = mx_grid(rows * ((cols + 255) / 256));
     const bool vec = aligned16(out);

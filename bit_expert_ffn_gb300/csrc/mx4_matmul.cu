@@ -14,10 +14,10 @@
 // A CTA walks (row tile, weight tile) items.  A step is 256 of K (128 bytes
 // of codes per row).  Warp 0 loads the codes of both operands with TMA
 // (128-byte swizzle); warps 2 and 3 load the scales (eight bytes per row and
-// step, four steps at a time, taken in turn) and put them into shared memory
+// step, 32 bytes for four steps at a time, taken in turn) and put them into shared memory
 // in the order that tcgen05.cp spreads over tensor memory (row r of a
 // 128-row, 128-K chunk at byte (r % 32) * 16 + (r / 32) * 4); warp 1 issues the
-// copies of the scales and four MMAs of K = 64; warps 4..7 take the sums out
+// copies of the scales and four MMAs of K = 64; warps 4..11 take the sums out
 // of tensor memory, two accumulators in turn.
 //
 // With SwiGLU a tile holds 64 gate rows and their 64 up rows, 16 of each in
@@ -45,8 +45,8 @@ constexpr int MAX_STAGES = 12;
 constexpr int A_BYTES = BM * BK / 2;
 constexpr int SF_BYTES = 2 * 512 + 4 * 512;  // scales of a step: weights, then rows (two chunks of 128 rows)
 constexpr int SF_COL = 2 * MAX_BN;           // tensor memory columns of the scales (two sets of 32)
-constexpr int THREADS = 256;
-constexpr int EPI_WARP0 = 4;
+constexpr int THREADS = 384;
+constexpr int EPI_WARP0 = 4, EPI_WARPS = 8;  // two per quarter of the lanes: alone in its quarter a warp mostly waits
 constexpr int MAX_E = 1024;
 constexpr int STAGE_PITCH = 80;  // 32 16-bit columns and 16 bytes, so that eight rows fall into different banks
 constexpr unsigned long long kWaitNs = 2000000000ull;
@@ -57,7 +57,7 @@ struct Params {
     int n_tiles, bn, stages, splits, swiglu;
     const int32_t *offsets;      // NULL: one group of all rows
     const uint8_t *w_scales, *x_scales;
-    int pitch;                   // bytes of scales per row
+    int pitch;                   // bytes of scales per row, a multiple of 32: four steps
     void *out;
     int vec;  // rows of out are 16-byte pieces
     int32_t *status;
@@ -70,10 +70,10 @@ struct Shared {
     uint64_t mma_done;
     uint32_t tmem;
     volatile int abort;
-    int warp_tot[THREADS / 32];
+    int warp_tot[MAX_E / 128];
     int tile0[MAX_E + 1];  // row tiles before expert e
     int start[MAX_E], count[MAX_E];
-    alignas(16) char stage[4][16 * STAGE_PITCH];  // epilogue warps: 16 rows on their way out
+    alignas(16) char stage[EPI_WARPS][16 * STAGE_PITCH];  // epilogue warps: 16 rows on their way out
 };
 
 // The value of lane 0, which the compiler then knows to be the same in the
@@ -95,19 +95,6 @@ struct Item {
     int n0;          // first output column
     int kb0, kb1;    // steps of this CTA
 };
-
-__device__ __forceinline__ void group_of(const Params &p, int e, int &p0, int &cnt)
-{
-    if (!p.offsets) {
-        p0 = 0;
-        cnt = p.rows;
-        return;
-    }
-    // both ends clipped first, so that no offsets lead out of the rows
-    const int a = min(max(__ldg(p.offsets + e), 0), p.rows), b = min(max(__ldg(p.offsets + e + 1), 0), p.rows);
-    p0 = a;
-    cnt = max(0, b - a);
-}
 
 // The whole warp finds the last expert with tile0 <= tt: 32 ranges, then one.
 __device__ __forceinline__ Item item_of(const Params &p, const Shared &S, int item, int split)
@@ -228,6 +215,20 @@ __device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, float (&r)[8]
     for (int i = 0; i < 8; i++) r[i] = __uint_as_float(u[i]);
 }
 
+// 32 lanes x 16 columns, a lane per thread.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, float (&r)[16])
+{
+    uint32_t u[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 16; i++) r[i] = __uint_as_float(u[i]);
+}
+
 __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
@@ -255,8 +256,19 @@ __device__ __forceinline__ void write_rows(const Params &p, const Item &m, int q
     using T = typename O::T;
     const int n0 = m.n0 + q * W, rows = m.cnt - c;
     T *out = static_cast<T *>(p.out) + (int64_t)(m.p0 + c) * p.N;
-    float a[8], b[8];
     __syncwarp();
+    if (!kSwiglu && O::kBytes == 4) {  // a row's 32 columns are 128 bytes as they lie
+        float v[16];
+        tmem_ld_32x32b_x16(taddr, v);
+        tc::tmem_ld_wait();
+        const int in = n0 + lane < p.N ? rows : 0;
+        T *o = out + n0 + lane;
+#pragma unroll
+        for (int i = 0; i < 16; i++, o += p.N)
+            if (i < in) O::store(o, v[i]);
+        return;
+    }
+    float a[8], b[8];
     tmem_ld_16x256b_x2(taddr, a);
     tmem_ld_16x256b_x2(taddr + (16u << 16), b);
     tc::tmem_ld_wait();
@@ -268,9 +280,7 @@ __device__ __forceinline__ void write_rows(const Params &p, const Item &m, int q
 #pragma unroll
         for (int i = 0; i < 8; i++) {
             const int row = (i >> 2) * 8 + 2 * (lane & 3) + (i & 1), n = n0 + lane / 4 + (i & 2) * 4;
-            T *o = out + (int64_t)row * p.N + n;
-            if (row < rows && n < p.N) O::store(o, a[i]);
-            if (!kSwiglu && row < rows && n + 16 < p.N) O::store(o + 16, b[i]);
+            if (row < rows && n < p.N) O::store(out + (int64_t)row * p.N + n, a[i]);
         }
         return;
     }
@@ -311,6 +321,17 @@ __device__ __forceinline__ void write_row(const Params &p, const Item &m, int q,
     if (lane < 16 && n < p.N) O::store(out + n, swiglu<O>(v, u));
 }
 
+// 32 bytes (four steps) of a row's scales, or zeros.
+__device__ __forceinline__ void load32(const uint8_t *src, bool in, uint32_t (&v)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = 0;
+    if (in)
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                     : "l"(src));
+}
+
 template <class O, bool kSwiglu>
 __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_constant__ Params p,
                                                                 const __grid_constant__ CUtensorMap mw,
@@ -325,23 +346,40 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
     const int split = p.splits > 1 ? (int)cluster_rank() : 0;
     const int first = blockIdx.x / p.splits, step = gridDim.x / p.splits;
 
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; s++) {
+            tc::mbar_init(&S.full[s], 2);  // the producer's (with the bytes of its copies) and the scales'
+            tc::mbar_init(&S.empty[s], 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            tc::mbar_init(&S.acc_full[i], 1);
+            tc::mbar_init(&S.acc_empty[i], EPI_WARPS);
+        }
+        tc::mbar_init(&S.turn[0], 1);
+        tc::mbar_init(&S.turn[1], 1);
+        tc::mbar_init(&S.mma_done, 1);
+        S.abort = 0;
+        tc::fence_mbar_init();
+        tc::tma_prefetch_desc(&mw);
+        tc::tma_prefetch_desc(&mx);
+    }
+    if (warp == THREADS / 32 - 1) tc::tmem_alloc(&S.tmem, 512);
     // row tiles before each expert: four experts per thread, then a scan
-    {
-        int n[MAX_E / THREADS], sum = 0;
+    if (threadIdx.x < MAX_E / 4) {
+        int off[5], n[4], sum = 0;
+        const int e0 = threadIdx.x * 4;
 #pragma unroll
-        for (int i = 0; i < MAX_E / THREADS; i++) {
-            const int e = threadIdx.x * (MAX_E / THREADS) + i;
-            int p0 = 0, cnt = 0;
-            if (e < p.E) {
-                group_of(p, e, p0, cnt);
-                if (p.offsets && blockIdx.x == 0) {
-                    const int a = p.offsets[e], b = p.offsets[e + 1];
-                    if (a < 0 || b < a || b > p.rows) set_status(p.status, MOE_ERR_BOUNDS);
-                }
-            }
-            if (e < p.E) {
-                S.start[e] = p0;
-                S.count[e] = cnt;
+        for (int i = 0; i < 5; i++) off[i] = p.offsets && e0 + i <= p.E ? __ldg(p.offsets + e0 + i) : (e0 + i ? p.rows : 0);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            // both ends clipped first, so that no offsets lead out of the rows
+            const int a = min(max(off[i], 0), p.rows), b = min(max(off[i + 1], 0), p.rows);
+            const int cnt = e0 + i < p.E ? max(0, b - a) : 0;
+            if (e0 + i < p.E) {
+                if (blockIdx.x == 0 && (off[i] < 0 || off[i + 1] < off[i] || off[i + 1] > p.rows))
+                    set_status(p.status, MOE_ERR_BOUNDS);
+                S.start[e0 + i] = a;
+                S.count[e0 + i] = cnt;
             }
             n[i] = sum;
             sum += (cnt + p.bn - 1) / p.bn;
@@ -353,34 +391,14 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
             if (lane >= o) incl += v;
         }
         if (lane == 31) S.warp_tot[warp] = incl;
-        __syncthreads();
+        tc::named_sync(1, MAX_E / 4);
         int base = incl - sum;
         for (int i = 0; i < warp; i++) base += S.warp_tot[i];
 #pragma unroll
-        for (int i = 0; i < MAX_E / THREADS; i++) {
-            const int e = threadIdx.x * (MAX_E / THREADS) + i;
-            if (e <= p.E) S.tile0[e] = base + n[i];
-        }
-        if (p.E == MAX_E && threadIdx.x == THREADS - 1) S.tile0[MAX_E] = base + sum;
+        for (int i = 0; i < 4; i++)
+            if (e0 + i <= p.E) S.tile0[e0 + i] = base + n[i];
+        if (p.E == MAX_E && e0 + 4 == MAX_E) S.tile0[MAX_E] = base + sum;
     }
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < p.stages; s++) {
-            tc::mbar_init(&S.full[s], 2);  // the producer's (with the bytes of its copies) and the scales'
-            tc::mbar_init(&S.empty[s], 1);
-        }
-        for (int i = 0; i < 2; i++) {
-            tc::mbar_init(&S.acc_full[i], 1);
-            tc::mbar_init(&S.acc_empty[i], 4);
-        }
-        tc::mbar_init(&S.turn[0], 1);
-        tc::mbar_init(&S.turn[1], 1);
-        tc::mbar_init(&S.mma_done, 1);
-        S.abort = 0;
-        tc::fence_mbar_init();
-        tc::tma_prefetch_desc(&mw);
-        tc::tma_prefetch_desc(&mx);
-    }
-    if (warp == 2) tc::tmem_alloc(&S.tmem, 512);
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
@@ -487,50 +505,43 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
         for (int item = first; item < total; item += step) {
             const Item m = item_of(p, S, item, split);
             bool stop = false;
-            for (int kb = m.kb0; kb < m.kb1; kb += 4, batch++) {
-                const int n = min(4, m.kb1 - kb);
+            for (int base = m.kb0 & ~3; base < m.kb1; base += 4, batch++) {
+                const int lo = max(base, m.kb0), n = min(base + 4, m.kb1) - lo;  // (a part of K may begin within the four)
                 if ((batch & 1) == (warp & 1)) {
-                    uint2 wv[4][4], xv[MAX_BN / 32][4];
+                    uint32_t wv[4][8], xv[MAX_BN / 32][8];
 #pragma unroll
                     for (int g = 0; g < 4; g++) {
-                        const int r = g * 32 + lane;
-                        const int row = kSwiglu ? m.n0 + g * 16 + (lane & 15) : m.n0 + r;
-                        const bool in = row < p.N;
-                        const uint8_t *src =
-                            p.w_scales + ((int64_t)m.e * p.w_rows + (kSwiglu && lane >= 16 ? p.N : 0) + row) * p.pitch + kb * 8;
-#pragma unroll
-                        for (int i = 0; i < 4; i++)
-                            wv[g][i] = in && i < n ? __ldg(reinterpret_cast<const uint2 *>(src) + i) : make_uint2(0u, 0u);
+                        const int row = kSwiglu ? m.n0 + g * 16 + (lane & 15) : m.n0 + g * 32 + lane;
+                        load32(p.w_scales + ((int64_t)m.e * p.w_rows + (kSwiglu && lane >= 16 ? p.N : 0) + row) * p.pitch + base * 8,
+                               row < p.N, wv[g]);
                     }
 #pragma unroll
                     for (int g = 0; g < MAX_BN / 32; g++) {
                         const int r = g * 32 + lane;
-                        const uint8_t *src = p.x_scales + (int64_t)(m.p0 + r) * p.pitch + kb * 8;
-#pragma unroll
-                        for (int i = 0; i < 4; i++)
-                            xv[g][i] = r < m.cnt && i < n ? __ldg(reinterpret_cast<const uint2 *>(src) + i) : make_uint2(0u, 0u);
+                        load32(p.x_scales + (int64_t)(m.p0 + r) * p.pitch + base * 8, r < m.cnt, xv[g]);
                     }
                     if (batch > 0) stop = !warp_wait(S, &S.turn[(batch - 1) & 1], ((batch - 1) >> 1) & 1);
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
-                        if (i >= n || stop) break;
-                        const int s = (it + i) % p.stages, u = (it + i) / p.stages;
+                        const int at = it + base + i - lo;
+                        if (base + i < lo || base + i >= lo + n || stop) continue;
+                        const int s = at % p.stages, u = at / p.stages;
                         if (u > 0 && !warp_wait(S, &S.empty[s], (u - 1) & 1)) {
                             stop = true;
-                            break;
+                            continue;
                         }
                         char *f = sF + s * SF_BYTES;
 #pragma unroll
                         for (int g = 0; g < 4; g++) {
-                            *reinterpret_cast<uint32_t *>(f + lane * 16 + g * 4) = wv[g][i].x;
-                            *reinterpret_cast<uint32_t *>(f + 512 + lane * 16 + g * 4) = wv[g][i].y;
+                            *reinterpret_cast<uint32_t *>(f + lane * 16 + g * 4) = wv[g][2 * i];
+                            *reinterpret_cast<uint32_t *>(f + 512 + lane * 16 + g * 4) = wv[g][2 * i + 1];
                         }
 #pragma unroll
                         for (int g = 0; g < MAX_BN / 32; g++) {
                             if (g * 32 >= p.bn) break;
                             char *b = f + 1024 + (g >> 2) * 512 + lane * 16 + (g & 3) * 4;
-                            *reinterpret_cast<uint32_t *>(b) = xv[g][i].x;
-                            *reinterpret_cast<uint32_t *>(b + 1024) = xv[g][i].y;
+                            *reinterpret_cast<uint32_t *>(b) = xv[g][2 * i];
+                            *reinterpret_cast<uint32_t *>(b + 1024) = xv[g][2 * i + 1];
                         }
                         tc::fence_proxy_async_smem();
                         __syncwarp();
@@ -545,7 +556,7 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
         }
     } else {
         // ---------------- sums out
-        const int q = warp - EPI_WARP0;
+        const int q = warp & 3, half = (warp - EPI_WARP0) >> 2;
         int j = 0;
         for (int item = first; item < total; item += step, j++) {
             const Item m = item_of(p, S, item, split);
@@ -559,19 +570,19 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
             const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * MAX_BN);
             if (p.splits == 1) {
 #pragma unroll 1
-                for (int c = 0; c < m.cnt; c += 16)
-                    write_rows<O, kSwiglu>(p, m, q, lane, tbase + c, c, S.stage[q]);
+                for (int c = half * 16; c < m.cnt; c += 32)
+                    write_rows<O, kSwiglu>(p, m, q, lane, tbase + c, c, S.stage[warp - EPI_WARP0]);
             }
-            for (int c = 0; p.splits > 1 && c < m.cnt; c += 32) {
-                uint32_t r[32];
+            for (int c = half * 16; p.splits > 1 && c < m.cnt; c += 32) {
+                float r[16];
                 __syncwarp();
-                tc::tmem_ld_32x32b_x32(tbase + c, r);
+                tmem_ld_32x32b_x16(tbase + c, r);
                 tc::tmem_ld_wait();
                 // every copy of this (only) item has been consumed: its stages hold the part now
                 float *part = reinterpret_cast<float *>(dyn) + c * BM + q * 32 + lane;
 #pragma unroll
-                for (int i = 0; i < 32; i++)
-                    if (c + i < m.cnt) part[i * BM] = __uint_as_float(r[i]);
+                for (int i = 0; i < 16; i++)
+                    if (c + i < m.cnt) part[i * BM] = r[i];
             }
             tc::tc_fence_before();
             __syncwarp();
@@ -580,13 +591,14 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
         if (p.offsets) {  // rows of no group
             const int z0 = max(0, min(p.rows, __ldg(p.offsets + p.E)));
             const int64_t n = (int64_t)(p.rows - z0) * p.N;
-            for (int64_t i = (int64_t)blockIdx.x * 128 + (threadIdx.x - EPI_WARP0 * 32); i < n; i += (int64_t)gridDim.x * 128)
+            constexpr int kThreads = EPI_WARPS * 32;
+            for (int64_t i = (int64_t)blockIdx.x * kThreads + (threadIdx.x - EPI_WARP0 * 32); i < n; i += (int64_t)gridDim.x * kThreads)
                 O::store(static_cast<typename O::T *>(p.out) + (int64_t)z0 * p.N + i, 0.f);
         }
     }
     tc::tc_fence_before();
     __syncthreads();
-    if (warp == 2) {
+    if (warp == THREADS / 32 - 1) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem, 512);
     }
@@ -594,11 +606,11 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
         // the cluster's parts, added in order; each CTA takes its share of the rows
         cluster_sync();
         if (warp >= EPI_WARP0 && first < total) {
-            const int q = warp - EPI_WARP0;
+            const int q = warp & 3, half = (warp - EPI_WARP0) >> 2;
             const Item m = item_of(p, S, first, split);
             const int per = (m.cnt + p.splits - 1) / p.splits;  // rows of this CTA
             const int c1 = min(m.cnt, (split + 1) * per);
-            for (int c = split * per; c < c1; c++) {
+            for (int c = split * per + half; c < c1; c += 2) {
                 const uint32_t a = tc::smem_u32(reinterpret_cast<float *>(dyn) + c * BM + q * 32 + lane);
                 float v = 0.f;
                 for (int r = 0; r < p.splits; r++) v += ld_cluster(a, r);
@@ -631,8 +643,8 @@ extern "C" moe_status moe_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_sc
     MOE_REQUIRE(offsets || E == 1, "offsets may be NULL for E = 1 only (got E=%d)", E);
     if (rows == 0) return MOE_OK;
     MOE_REQUIRE(w_codes && w_scales && x_codes && x_scales && out, "NULL pointer");
-    MOE_REQUIRE(aligned16(w_codes) && aligned16(w_scales) && aligned16(x_codes) && aligned16(x_scales),
-                "codes and scales must be 16-byte aligned");
+    MOE_REQUIRE(aligned16(w_codes) && aligned16(x_codes), "codes must be 16-byte aligned");
+    MOE_REQUIRE(aligned_to(w_scales, 32) && aligned_to(x_scales, 32), "scales must be 32-byte aligned");
     MOE_REQUIRE(aligned_to(out, dtype_bytes(out_dtype)) && aligned_to(offsets, 4), "out and offsets must be aligned to their types");
     const bool swiglu = epilogue == MOE_MX4_SWIGLU;
     Params p = {};
@@ -641,7 +653,7 @@ extern "C" moe_status moe_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_sc
     const int tn = swiglu ? BM / 2 : BM;
     p.n_tiles = (N + tn - 1) / tn;
     p.swiglu = swiglu;
-    p.offsets = offsets, p.w_scales = w_scales, p.x_scales = x_scales, p.pitch = p.nk * 8;
+    p.offsets = offsets, p.w_scales = w_scales, p.x_scales = x_scales, p.pitch = (p.nk + 3) / 4 * 32;
     p.out = out, p.vec = aligned16(out) && N % 8 == 0, p.status = dev_status;
     // Rows per tile: what one group needs, twice the mean where there are
     // several (the groups' sizes are known on the device only).

@@ -541,10 +541,10 @@ moe_status moe_combine_backward(const void *dout, const void *y, moe_dtype dtype
  *   codes:  [rows][cols/2] bytes, value i of a row in the low (i even) or high
  *           (i odd) half of byte i/2: an e2m1 number, sign at bit 3, magnitude
  *           0, 0.5, 1, 1.5, 2, 3, 4 or 6 for codes 0..7;
- *   scales: [rows][8 * ceil(cols/256)] bytes, byte b of a row the exponent
+ *   scales: [rows][32 * ceil(cols/1024)] bytes, byte b of a row the exponent
  *           (e8m0, 2^(byte - 127), 255 = NaN) of values 32b .. 32b+31; bytes
  *           past cols/32 are 0.
- * Both are 16-byte aligned.
+ * codes are 16-byte and scales 32-byte aligned.
  *
  * moe_mx4_quantise: per block of 32, with m its largest magnitude,
  * e = max(floor(log2 m) - 2, -127) and code = e2m1(x 2^-e), to nearest, ties

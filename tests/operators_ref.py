@@ -56,10 +56,10 @@ def quantise(x):
 
 
 def pack(code, byte):
-    """The stored form: two codes per byte, scale rows padded with zeros to a multiple of eight bytes."""
+    """The stored form: two codes per byte, scale rows padded with zeros to a multiple of 32 bytes."""
     r = code.shape[0]
     codes = (code[:, 0::2] | (code[:, 1::2] << 4)).astype(np.uint8)
-    scales = np.zeros((r, (byte.shape[1] + 7) // 8 * 8), np.uint8)
+    scales = np.zeros((r, (byte.shape[1] + 31) // 32 * 32), np.uint8)
     scales[:, :byte.shape[1]] = byte
     return codes, scales
 

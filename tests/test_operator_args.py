@@ -49,9 +49,10 @@ def test_existing_calls_still_refuse_fp16():
 
 
 def test_mx4():
-    assert m.moe_mx4_size(3, 32) == (48, 24)
-    assert m.moe_mx4_size(1, 256) == (128, 8)
-    assert m.moe_mx4_size(2, 288) == (288, 32)
+    assert m.moe_mx4_size(3, 32) == (48, 96)
+    assert m.moe_mx4_size(1, 256) == (128, 32)
+    assert m.moe_mx4_size(2, 288) == (288, 64)
+    assert m.moe_mx4_size(1, 1056) == (528, 64)
     assert m.moe_mx4_size(0, 64) == (0, 0)
     refused(BAD, "cols", m.moe_mx4_size, 1, 33)
     refused(BAD, "cols", m.moe_mx4_size, 1, 0)
@@ -61,7 +62,7 @@ def test_mx4():
     refused(BAD, "aligned", m.moe_mx4_quantise, A + 2, m.MOE_F32, 1, 64, A, A)
     refused(BAD, "NULL", m.moe_mx4_quantise, None, m.MOE_F32, 1, 64, A, A)
     refused(BAD, "NULL", m.moe_mx4_dequantise, A, A, 1, 64, None)
-    refused(BAD, "16-byte", m.moe_mx4_dequantise, A, A + 4, 1, 64, A)
+    refused(BAD, "32-byte", m.moe_mx4_dequantise, A, A + 16, 1, 64, A)
     args = dict(out_dtype=m.MOE_F32)
     refused(BAD, "E", m.moe_mx4_matmul, A, A, 0, 8, 64, A, A, 1, A, A, **args)
     refused(BAD, "E", m.moe_mx4_matmul, A, A, 1025, 8, 64, A, A, 1, A, A, **args)
@@ -115,5 +116,5 @@ def test_tensors_that_are_too_small_or_not_packed():
     refused(BAD, "offsets", m.moe_dispatch, x, m.MOE_F32, 4, 8, 2, 4, off[:4], inv, out)
     refused(BAD, "inv_perm", m.moe_dispatch, x, m.MOE_F32, 4, 8, 2, 4, off, inv.long(), out)
     refused(BAD, "codes", m.moe_mx4_quantise, torch.zeros(2, 64), m.MOE_F32, 2, 64, torch.zeros(63, dtype=torch.uint8),
-            torch.zeros(16, dtype=torch.uint8))
+            torch.zeros(64, dtype=torch.uint8))
     refused(BAD, "w_post", m.moe_block_norm, **norm(w_post=torch.zeros(63)), y=A, u=A)
