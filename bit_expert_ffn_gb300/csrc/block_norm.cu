@@ -21,13 +21,16 @@ __global__ void __launch_bounds__(G::kThreads) block_norm_kernel(const __grid_co
     constexpr int N = G::N;
     constexpr bool kRing = G::NV < 4;
     extern __shared__ __align__(16) char ring[];
-    __shared__ float slots[2][32];
+    __shared__ __align__(16) float slots[2][32];
     const int H = p.H, step = gridDim.x * G::count();
+    const float inv_h = 1.0f / (float)H;
     const int xs = norm_slot(H, R::kBytes), row_bytes = xs + norm_slot(H, A::kBytes);
+    G::clear(slots);
     char *mine = ring + G::index() * p.stages * row_bytes;
     auto x_row = [&](int64_t t) { return static_cast<const typename R::T *>(p.x) + t * p.x_stride; };
     auto b_row = [&](int64_t t) { return static_cast<const typename A::T *>(p.b) + t * p.b_stride; };
-    auto fetch = [&](int64_t t, char *to) {
+    auto fetch = [&](int64_t t, const char *slot) {
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot);
         if (t < p.T) {
             norm_fetch<R, G>(to, x_row(t), H);
             norm_fetch<A, G>(to + xs, b_row(t), H);
@@ -46,9 +49,9 @@ __global__ void __launch_bounds__(G::kThreads) block_norm_kernel(const __grid_co
         char *slot = mine + s * row_bytes;
         if (kRing) {
             norm_wait(p.stages);
-            G::sync();
-            G::template load<A>(norm_slot_row<A>(slot + xs, b_row(t)), H, b);
-            G::template load<R>(norm_slot_row<R>(slot, x_row(t)), H, x);
+            if (!G::kVec) G::sync();
+            norm_read<A, G>(slot + xs, b_row(t), H, b);
+            norm_read<R, G>(slot, x_row(t), H, x);
         } else {
             G::template load<A>(b_row(t), H, b);
             G::template load<R>(x_row(t), H, x);
@@ -58,11 +61,11 @@ __global__ void __launch_bounds__(G::kThreads) block_norm_kernel(const __grid_co
         for (int i = 0; i < N; i++) q[0] = fmaf(b[i], b[i], q[0]);
         G::sum(q, slots);
         if (kRing) {  // every thread has read the slot
-            if (G::kWarp) __syncwarp();
+            if (G::kWarp && !G::kVec) __syncwarp();
             fetch(t + (int64_t)p.stages * step, slot);
             if (++s == p.stages) s = 0;
         }
-        const float r1 = 1.0f / sqrtf(q[0] / (float)H + p.eps);
+        const float r1 = rsqrtf(q[0] * inv_h + p.eps);
         const float f = p.alpha * r1 * (p.gate_kind == MOE_GATE_TOKEN ? p.gate[t] : 1.f);
         q[0] = 0.f;
 #pragma unroll
@@ -71,7 +74,7 @@ __global__ void __launch_bounds__(G::kThreads) block_norm_kernel(const __grid_co
             q[0] = fmaf(x[i], x[i], q[0]);
         }
         G::sum(q, slots + 1);
-        const float r2 = 1.0f / sqrtf(q[0] / (float)H + p.eps);
+        const float r2 = rsqrtf(q[0] * inv_h + p.eps);
         G::template store<R>(static_cast<typename R::T *>(p.y) + t * H, H, x);
 #pragma unroll
         for (int i = 0; i < N; i++) x[i] *= r2 * gn[i];
@@ -92,7 +95,7 @@ NormPlan norm_plan(int T, int H, int res_bytes, int act_bytes, bool backward, bo
     q.stages = q.nv == 4 ? 0 : 2 * row <= kNormRingBytes ? 2 : 1;
     q.smem = row * q.stages;
     // threads that an SM holds at the kernels' registers
-    const int per_sm = backward ? (q.warp ? 384 : q.nv == 1 ? 768 : 512) : (q.warp || q.nv > 1 ? 512 : 1024);
+    const int per_sm = backward ? (!q.warp && q.nv == 1 ? 768 : 512) : (q.warp || q.nv > 1 ? 512 : 1024);
     int resident = std::max(1, std::min(32, per_sm / q.threads));
     if (q.smem) resident = std::max(1, std::min<int>(resident, (int)((kNormRingBytes + 20 * 1024) / (q.smem + 1024))));
     q.grid = (int)std::min<int64_t>((T + groups - 1) / groups, (int64_t)sm_count() * resident);
@@ -134,9 +137,10 @@ extern "C" moe_status moe_block_norm(const void *x, moe_dtype res_dtype, int64_t
     const int rb = dtype_bytes(res_dtype), ab = dtype_bytes(dtype);
     MOE_REQUIRE(aligned_to(y, rb) && aligned_to(u, ab) && aligned_to(w_post, 4) && aligned_to(w_pre, 4),
                 "y, u, w_post and w_pre must be aligned to their types");
-    const bool vec = H % 8 == 0 && aligned16(x) && aligned16(b) && aligned16(y) && aligned16(u) && aligned16(w_post) &&
+    const bool vec = H % 4 == 0 && aligned_to(x, 4 * rb) && aligned_to(b, 4 * ab) && aligned_to(y, 4 * rb) && aligned_to(u, 4 * ab) &&
+                     aligned16(w_post) &&
                      aligned16(w_pre) && (gate_kind != MOE_GATE_CHANNEL || aligned16(gate)) &&
-                     x_stride * rb % 16 == 0 && b_stride * ab % 16 == 0;
+                     x_stride % 4 == 0 && b_stride % 4 == 0;
     const NormPlan q = norm_plan(T, H, rb, ab, false, vec);
     NormArgs p = {};
     p.x = x, p.b = b, p.x_stride = x_stride, p.b_stride = b_stride, p.T = T, p.H = H, p.w_post = w_post, p.w_pre = w_pre;

@@ -25,15 +25,17 @@ struct NormArgs {
 };
 
 // How a group of threads shares a row.  kWarp: a warp per row, four rows a CTA;
-// else the CTA.  A thread holds NV groups of eight columns, consecutive when
-// kVec (16 or 32 byte accesses), else strided by the group's width.
+// else the CTA.  A thread holds 8 NV columns: fours, strided by the group's
+// width, when kVec (a warp's access is 256 or 512 bytes in a row; eights gave
+// fp32 rows half sectors, 156 against 100 us for the gradient of 16384 x 2048), else single
+// ones.
 template <int NV_, bool kVec_, bool kWarp_>
 struct Group {
     static constexpr int NV = NV_, N = NV_ * 8;
     static constexpr bool kVec = kVec_, kWarp = kWarp_;
     static constexpr int kThreads = kWarp ? 128 : 512;  // at most
     // registers of the gradient's kernel: 80 leave room for three CTAs of 256 threads
-    static constexpr int kBackRegs = kWarp ? 168 : NV == 1 ? 80 : 128;
+    static constexpr int kBackRegs = NV == 1 ? 80 : 128;
 
     __device__ static int width() { return kWarp ? 32 : (int)blockDim.x; }
     __device__ static int rank() { return kWarp ? lane_id() : (int)threadIdx.x; }
@@ -46,7 +48,7 @@ struct Group {
     }
 
     // K sums over the group, the same bits in every thread: lanes by a tree,
-    // then the warps in order.  `slots`: 32 floats per sum, not those of the
+    // then the warps in fours.  `slots`: 32 floats per sum, not those of the
     // sum before (so one barrier per call is enough).
     template <int K>
     __device__ static void sum(float (&v)[K], float (*slots)[32])
@@ -60,48 +62,54 @@ struct Group {
             for (int k = 0; k < K; k++)
                 if (lane_id() == 0) slots[k][warp_id()] = v[k];
             __syncthreads();
-            const int warps = (int)(blockDim.x >> 5);
 #pragma unroll
-            for (int k = 0; k < K; k++) v[k] = 0.f;
-            for (int i = 0; i < warps; i++)
+            for (int k = 0; k < K; k++) {
+                v[k] = 0.f;
 #pragma unroll
-                for (int k = 0; k < K; k++) v[k] += slots[k][i];
+                for (int i = 0; i < kThreads / 128; i++) {
+                    if (i * 128 >= (int)blockDim.x) break;
+                    const float4 q = reinterpret_cast<const float4 *>(slots[k])[i];  // zero past the last warp
+                    v[k] += (q.x + q.y) + (q.z + q.w);
+                }
+            }
         }
     }
 
-    __device__ static int col(int i) { return kVec ? ((i >> 3) * width() + rank()) * 8 + (i & 7) : rank() + i * width(); }
+    // Before the first sum.
+    template <int K>
+    __device__ static void clear(float (&slots)[K][32])
+    {
+        if constexpr (!kWarp) {
+            for (int i = threadIdx.x; i < K * 32; i += blockDim.x) slots[i / 32][i % 32] = 0.f;
+            __syncthreads();
+        }
+    }
+
+    __device__ static int col(int i) { return kVec ? ((i >> 2) * width() + rank()) * 4 + (i & 3) : rank() + i * width(); }
 
     template <class A>
     __device__ static void load(const typename A::T *p, int H, float (&v)[N])
     {
-        if (kVec) {
 #pragma unroll
-            for (int g = 0; g < NV; g++) {
-                float t[8] = {};
-                if (col(g * 8) < H) A::load8(p + col(g * 8), t);
-#pragma unroll
-                for (int i = 0; i < 8; i++) v[g * 8 + i] = t[i];
+        for (int i = 0; i < N; i += kVec ? 4 : 1) {
+            const int c = col(i);
+            if constexpr (kVec) {
+                v[i] = v[i + 1] = v[i + 2] = v[i + 3] = 0.f;
+                if (c < H) A::load4(p + c, v + i);
+            } else {
+                v[i] = c < H ? A::load(p + c) : 0.f;
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; i++) v[i] = col(i) < H ? A::load(p + col(i)) : 0.f;
         }
     }
     template <class A>
     __device__ static void store(typename A::T *p, int H, const float (&v)[N])
     {
-        if (kVec) {
 #pragma unroll
-            for (int g = 0; g < NV; g++) {
-                float t[8];
-#pragma unroll
-                for (int i = 0; i < 8; i++) t[i] = v[g * 8 + i];
-                if (col(g * 8) < H) A::store8(p + col(g * 8), t);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; i++)
-                if (col(i) < H) A::store(p + col(i), v[i]);
+        for (int i = 0; i < N; i += kVec ? 4 : 1) {
+            const int c = col(i);
+            if (c >= H) continue;
+            if constexpr (kVec) A::store4(p + c, v + i);
+            else A::store(p + c, v[i]);
         }
     }
     // w (NULL: ones), times the channel gate if there is one
@@ -126,23 +134,41 @@ struct Group {
 // its first 16-byte piece.
 __host__ __device__ constexpr int norm_slot(int H, int elem) { return ((H * elem + 15) / 16 + 1) * 16; }
 
-// Starts the copy of a row's 16-byte pieces (those that hold any of it; the
-// last one only up to the row's end) into shared memory.
-template <class A, class G>
-__device__ __forceinline__ void norm_fetch(char *dst, const typename A::T *row, int H)
+__device__ __forceinline__ void norm_copy16(uint32_t dst, const void *src, int n)
 {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(row), lo = a & ~uintptr_t(15), end = a + (uintptr_t)H * A::kBytes;
-    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-    for (uintptr_t c = lo + G::rank() * 16; c < end; c += G::width() * 16) {
-        const int n = end - c < 16 ? (int)(end - c) : 16;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + (uint32_t)(c - lo)), "l"(c), "r"(n) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+// Starts the copy of a row into shared memory.  Aligned rows: each thread
+// fetches the pieces of its own columns and needs no barrier to read them.  Others: all 16-byte
+// pieces that hold any of the row, the last one only up to the row's end.
+template <class A, class G>
+__device__ __forceinline__ void norm_fetch(uint32_t dst, const typename A::T *row, int H)
+{
+    if constexpr (G::kVec) {
+#pragma unroll
+        for (int i = 0; i < G::N; i += 4) {
+            const int c = G::col(i);
+            if (c >= H) break;
+            if (A::kBytes == 4) norm_copy16(dst + c * 4, row + c, 16);
+            else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst + c * 2), "l"(row + c) : "memory");
+        }
+    } else {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(row), lo = a & ~uintptr_t(15), end = a + (uintptr_t)H * A::kBytes;
+        for (uintptr_t c = lo + G::rank() * 16; c < end; c += G::width() * 16)
+            norm_copy16(dst + (uint32_t)(c - lo), reinterpret_cast<const void *>(c), end - c < 16 ? (int)(end - c) : 16);
     }
 }
 
-template <class A>
-__device__ __forceinline__ const typename A::T *norm_slot_row(const char *slot, const typename A::T *row)
+// The thread's columns of a row fetched to `slot` (`row`: where it came from).
+template <class A, class G>
+__device__ __forceinline__ void norm_read(const char *slot, const typename A::T *row, int H, float (&v)[G::N])
 {
-    return reinterpret_cast<const typename A::T *>(slot + (reinterpret_cast<uintptr_t>(row) & 15));
+    if constexpr (G::kVec) {
+        G::template load<A>(reinterpret_cast<const typename A::T *>(slot), H, v);
+    } else {
+        G::template load<A>(reinterpret_cast<const typename A::T *>(slot + (reinterpret_cast<uintptr_t>(row) & 15)), H, v);
+    }
 }
 
 __device__ __forceinline__ void norm_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }

@@ -19,19 +19,21 @@ __global__ void __launch_bounds__(G::kThreads) __maxnreg__(G::kBackRegs) block_n
 {
     constexpr int N = G::N;
     constexpr bool kRing = G::NV < 4;
-    constexpr bool kKeep = G::NV == 1 || G::kWarp;  // the weights stay in registers (else they come from L1 for each row)
+    constexpr bool kKeep = G::NV < 4;  // the weights stay in registers (else they come from L1 for each row)
     extern __shared__ __align__(16) char ring[];
-    __shared__ float slots[4][32];
+    __shared__ __align__(16) float slots[4][32];
     const int H = p.H, step = gridDim.x * G::count();
     const float inv_h = 1.0f / (float)H;
     const int rs = norm_slot(H, R::kBytes), as = norm_slot(H, A::kBytes), row_bytes = 2 * (rs + as);
+    G::clear(slots);
     char *mine = ring + G::index() * p.stages * row_bytes;
     const float *gate_c = p.gate_kind == MOE_GATE_CHANNEL ? p.gate : nullptr;
     auto x_row = [&](int64_t t) { return static_cast<const typename R::T *>(p.x) + t * p.x_stride; };
     auto b_row = [&](int64_t t) { return static_cast<const typename A::T *>(p.b) + t * p.b_stride; };
     auto dy_row = [&](int64_t t) { return static_cast<const typename R::T *>(p.dy) + t * H; };
     auto du_row = [&](int64_t t) { return static_cast<const typename A::T *>(p.du) + t * H; };
-    auto fetch = [&](int64_t t, char *to) {
+    auto fetch = [&](int64_t t, const char *slot) {
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot);
         if (t < p.T) {
             norm_fetch<R, G>(to, x_row(t), H);
             norm_fetch<A, G>(to + rs, b_row(t), H);
@@ -50,31 +52,32 @@ __global__ void __launch_bounds__(G::kThreads) __maxnreg__(G::kBackRegs) block_n
     }
     int s = 0;
     for (int64_t t = t0; t < p.T; t += step) {
-        float y[N], b[N], du[N], dy[N];
+        float y[N], b[N], d[N];  // (du and dy are read again where they are needed: registers are scarcer)
         char *slot = mine + s * row_bytes;
-        if (kRing) {
+        auto read_du = [&] {
+            if (!p.du) {
+#pragma unroll
+                for (int i = 0; i < N; i++) d[i] = 0.f;
+            } else if constexpr (kRing) {
+                norm_read<A, G>(slot + 2 * rs + as, du_row(t), H, d);
+            } else {
+                G::template load<A>(du_row(t), H, d);
+            }
+        };
+        if constexpr (kRing) {
             norm_wait(p.stages);
-            G::sync();
-            G::template load<A>(norm_slot_row<A>(slot + rs, b_row(t)), H, b);
-            G::template load<R>(norm_slot_row<R>(slot, x_row(t)), H, y);
+            if (!G::kVec) G::sync();
+            norm_read<A, G>(slot + rs, b_row(t), H, b);
+            norm_read<R, G>(slot, x_row(t), H, y);
         } else {
             G::template load<A>(b_row(t), H, b);
             G::template load<R>(x_row(t), H, y);
         }
-#pragma unroll
-        for (int i = 0; i < N; i++) du[i] = dy[i] = 0.f;
-        if (p.du) G::template load<A>(kRing ? norm_slot_row<A>(slot + 2 * rs + as, du_row(t)) : du_row(t), H, du);
-        if (p.dy) G::template load<R>(kRing ? norm_slot_row<R>(slot + rs + as, dy_row(t)) : dy_row(t), H, dy);
         float q[1] = {};
 #pragma unroll
         for (int i = 0; i < N; i++) q[0] = fmaf(b[i], b[i], q[0]);
         G::sum(q, slots);
-        if (kRing) {  // every thread has read the slot
-            if (G::kWarp) __syncwarp();
-            fetch(t + (int64_t)p.stages * step, slot);
-            if (++s == p.stages) s = 0;
-        }
-        const float r1 = 1.0f / sqrtf(q[0] * inv_h + p.eps);
+        const float r1 = rsqrtf(q[0] * inv_h + p.eps);
         const float gt = p.gate_kind == MOE_GATE_TOKEN ? p.gate[t] : 1.f;
         const float f = p.alpha * r1 * gt;
         if (!kKeep) {
@@ -82,29 +85,44 @@ __global__ void __launch_bounds__(G::kThreads) __maxnreg__(G::kBackRegs) block_n
             G::weights(p.w_pre, nullptr, H, gn);
         }
         float q2[2] = {};
+        read_du();
 #pragma unroll
         for (int i = 0; i < N; i++) {
             y[i] = fmaf(f * b[i], gp[i], y[i]);
             q2[0] = fmaf(y[i], y[i], q2[0]);
-            q2[1] = fmaf(du[i] * gn[i], y[i], q2[1]);
+            q2[1] = fmaf(d[i] * gn[i], y[i], q2[1]);
         }
         G::sum(q2, slots + 1);
-        const float r2 = 1.0f / sqrtf(q2[0] * inv_h + p.eps);
+        const float r2 = rsqrtf(q2[0] * inv_h + p.eps);
         const float m2 = r2 * r2 * r2 * q2[1] * inv_h;
         q[0] = 0.f;
+        read_du();
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            const float n2 = y[i] * r2;
-            a2[i] = fmaf(du[i], n2, a2[i]);
-            dy[i] = dy[i] + r2 * du[i] * gn[i] - y[i] * m2;
-            a1[i] = fmaf(f * dy[i], b[i], a1[i]);
-            q[0] = fmaf(dy[i] * gp[i], b[i], q[0]);
+            a2[i] = fmaf(d[i], y[i] * r2, a2[i]);
+            y[i] = r2 * d[i] * gn[i] - y[i] * m2;
         }
-        G::template store<R>(static_cast<typename R::T *>(p.y) + t * H, H, dy);
+        if (p.dy) {
+            if constexpr (kRing) norm_read<R, G>(slot + rs + as, dy_row(t), H, d);
+            else G::template load<R>(dy_row(t), H, d);
+#pragma unroll
+            for (int i = 0; i < N; i++) y[i] += d[i];
+        }
+#pragma unroll
+        for (int i = 0; i < N; i++) {  // y holds t now
+            a1[i] = fmaf(f * y[i], b[i], a1[i]);
+            q[0] = fmaf(y[i] * gp[i], b[i], q[0]);
+        }
         G::sum(q, slots + 3);  // sum of t w_post' b
+        if (kRing) {  // every thread has read the slot
+            if (G::kWarp && !G::kVec) __syncwarp();
+            fetch(t + (int64_t)p.stages * step, slot);
+            if (++s == p.stages) s = 0;
+        }
+        G::template store<R>(static_cast<typename R::T *>(p.y) + t * H, H, y);
         const float m1 = p.alpha * gt * r1 * r1 * r1 * q[0] * inv_h;
 #pragma unroll
-        for (int i = 0; i < N; i++) b[i] = f * gp[i] * dy[i] - b[i] * m1;
+        for (int i = 0; i < N; i++) b[i] = f * gp[i] * y[i] - b[i] * m1;
         G::template store<A>(static_cast<typename A::T *>(p.u) + t * H, H, b);
         if (p.dgate_token && G::rank() == 0) p.dgate_token[t] = p.alpha * r1 * q[0];
     }
@@ -203,10 +221,9 @@ extern "C" moe_status moe_block_norm_backward(const void *x, moe_dtype res_dtype
                     aligned_to(w_post, 4) && aligned_to(w_pre, 4) && aligned_to(dw_post, 4) && aligned_to(dw_pre, 4) &&
                     aligned_to(dgate, 4),
                 "the gradients and weights must be aligned to their types");
-    const bool vec = H % 8 == 0 && aligned16(x) && aligned16(b) && aligned16(dy) && aligned16(du) && aligned16(dx) &&
-                     aligned16(db) && aligned16(w_post) && aligned16(w_pre) &&
-                     (gate_kind != MOE_GATE_CHANNEL || aligned16(gate)) && x_stride * rb % 16 == 0 &&
-                     b_stride * ab % 16 == 0;
+    const bool vec = H % 4 == 0 && aligned_to(x, 4 * rb) && aligned_to(b, 4 * ab) && aligned_to(dy, 4 * rb) &&
+                     aligned_to(du, 4 * ab) && aligned_to(dx, 4 * rb) && aligned_to(db, 4 * ab) && aligned16(w_post) && aligned16(w_pre) &&
+                     (gate_kind != MOE_GATE_CHANNEL || aligned16(gate)) && x_stride % 4 == 0 && b_stride % 4 == 0;
     const NormPlan q = norm_plan(T, H, rb, ab, true, vec);
     const size_t need = (size_t)norm_parts(T, H) * 2 * H * sizeof(float);
     if (!ws || ws_bytes < need)

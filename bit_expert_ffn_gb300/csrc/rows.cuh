@@ -21,6 +21,12 @@ struct F32 {
         reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
         reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
     }
+    __device__ static void load4(const T *p, float *v)
+    {
+        const float4 a = *reinterpret_cast<const float4 *>(p);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    }
+    __device__ static void store4(T *p, const float *v) { *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]); }
 };
 
 struct Bf16 {
@@ -47,6 +53,23 @@ struct Bf16 {
     }
     __device__ static void load8(const T *p, float (&v)[8]) { unpack8(*reinterpret_cast<const uint4 *>(p), v); }
     __device__ static void store8(T *p, const float (&v)[8]) { *reinterpret_cast<uint4 *>(p) = pack8(v); }
+    __device__ static void load4(const T *p, float *v)
+    {
+        const uint2 q = *reinterpret_cast<const uint2 *>(p);
+        const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    __device__ static void store4(T *p, const float *v)
+    {
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < 2; i++) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    }
 };
 
 struct Fp16 {
@@ -73,6 +96,23 @@ struct Fp16 {
     }
     __device__ static void load8(const T *p, float (&v)[8]) { unpack8(*reinterpret_cast<const uint4 *>(p), v); }
     __device__ static void store8(T *p, const float (&v)[8]) { *reinterpret_cast<uint4 *>(p) = pack8(v); }
+    __device__ static void load4(const T *p, float *v)
+    {
+        const uint2 q = *reinterpret_cast<const uint2 *>(p);
+        const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            v[2 * i] = fp16_to_f32((uint16_t)(w[i] & 0xffffu));
+            v[2 * i + 1] = fp16_to_f32((uint16_t)(w[i] >> 16));
+        }
+    }
+    __device__ static void store4(T *p, const float *v)
+    {
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < 2; i++) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    }
 };
 
 inline bool dtype_ok(moe_dtype t) { return t == MOE_F32 || t == MOE_BF16 || t == MOE_F16; }
