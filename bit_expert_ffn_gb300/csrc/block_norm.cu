@@ -87,7 +87,7 @@ NormPlan norm_plan(int T, int H, int res_bytes, int act_bytes, bool backward, bo
     NormPlan q = {};
     q.vec = vec;
     q.warp = H <= kNormWarpH;
-    q.nv = q.warp ? 2 : H <= 4096 ? 1 : H <= 8192 ? 2 : 4;
+    q.nv = q.warp ? (H <= 256 ? 1 : 2) : H <= 4096 ? 1 : H <= 8192 ? 2 : 4;
     const int groups = q.warp ? 4 : 1;
     q.threads = q.warp ? 128 : ((H + 8 * q.nv - 1) / (8 * q.nv) + 31) / 32 * 32;
     const size_t row = (size_t)(backward ? 2 : 1) * (norm_slot(H, res_bytes) + norm_slot(H, act_bytes)) * groups;
@@ -95,7 +95,7 @@ NormPlan norm_plan(int T, int H, int res_bytes, int act_bytes, bool backward, bo
     q.stages = q.nv == 4 ? 0 : 2 * row <= kNormRingBytes ? 2 : 1;
     q.smem = row * q.stages;
     // threads that an SM holds at the kernels' registers
-    const int per_sm = backward ? (!q.warp && q.nv == 1 ? 768 : 512) : (q.warp || q.nv > 1 ? 512 : 1024);
+    const int per_sm = q.nv > 1 ? 512 : backward ? 768 : 1024;
     int resident = std::max(1, std::min(32, per_sm / q.threads));
     if (q.smem) resident = std::max(1, std::min<int>(resident, (int)((kNormRingBytes + 20 * 1024) / (q.smem + 1024))));
     q.grid = (int)std::min<int64_t>((T + groups - 1) / groups, (int64_t)sm_count() * resident);

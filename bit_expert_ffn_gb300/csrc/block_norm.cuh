@@ -202,6 +202,7 @@ moe_status with_norm_types(moe_dtype r, moe_dtype a, F f)
 template <class F>
 moe_status with_norm_group(const NormPlan &q, F f)
 {
+    if (q.warp && q.nv == 1) return q.vec ? f(Group<1, true, true>{}) : f(Group<1, false, true>{});
     if (q.warp) return q.vec ? f(Group<2, true, true>{}) : f(Group<2, false, true>{});
     if (q.nv == 1) return q.vec ? f(Group<1, true, false>{}) : f(Group<1, false, false>{});
     if (q.nv == 2) return q.vec ? f(Group<2, true, false>{}) : f(Group<2, false, false>{});
