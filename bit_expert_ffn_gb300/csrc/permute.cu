@@ -12,6 +12,7 @@ namespace moe {
 
 constexpr int kPermChunk = 2048;     // pairs per chunk in the multi-CTA path
 constexpr int kPermSmallMax = 4096;  // single-CTA path up to this many pairs
+constexpr int kPlaceWarps = 8;       // warps per chunk in the multi-CTA path
 
 // Warp-serial stable placement of pairs [f0, f1) starting from per-expert
 // cursors `cur` (shared memory).  Lanes take 32 pairs at a time in order.
@@ -37,6 +38,37 @@ __device__ void place_pairs(const int32_t *__restrict__ ids, int64_t f0, int64_t
         __syncwarp();
         if (valid && (m & lt) == 0) cur[id] += __popc(m);
         __syncwarp();
+    }
+}
+
+// The warps of a CTA share pairs [f0, f1): warp w takes the w-th run of `seg`
+// (a multiple of 32) pairs.  A warp places 32 pairs in some 0.4 us whatever
+// it does beside (a chain of dependent steps), so the runs are short: each
+// warp first counts its own, and starts from the counts of the warps before.
+// hist: [warps][E] int32 in shared memory.
+__device__ void count_runs(const int32_t *__restrict__ ids, int64_t f0, int64_t f1, int seg, int E, int warps,
+                           int32_t *hist, int32_t *status)
+{
+    for (int i = threadIdx.x; i < warps * E; i += blockDim.x) hist[i] = 0;
+    __syncthreads();
+    if (warp_id() < warps) {
+        const int64_t a = f0 + (int64_t)warp_id() * seg, b = min(f1, a + seg);
+        for (int64_t f = a + lane_id(); f < b; f += 32) {
+            const int id = ids[f];
+            if (id >= 0 && id < E) atomicAdd(&hist[warp_id() * E + id], 1);
+            else if (id != MOE_ID_NOT_LOCAL) set_status(status, MOE_ERR_BOUNDS);
+        }
+    }
+    __syncthreads();
+}
+
+// Counts become cursors: expert e's first warp starts at `start`.
+__device__ __forceinline__ void runs_to_cursors(int e, int E, int warps, int start, int32_t *hist)
+{
+    for (int w = 0; w < warps; w++) {
+        const int c = hist[w * E + e];
+        hist[w * E + e] = start;
+        start += c;
     }
 }
 
@@ -71,32 +103,31 @@ __device__ int block_exclusive_scan(int v, int32_t *warp_tot, int &total)
 }
 
 // Single CTA (1024 threads): count, scan, place.
-__global__ void __launch_bounds__(1024) permute_small_kernel(const int32_t *__restrict__ ids, int n, int E,
-                                                             int32_t *__restrict__ offsets, int32_t *__restrict__ perm,
-                                                             int32_t *__restrict__ inv, int32_t *status)
+__global__ void __launch_bounds__(1024) permute_small_kernel(const int32_t *__restrict__ ids, int n, int E, int warps,
+                                                             int seg, int32_t *__restrict__ offsets,
+                                                             int32_t *__restrict__ perm, int32_t *__restrict__ inv,
+                                                             int32_t *status)
 {
-    __shared__ int32_t cnt[1024];
+    extern __shared__ int32_t hist[];
     __shared__ int32_t warp_tot[33];
     int tid = threadIdx.x;
-    if (tid < E) cnt[tid] = 0;
-    __syncthreads();
-    for (int f = tid; f < n; f += blockDim.x) {
-        int id = ids[f];
-        if (id >= 0 && id < E) atomicAdd(&cnt[id], 1);
-        else if (id != MOE_ID_NOT_LOCAL) set_status(status, MOE_ERR_BOUNDS);
-    }
-    __syncthreads();
-    int v = tid < E ? cnt[tid] : 0;
+    count_runs(ids, 0, n, seg, E, warps, hist, status);
+    int v = 0;
+    if (tid < E)
+        for (int w = 0; w < warps; w++) v += hist[w * E + tid];
     int total = 0;
     int excl = block_exclusive_scan(v, warp_tot, total);
     if (tid < E) {
         offsets[tid] = excl;
-        cnt[tid] = excl;  // becomes the placement cursor
+        runs_to_cursors(tid, E, warps, excl, hist);
     }
     if (tid == 0) offsets[E] = total;
     for (int p = total + tid; p < n; p += blockDim.x) perm[p] = -1;
     __syncthreads();
-    if (warp_id() == 0) place_pairs(ids, 0, n, E, cnt, perm, inv);
+    if (warp_id() < warps) {
+        const int64_t f0 = (int64_t)warp_id() * seg;
+        place_pairs(ids, f0, min((int64_t)n, f0 + seg), E, hist + warp_id() * E, perm, inv);
+    }
 }
 
 // Multi-CTA pass 1: per-chunk histograms -> counts[chunk][E].
@@ -125,13 +156,16 @@ __global__ void __launch_bounds__(1024) permute_scan_kernel(const int32_t *__res
     __shared__ int32_t warp_tot[33];
     int tid = threadIdx.x;
     int v = 0;
-    if (tid < E)
+    if (tid < E) {
+#pragma unroll 16
         for (int c = 0; c < n_chunks; c++) v += counts[(int64_t)c * E + tid];
+    }
     int total = 0;
     int excl = block_exclusive_scan(v, warp_tot, total);
     if (tid < E) {
         offsets[tid] = excl;
         int run = excl;
+#pragma unroll 16
         for (int c = 0; c < n_chunks; c++) {
             base[(int64_t)c * E + tid] = run;
             run += counts[(int64_t)c * E + tid];
@@ -141,17 +175,21 @@ __global__ void __launch_bounds__(1024) permute_scan_kernel(const int32_t *__res
     for (int64_t p = total + tid; p < n; p += blockDim.x) perm[p] = -1;
 }
 
-// Multi-CTA pass 3: one warp per chunk places its pairs in order.
-__global__ void permute_place_kernel(const int32_t *__restrict__ ids, int64_t n, int E,
-                                     const int32_t *__restrict__ base, int32_t *__restrict__ perm,
-                                     int32_t *__restrict__ inv)
+// Multi-CTA pass 3: a CTA of kPlaceWarps warps per chunk places its pairs in order.
+__global__ void __launch_bounds__(kPlaceWarps * 32) permute_place_kernel(const int32_t *__restrict__ ids, int64_t n, int E,
+                                                                         const int32_t *__restrict__ base,
+                                                                         int32_t *__restrict__ perm,
+                                                                         int32_t *__restrict__ inv)
 {
-    __shared__ int32_t cur[1024];
-    for (int e = threadIdx.x; e < E; e += blockDim.x) cur[e] = base[(int64_t)blockIdx.x * E + e];
+    __shared__ int32_t hist[kPlaceWarps * 1024];
+    constexpr int seg = kPermChunk / kPlaceWarps;
+    const int64_t f0 = (int64_t)blockIdx.x * kPermChunk, f1 = min(n, f0 + kPermChunk);
+    count_runs(ids, f0, f1, seg, E, kPlaceWarps, hist, nullptr);
+    for (int e = threadIdx.x; e < E; e += blockDim.x)
+        runs_to_cursors(e, E, kPlaceWarps, base[(int64_t)blockIdx.x * E + e], hist);
     __syncthreads();
-    int64_t f0 = (int64_t)blockIdx.x * kPermChunk;
-    int64_t f1 = min(n, f0 + kPermChunk);
-    if (warp_id() == 0) place_pairs(ids, f0, f1, E, cur, perm, inv);
+    const int64_t a = f0 + (int64_t)warp_id() * seg;
+    place_pairs(ids, a, min(f1, a + seg), E, hist + warp_id() * E, perm, inv);
 }
 
 static int64_t n_chunks_for(int64_t n) { return (n + kPermChunk - 1) / kPermChunk; }
@@ -213,7 +251,12 @@ extern "C" moe_status moe_permute(const int32_t *ids, int T, int k, int E, int32
     }
     MOE_REQUIRE(ids && perm && inv_perm, "NULL pointer");
     if (n <= kPermSmallMax) {
-        permute_small_kernel<<<1, 1024, 0, s>>>(ids, (int)n, E, offsets, perm, inv_perm, dev_status);
+        // as many runs of 32 or more pairs as 48 KB of counters hold
+        const int most = (int)std::min<int64_t>(std::min(32, 12288 / E), (n + 31) / 32);
+        const int seg = (int)((n + most * 32 - 1) / (most * 32)) * 32;
+        const int warps = (int)((n + seg - 1) / seg);
+        permute_small_kernel<<<1, 1024, (size_t)warps * E * sizeof(int32_t), s>>>(ids, (int)n, E, warps, seg, offsets, perm,
+                                                                                inv_perm, dev_status);
         return check_launch("permute_small");
     }
     int64_t c = n_chunks_for(n);
@@ -229,7 +272,7 @@ extern "C" moe_status moe_permute(const int32_t *ids, int T, int k, int E, int32
     permute_scan_kernel<<<1, 1024, 0, s>>>(counts, (int)c, E, n, base, offsets, perm);
     st = check_launch("permute_scan");
     if (st != MOE_OK) return st;
-    permute_place_kernel<<<(unsigned)c, 32, 0, s>>>(ids, n, E, base, perm, inv_perm);
+    permute_place_kernel<<<(unsigned)c, kPlaceWarps * 32, 0, s>>>(ids, n, E, base, perm, inv_perm);
     return check_launch("permute_place");
 }
 
@@ -325,6 +368,6 @@ extern "C" moe_status moe_permute_noalloc(const int32_t *ids, int T, int k, int 
     permute_scan_kernel<<<1, 1024, 0, s>>>(counts, (int)c, E, n, base, offsets, perm);
     st = check_launch("permute_scan (no-alloc)");
     if (st != MOE_OK) return st;
-    permute_place_kernel<<<(unsigned)c, 32, 0, s>>>(ids, n, E, base, perm, inv_perm);
+    permute_place_kernel<<<(unsigned)c, kPlaceWarps * 32, 0, s>>>(ids, n, E, base, perm, inv_perm);
     return check_launch("permute_place (no-alloc)");
 }
