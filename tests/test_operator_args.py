@@ -56,6 +56,7 @@ def test_mx4():
     assert m.moe_mx4_size(0, 64) == (0, 0)
     refused(BAD, "cols", m.moe_mx4_size, 1, 33)
     refused(BAD, "cols", m.moe_mx4_size, 1, 0)
+    refused(BAD, "too many", m.moe_mx4_size, 2 ** 50, 64)
     refused(BAD, "cols", m.moe_mx4_quantise, A, m.MOE_F32, 1, 48, A, A)
     refused(BAD, "dtype", m.moe_mx4_quantise, A, 7, 1, 64, A, A)
     refused(BAD, "16-byte", m.moe_mx4_quantise, A, m.MOE_F32, 1, 64, A + 8, A)
