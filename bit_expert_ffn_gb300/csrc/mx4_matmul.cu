@@ -13,12 +13,11 @@
 //
 // A CTA walks (row tile, weight tile) items.  A step is 256 of K (128 bytes
 // of codes per row).  Warp 0 loads the codes of both operands with TMA
-// (128-byte swizzle); warps 2 and 3 load the scales (eight bytes per row and
-// step, 32 bytes for four steps at a time, taken in turn) and put them into shared memory
-// in the order that tcgen05.cp spreads over tensor memory (row r of a
-// 128-row, 128-K chunk at byte (r % 32) * 16 + (r / 32) * 4); warp 1 issues the
-// copies of the scales and four MMAs of K = 64; warps 4..11 take the sums out
-// of tensor memory, two accumulators in turn.
+// (128-byte swizzle); warps 2..5 load the scales (32 bytes of a row are four
+// steps) and put them into shared memory in the order that tcgen05.cp spreads
+// over tensor memory (row r of a 128-row, 128-K chunk at byte (r % 32) * 16 +
+// (r / 32) * 4); warp 1 issues the copies of the scales and four MMAs of K = 64;
+// warps 6..13 take the sums out of tensor memory, two accumulators in turn.
 //
 // With SwiGLU a tile holds 64 gate rows and their 64 up rows, 16 of each in
 // turn, so that both of a column's sums lie in one warp's lanes.
@@ -45,8 +44,9 @@ constexpr int MAX_STAGES = 12;
 constexpr int A_BYTES = BM * BK / 2;
 constexpr int SF_BYTES = 2 * 512 + 4 * 512;  // scales of a step: weights, then rows (two chunks of 128 rows)
 constexpr int SF_COL = 2 * MAX_BN;           // tensor memory columns of the scales (two sets of 32)
-constexpr int THREADS = 384;
-constexpr int EPI_WARP0 = 4, EPI_WARPS = 8;  // two per quarter of the lanes: alone in its quarter a warp mostly waits
+constexpr int SF_WARP0 = 2, SF_WARPS = 4;
+constexpr int THREADS = 448;
+constexpr int EPI_WARP0 = SF_WARP0 + SF_WARPS, EPI_WARPS = 8;  // two per quarter of the lanes: alone in its quarter a warp mostly waits
 constexpr int MAX_E = 1024;
 constexpr int STAGE_PITCH = 80;  // 32 16-bit columns and 16 bytes, so that eight rows fall into different banks
 constexpr unsigned long long kWaitNs = 2000000000ull;
@@ -66,7 +66,6 @@ struct Params {
 struct Shared {
     uint64_t full[MAX_STAGES], empty[MAX_STAGES];
     uint64_t acc_full[2], acc_empty[2];
-    uint64_t turn[2];  // the scale warps' hand-over
     uint64_t mma_done;
     uint32_t tmem;
     volatile int abort;
@@ -348,15 +347,13 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; s++) {
-            tc::mbar_init(&S.full[s], 2);  // the producer's (with the bytes of its copies) and the scales'
+            tc::mbar_init(&S.full[s], 1 + SF_WARPS);  // the producer's (with the bytes of its copies) and the scales'
             tc::mbar_init(&S.empty[s], 1);
         }
         for (int i = 0; i < 2; i++) {
             tc::mbar_init(&S.acc_full[i], 1);
             tc::mbar_init(&S.acc_empty[i], EPI_WARPS);
         }
-        tc::mbar_init(&S.turn[0], 1);
-        tc::mbar_init(&S.turn[1], 1);
         tc::mbar_init(&S.mma_done, 1);
         S.abort = 0;
         tc::fence_mbar_init();
@@ -496,63 +493,64 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
         }
         if (elect_one()) tc::mma_commit(&S.mma_done);
         if (!tc::mbar_wait(&S.mma_done, 0, kWaitNs) && lane == 0) set_status(p.status, MOE_ERR_TIMEOUT);
-    } else if (warp == 2 || warp == 3) {
-        // ---------------- scales: four steps at a time, the two warps in turn.
-        // Both load ahead, but a warp stores its steps only after the other has
-        // stored the ones before: a wait for a stage's parity may be at most one
-        // phase ahead, and steps stored out of order would be two.
-        int it = 0, batch = 0;
-        for (int item = first; item < total; item += step) {
-            const Item m = item_of(p, S, item, split);
-            bool stop = false;
-            for (int base = m.kb0 & ~3; base < m.kb1; base += 4, batch++) {
-                const int lo = max(base, m.kb0), n = min(base + 4, m.kb1) - lo;  // (a part of K may begin within the four)
-                if ((batch & 1) == (warp & 1)) {
-                    uint32_t wv[4][8], xv[MAX_BN / 32][8];
-#pragma unroll
-                    for (int g = 0; g < 4; g++) {
-                        const int row = kSwiglu ? m.n0 + g * 16 + (lane & 15) : m.n0 + g * 32 + lane;
-                        load32(p.w_scales + ((int64_t)m.e * p.w_rows + (kSwiglu && lane >= 16 ? p.N : 0) + row) * p.pitch + base * 8,
-                               row < p.N, wv[g]);
-                    }
-#pragma unroll
-                    for (int g = 0; g < MAX_BN / 32; g++) {
-                        const int r = g * 32 + lane;
-                        load32(p.x_scales + (int64_t)(m.p0 + r) * p.pitch + base * 8, r < m.cnt, xv[g]);
-                    }
-                    if (batch > 0) stop = !warp_wait(S, &S.turn[(batch - 1) & 1], ((batch - 1) >> 1) & 1);
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const int at = it + base + i - lo;
-                        if (base + i < lo || base + i >= lo + n || stop) continue;
-                        const int s = at % p.stages, u = at / p.stages;
-                        if (u > 0 && !warp_wait(S, &S.empty[s], (u - 1) & 1)) {
-                            stop = true;
-                            continue;
-                        }
-                        char *f = sF + s * SF_BYTES;
-#pragma unroll
-                        for (int g = 0; g < 4; g++) {
-                            *reinterpret_cast<uint32_t *>(f + lane * 16 + g * 4) = wv[g][2 * i];
-                            *reinterpret_cast<uint32_t *>(f + 512 + lane * 16 + g * 4) = wv[g][2 * i + 1];
-                        }
-#pragma unroll
-                        for (int g = 0; g < MAX_BN / 32; g++) {
-                            if (g * 32 >= p.bn) break;
-                            char *b = f + 1024 + (g >> 2) * 512 + lane * 16 + (g & 3) * 4;
-                            *reinterpret_cast<uint32_t *>(b) = xv[g][2 * i];
-                            *reinterpret_cast<uint32_t *>(b + 1024) = xv[g][2 * i + 1];
-                        }
-                        tc::fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(&S.full[s]);
-                    }
-                    if (lane == 0) tc::mbar_arrive(&S.turn[batch & 1]);
-                }
-                it += n;
-                if (stop) break;
+    } else if (warp < EPI_WARP0) {
+        // ---------------- scales.  Warp k takes rows 32 g + 8 k + l of each
+        // chunk of 128 (g the lane's low two bits, l the others): its 128 bytes
+        // of the chunk then lie in a row.  Four steps' scales are one load per
+        // row, and the next four are on their way while these are stored.
+        const int k = warp - SF_WARP0, r = (lane & 3) * 32 + k * 8 + (lane >> 2);
+        // (SwiGLU: row r of the tile is 16 of gate, 16 of up in turn)
+        const int wr = kSwiglu ? (r >> 5) * 16 + (r & 15) : r, up = kSwiglu && (r & 16) ? p.N : 0;
+        int item = first, base = 0, it = 0;
+        Item m, mn;
+        uint32_t cur[3][8], nxt[3][8];
+        auto fetch = [&](const Item &q, int b, uint32_t (&v)[3][8]) {
+            load32(p.w_scales + ((int64_t)q.e * p.w_rows + up + q.n0 + wr) * p.pitch + b * 8, q.n0 + wr < p.N, v[0]);
+            load32(p.x_scales + (int64_t)(q.p0 + r) * p.pitch + b * 8, r < q.cnt, v[1]);
+            load32(p.x_scales + (int64_t)(q.p0 + 128 + r) * p.pitch + b * 8, 128 + r < q.cnt, v[2]);
+        };
+        bool ok = item < total;
+        if (ok) {
+            m = item_of(p, S, item, split);
+            base = m.kb0 & ~3;  // (a part of K may begin within the four)
+            fetch(m, base, cur);
+        }
+        while (ok) {
+            // the four steps after these
+            int bn = base + 4;
+            bool more = true;
+            mn = m;
+            if (bn >= m.kb1) {
+                item += step;
+                more = item < total;
+                if (more) mn = item_of(p, S, item, split);
+                bn = mn.kb0 & ~3;
             }
-            if (stop) break;
+            if (more) fetch(mn, bn, nxt);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                if (base + i < m.kb0 || base + i >= m.kb1 || !ok) continue;
+                const int s = it % p.stages, u = it / p.stages;
+                it++;
+                if (u > 0) ok = warp_wait(S, &S.empty[s], (u - 1) & 1);
+                char *f = sF + s * SF_BYTES + k * 128 + lane * 4;
+#pragma unroll
+                for (int c = 0; c < 2; c++) {
+                    *reinterpret_cast<uint32_t *>(f + c * 512) = cur[0][2 * i + c];
+                    *reinterpret_cast<uint32_t *>(f + 1024 + c * 1024) = cur[1][2 * i + c];
+                    if (p.bn > 128) *reinterpret_cast<uint32_t *>(f + 1536 + c * 1024) = cur[2][2 * i + c];
+                }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&S.full[s]);
+            }
+            if (!more) break;
+            m = mn;
+            base = bn;
+#pragma unroll
+            for (int j = 0; j < 3; j++)
+#pragma unroll
+                for (int i = 0; i < 8; i++) cur[j][i] = nxt[j][i];
         }
     } else {
         // ---------------- sums out
@@ -621,6 +619,36 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
     }
 }
 
+// Rows per tile (a multiple of 16, at most MAX_BN).  Several groups: twice the
+// mean, since their sizes are known on the device only; a larger group takes
+// more tiles.
+static int grouped_rows(int rows, int E)
+{
+    const int64_t groups = std::min(E, rows), want = 2 * ((rows + groups - 1) / groups);
+    return (int)std::min<int64_t>(MAX_BN, (want + 31) / 32 * 32);
+}
+
+// One group: the count of equal tiles that takes the fewest rounds of the SMs
+// times the cost of a tile, counted in 128-byte rows moved: a step's rows of
+// both operands (measured: it moves about 0.4 a cycle), and leaving tensor
+// memory (a row's 128 columns cost about as much as eight).
+static int dense_rows(int rows, int n_tiles, int nk, int sms)
+{
+    int best = MAX_BN;
+    int64_t best_cost = INT64_MAX;
+    const int least = (rows + MAX_BN - 1) / MAX_BN;
+    for (int nt = least; nt <= least * 2 + 1; nt++) {
+        const int bn = ((rows + nt - 1) / nt + 15) / 16 * 16;
+        const int64_t rounds = ((int64_t)((rows + bn - 1) / bn) * n_tiles + sms - 1) / sms;
+        const int64_t cost = rounds * ((int64_t)nk * (BM + 24 + bn) + 8 * bn + 400);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = bn;
+        }
+    }
+    return best;
+}
+
 }  // namespace mx
 
 }  // namespace moe
@@ -655,20 +683,16 @@ extern "C" moe_status moe_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_sc
     p.swiglu = swiglu;
     p.offsets = offsets, p.w_scales = w_scales, p.x_scales = x_scales, p.pitch = (p.nk + 3) / 4 * 32;
     p.out = out, p.vec = aligned16(out) && N % 8 == 0, p.status = dev_status;
-    // Rows per tile: what one group needs, twice the mean where there are
-    // several (the groups' sizes are known on the device only).
-    const int64_t groups = std::min(E, rows);
-    const int64_t want = groups == 1 ? rows : 2 * ((rows + groups - 1) / groups);
-    p.bn = (int)std::min<int64_t>(MAX_BN, (want + 31) / 32 * 32);
-    const int stage = A_BYTES + p.bn * (BK / 2) + SF_BYTES;
+    const int sms = sm_count();
+    p.bn = offsets ? grouped_rows(rows, E) : dense_rows(rows, p.n_tiles, p.nk, sms);
+    const int stage = A_BYTES + (p.bn + 31) / 32 * 32 * (BK / 2) + SF_BYTES;
     p.stages = std::min(MAX_STAGES, (200 * 1024) / stage);
     // at most this many items: every group's last row tile may be short
-    const int64_t row_tiles = offsets ? groups + rows / p.bn : (rows + p.bn - 1) / p.bn;
+    const int64_t row_tiles = offsets ? std::min(E, rows) + rows / p.bn : (rows + p.bn - 1) / p.bn;
     const int64_t items = row_tiles * p.n_tiles;
     // (item numbers stay in 32 bits whatever the offsets say)
     MOE_REQUIRE((int64_t)E * ((rows + p.bn - 1) / p.bn) * p.n_tiles <= (1 << 30), "too many tiles (rows=%d N=%d E=%d)", rows,
                 N, E);
-    const int sms = sm_count();
     p.splits = 1;
     while (p.splits < 8 && items * p.splits * 2 <= sms && p.nk >= 2 * p.splits) p.splits *= 2;
     const int64_t grid = p.splits > 1 ? items * p.splits : std::min<int64_t>(items, sms);
