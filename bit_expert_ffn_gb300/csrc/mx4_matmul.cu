@@ -125,9 +125,16 @@ __device__ __forceinline__ Item item_of(const Params &p, const Shared &S, int it
     return it;
 }
 
+// Whether the whole warp sees the phase complete (no waiting).
+__device__ __forceinline__ bool warp_peek(uint64_t *bar, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity));
+}
+
 // A whole warp waits; false for all of it when the time is up or the CTA stops.
 __device__ __forceinline__ bool warp_wait(Shared &S, uint64_t *bar, uint32_t parity)
 {
+    if (warp_peek(bar, parity)) return true;
     const bool ok = tc::mbar_wait(bar, parity, kWaitNs);
     return __all_sync(0xffffffffu, ok && !S.abort);
 }
@@ -429,7 +436,6 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
                     for (int i = 0; i < boxes; i++)
                         tc::tma_load_2d(b + i * 32 * (BK / 2), &mx, x, m.p0 + i * 32, &S.full[s]);
                 }
-                __syncwarp();
                 if (++s == p.stages) s = 0, phase ^= 1;
             }
         }
@@ -483,7 +489,6 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
                     tc::mma_commit(&S.empty[s]);
                     if (kb + 1 == m.kb1) tc::mma_commit(&S.acc_full[acc]);
                 }
-                __syncwarp();
                 if (++s == p.stages) s = 0, phase ^= 1;
             }
         }
