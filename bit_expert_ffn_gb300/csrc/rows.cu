@@ -10,6 +10,13 @@
 namespace moe {
 
 constexpr int kRowThreads = 256;
+// CTAs per SM that the kernels are built for.  combine's grid is that many, and
+// a CTA takes several pieces; dispatch, which mostly writes, is faster with a
+// CTA per eight pieces (32K tokens of 4 KB, ten places each: 220 against 250
+// us), and combine's gradient with some (106 against 113 us at 8192 tokens).
+// combine: more CTAs with a row or two on their way per lane each do better
+// than fewer with four or five (16-bit rows: 64 against 83 us at 8192 tokens).
+constexpr int kDispatchPerSm = 6, kCombinePerSm = 8, kBackPerSm = 4, kBackGrid = 32;
 constexpr int kMaxK = 16;
 
 // inv_perm of a token's slot (lane j of the warp), -1 for left-out pairs; an
@@ -30,7 +37,7 @@ __device__ __forceinline__ int64_t first_tail_row(const int32_t *offsets, int E,
 // A copy, whatever the type: V is the widest unit that row bytes and pointers
 // allow.  Unit of work: kUnroll * 32 V's of one token's row, to its k places.
 template <class V, int kUnroll>
-__global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const V *__restrict__ x, int64_t x_stride, int64_t T,
+__global__ void __launch_bounds__(kRowThreads, kDispatchPerSm) dispatch_kernel(const V *__restrict__ x, int64_t x_stride, int64_t T,
                                                                int row, int k, int E,
                                                                const int32_t *__restrict__ offsets,
                                                                const int32_t *__restrict__ inv, V *__restrict__ out)
@@ -72,7 +79,7 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const V *__restri
 // one rounding at the end.  Unit of work: 256 columns of one token (eight per
 // lane; scalar columns where rows are not 16-byte aligned).
 template <class A, class O, bool kVec>
-__global__ void __launch_bounds__(kRowThreads) combine_kernel(const typename A::T *__restrict__ y, int64_t T, int H,
+__global__ void __launch_bounds__(kRowThreads, kCombinePerSm) combine_kernel(const typename A::T *__restrict__ y, int64_t T, int H,
                                                               int k, const float *__restrict__ w,
                                                               const int32_t *__restrict__ inv,
                                                               typename O::T *__restrict__ out, int accumulate)
@@ -127,11 +134,12 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const typename A::
 // One warp per (token, slot): dy[inv] = w dout[t] and dw = <dout[t], y[inv]>,
 // the dot product in fp32 (lane sums over strided pieces, then a fixed tree).
 template <class A, bool kVec>
-__global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(
+__global__ void __launch_bounds__(kRowThreads, kBackPerSm) combine_backward_kernel(
     const typename A::T *__restrict__ dout, const typename A::T *__restrict__ y, int64_t T, int H, int k, int E,
     const int32_t *__restrict__ offsets, const float *__restrict__ w, const int32_t *__restrict__ inv,
     typename A::T *__restrict__ dy, float *__restrict__ dw)
 {
+    constexpr int kBatch = A::kBytes == 2 ? 4 : 2;  // pieces of both rows on their way per lane
     const int lane = lane_id();
     const int64_t n_pairs = T * k;
     const int64_t w0 = (int64_t)blockIdx.x * (kRowThreads / 32) + warp_id(), wn = (int64_t)gridDim.x * (kRowThreads / 32);
@@ -146,17 +154,27 @@ __global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(
         typename A::T *o = dy + (int64_t)r * H;
         float sum = 0.f;
         if (kVec) {
-#pragma unroll 4
-            for (int c = lane * 8; c < H; c += 256) {
-                float a[8], b[8];
-                A::load8(d + c, a);
-                A::load8(yr + c, b);
+            for (int c0 = lane * 8; c0 < H; c0 += kBatch * 256) {
+                typename A::Raw8 dq[kBatch], yq[kBatch];
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    sum = fmaf(a[i], b[i], sum);
-                    a[i] *= f;
+                for (int i = 0; i < kBatch; i++)
+                    if (c0 + i * 256 < H) {
+                        yq[i] = A::raw8(yr + c0 + i * 256);
+                        dq[i] = A::raw8(d + c0 + i * 256);
+                    }
+#pragma unroll
+                for (int i = 0; i < kBatch; i++) {
+                    if (c0 + i * 256 >= H) break;
+                    float a[8], b[8];
+                    A::unpack8(dq[i], a);
+                    A::unpack8(yq[i], b);
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        sum = fmaf(a[e], b[e], sum);
+                        a[e] *= f;
+                    }
+                    A::store8(o + c0 + i * 256, a);
                 }
-                A::store8(o + c, a);
             }
         } else {
 #pragma unroll 4
@@ -176,10 +194,10 @@ __global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(
     }
 }
 
-static unsigned row_grid(int64_t warps)
+static unsigned row_grid(int64_t warps, int per_sm)
 {
     const int64_t blocks = (warps + kRowThreads / 32 - 1) / (kRowThreads / 32);
-    return (unsigned)std::max<int64_t>(1, std::min<int64_t>(blocks, (int64_t)sm_count() * 8));
+    return (unsigned)std::max<int64_t>(1, std::min<int64_t>(blocks, (int64_t)sm_count() * per_sm));
 }
 
 // 16-byte accesses of eight (or four) elements need aligned rows.
@@ -200,7 +218,8 @@ static void launch_dispatch(const void *x, int64_t stride_bytes, int T, int64_t 
 {
     const int row = (int)(row_bytes / (int64_t)sizeof(V));
     const int64_t units = (int64_t)T * ((row + 127) / 128);
-    dispatch_kernel<V, 4><<<row_grid(units), kRowThreads, 0, s>>>(static_cast<const V *>(x),
+    const unsigned grid = (unsigned)std::min<int64_t>((units + kRowThreads / 32 - 1) / (kRowThreads / 32), INT32_MAX);
+    dispatch_kernel<V, 4><<<grid, kRowThreads, 0, s>>>(static_cast<const V *>(x),
                                                                   stride_bytes / (int64_t)sizeof(V), T, row, k, E,
                                                                   offsets, inv, static_cast<V *>(out));
 }
@@ -209,8 +228,8 @@ static moe_status combine_any(const void *y, moe_dtype dtype, int T, int H, int 
                               const int32_t *inv, void *out, moe_dtype out_dtype, int accumulate, cudaStream_t s,
                               const char *what)
 {
-    const unsigned grid = row_grid((int64_t)T * ((H + 255) / 256));
     const bool vec = vec_rows(dtype, H, y) && vec_rows(out_dtype, H, out);
+    const unsigned grid = row_grid((int64_t)T * ((H + 255) / 256), kCombinePerSm);
     return with_dtype(dtype, [&](auto a) {
         using A = decltype(a);
         auto go = [&](auto o) {
@@ -293,7 +312,7 @@ extern "C" moe_status moe_combine_backward(const void *dout, const void *y, moe_
     MOE_REQUIRE(aligned_to(dout, dtype_bytes(dtype)) && aligned_to(y, dtype_bytes(dtype)) &&
                     aligned_to(dy, dtype_bytes(dtype)),
                 "dout, y and dy must be aligned to their type");
-    const unsigned grid = row_grid((int64_t)T * k);
+    const unsigned grid = row_grid((int64_t)T * k, kBackGrid);
     const bool vec = vec_rows(dtype, H, dout) && vec_rows(dtype, H, y) && vec_rows(dtype, H, dy);
     return with_dtype(dtype, [&](auto a) {
         using A = decltype(a);

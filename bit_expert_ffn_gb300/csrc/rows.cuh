@@ -1,5 +1,6 @@
 // rows.cuh -- element types of activation rows: fp32, bf16 and fp16 values to
-// and from fp32 registers, one at a time or eight (16 or 32 bytes) at once.
+// and from fp32 registers, one at a time or four or eight at once (raw8: eight
+// as they lie, so that several loads fit into registers before any is used).
 #pragma once
 
 #include "common.cuh"
@@ -9,6 +10,14 @@ namespace moe {
 struct F32 {
     using T = float;
     static constexpr int kBytes = 4;
+    struct Raw8 {
+        float4 a, b;
+    };
+    __device__ static Raw8 raw8(const T *p) { return {reinterpret_cast<const float4 *>(p)[0], reinterpret_cast<const float4 *>(p)[1]}; }
+    __device__ static void unpack8(const Raw8 &q, float (&v)[8])
+    {
+        v[0] = q.a.x, v[1] = q.a.y, v[2] = q.a.z, v[3] = q.a.w, v[4] = q.b.x, v[5] = q.b.y, v[6] = q.b.z, v[7] = q.b.w;
+    }
     __device__ static float load(const T *p) { return *p; }
     __device__ static void store(T *p, float v) { *p = v; }
     __device__ static void load8(const T *p, float (&v)[8])
@@ -32,6 +41,8 @@ struct F32 {
 struct Bf16 {
     using T = uint16_t;
     static constexpr int kBytes = 2;
+    using Raw8 = uint4;
+    __device__ static Raw8 raw8(const T *p) { return *reinterpret_cast<const uint4 *>(p); }
     __device__ static float load(const T *p) { return bf16_to_f32(*p); }
     __device__ static void store(T *p, float v) { *p = f32_to_bf16(v); }
     __device__ static void unpack8(uint4 q, float (&v)[8])
@@ -75,6 +86,8 @@ struct Bf16 {
 struct Fp16 {
     using T = uint16_t;
     static constexpr int kBytes = 2;
+    using Raw8 = uint4;
+    __device__ static Raw8 raw8(const T *p) { return *reinterpret_cast<const uint4 *>(p); }
     __device__ static float load(const T *p) { return fp16_to_f32(*p); }
     __device__ static void store(T *p, float v) { *p = __half_as_ushort(__float2half_rn(v)); }
     __device__ static void unpack8(uint4 q, float (&v)[8])
