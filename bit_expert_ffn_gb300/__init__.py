@@ -185,23 +185,26 @@ _BYTES = {MOE_F32: 4, MOE_BF16: 2, MOE_F16: 2}
 
 def _packed(t, name, n, size):
     """The pointer of a packed buffer of at least n elements of `size` bytes (a tensor), or of a raw address."""
-    if t is None or isinstance(t, int):
+    if t.__class__ is int or t is None:
         return t
-    if not t.is_contiguous() or t.element_size() != size or t.numel() < n:
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{name} must be a packed tensor of at least {n} elements of {size} bytes "
-                                            f"(got {tuple(t.shape)}, strides {t.stride()}, {t.dtype})")
-    return t.data_ptr() if n else None
+    if t.is_contiguous() and t.element_size() == size and t.numel() >= n:
+        return t.data_ptr() if n else None
+    raise MoeError(MOE_ERR_INVALID_ARG, f"{name} must be a packed tensor of at least {n} elements of {size} bytes "
+                                        f"(got {tuple(t.shape)}, strides {t.stride()}, {t.dtype})")
 
 
 def _rows(t, name, n, cols, dtype):
     """Pointer and row stride of n rows of `cols` elements: a packed tensor, a 2D one whose rows are packed (stride 0
     repeats one row), or a raw address of packed rows."""
-    if t is None or isinstance(t, int):
+    if t.__class__ is int or t is None:
         return t, cols
-    if t.dim() == 2 and t.element_size() == _BYTES.get(dtype) and t.shape[0] >= n and t.shape[1] == cols and (
-            t.stride(1) == 1 or cols == 1):
+    size = _BYTES.get(dtype, 0)
+    if t.is_contiguous() and t.element_size() == size and t.numel() >= n * cols:
+        return t.data_ptr() if n else None, cols
+    if t.dim() == 2 and t.element_size() == size and t.shape[0] >= n and t.shape[1] == cols and (t.stride(1) == 1
+                                                                                                or cols == 1):
         return (t.data_ptr(), t.stride(0) if n > 1 else cols) if n else (None, cols)
-    return _packed(t, name, n * cols, _BYTES.get(dtype, 0)), cols
+    return _packed(t, name, n * cols, size), cols
 
 
 _raw_stream = None  # torch's current stream handle of a device, and the current device, once a GPU is there
@@ -366,7 +369,7 @@ def moe_selftest_barrier(extra_arrivals, timeout_ms, ws, ws_bytes, dev_status=No
 def moe_dispatch(x, dtype, T, H, k, E, offsets, inv_perm, out, stream=None):
     """out[inv_perm[t, j]] = x[t]; rows of no pair are zero.  x: [T][H], packed rows at any row stride."""
     xp, xs = _rows(x, "x", T, H, dtype)
-    _check(lib().moe_dispatch(xp, dtype, xs, T, H, k, E, _packed(offsets, "offsets", E + 1, 4),
+    _check((_lib or load()).moe_dispatch(xp, dtype, xs, T, H, k, E, _packed(offsets, "offsets", E + 1, 4),
                               _packed(inv_perm, "inv_perm", T * k, 4), _packed(out, "out", T * k * H, _BYTES.get(dtype, 0)),
                               _stream(stream)), "moe_dispatch")
 
@@ -374,14 +377,14 @@ def moe_dispatch(x, dtype, T, H, k, E, offsets, inv_perm, out, stream=None):
 def moe_dispatch_backward(drows, dtype, T, H, k, inv_perm, dx, stream=None):
     """dx[t] = sum_j drows[inv_perm[t, j]]."""
     b = _BYTES.get(dtype, 0)
-    _check(lib().moe_dispatch_backward(_packed(drows, "drows", T * k * H, b), dtype, T, H, k,
+    _check((_lib or load()).moe_dispatch_backward(_packed(drows, "drows", T * k * H, b), dtype, T, H, k,
                                        _packed(inv_perm, "inv_perm", T * k, 4), _packed(dx, "dx", T * H, b),
                                        _stream(stream)), "moe_dispatch_backward")
 
 
 def moe_combine(y, dtype, T, H, k, w, inv_perm, out, out_dtype=MOE_F32, accumulate=False, stream=None):
     """out[t] (+)= sum_j w[t, j] * y[inv_perm[t, j]]."""
-    _check(lib().moe_combine(_packed(y, "y", T * k * H, _BYTES.get(dtype, 0)), dtype, T, H, k, _packed(w, "w", T * k, 4),
+    _check((_lib or load()).moe_combine(_packed(y, "y", T * k * H, _BYTES.get(dtype, 0)), dtype, T, H, k, _packed(w, "w", T * k, 4),
                              _packed(inv_perm, "inv_perm", T * k, 4),
                              _packed(out, "out", T * H, _BYTES.get(out_dtype, 0)), out_dtype, int(accumulate),
                              _stream(stream)), "moe_combine")
@@ -390,7 +393,7 @@ def moe_combine(y, dtype, T, H, k, w, inv_perm, out, out_dtype=MOE_F32, accumula
 def moe_combine_backward(dout, y, dtype, T, H, k, E, offsets, w, inv_perm, dy, dw, stream=None):
     """dy[inv_perm[t, j]] = w[t, j] * dout[t], dw[t, j] = <dout[t], y[inv_perm[t, j]]>."""
     b = _BYTES.get(dtype, 0)
-    _check(lib().moe_combine_backward(_packed(dout, "dout", T * H, b), _packed(y, "y", T * k * H, b), dtype, T, H, k, E,
+    _check((_lib or load()).moe_combine_backward(_packed(dout, "dout", T * H, b), _packed(y, "y", T * k * H, b), dtype, T, H, k, E,
                                       _packed(offsets, "offsets", E + 1, 4), _packed(w, "w", T * k, 4),
                                       _packed(inv_perm, "inv_perm", T * k, 4), _packed(dy, "dy", T * k * H, b),
                                       _packed(dw, "dw", T * k, 4), _stream(stream)), "moe_combine_backward")
@@ -401,7 +404,7 @@ def moe_combine_backward(dout, y, dtype, T, H, k, E, offsets, w, inv_perm, dy, d
 def moe_mx4_size(rows: int, cols: int):
     """(bytes of codes, bytes of scales) of a [rows][cols] matrix; cols a multiple of 32."""
     cb, sb = ctypes.c_size_t(0), ctypes.c_size_t(0)
-    _check(lib().moe_mx4_size(rows, cols, ctypes.byref(cb), ctypes.byref(sb)), "moe_mx4_size")
+    _check((_lib or load()).moe_mx4_size(rows, cols, ctypes.byref(cb), ctypes.byref(sb)), "moe_mx4_size")
     return cb.value, sb.value
 
 
@@ -416,14 +419,14 @@ def moe_mx4_quantise(x, dtype, rows, cols, codes, scales, dev_status=None, strea
         x = x.view(-1, cols) if x.shape[-1] == cols else x
     xp, xs = _rows(x, "x", rows, cols, dtype)
     cp, sp = _mx4(codes, scales, "", rows, cols)
-    _check(lib().moe_mx4_quantise(xp, dtype, xs, rows, cols, cp, sp, _ptr(dev_status), _stream(stream)),
+    _check((_lib or load()).moe_mx4_quantise(xp, dtype, xs, rows, cols, cp, sp, _ptr(dev_status), _stream(stream)),
            "moe_mx4_quantise")
 
 
 def moe_mx4_dequantise(codes, scales, rows, cols, out, dtype=MOE_BF16, stream=None):
     """The values that codes and scales stand for."""
     cp, sp = _mx4(codes, scales, "", rows, cols)
-    _check(lib().moe_mx4_dequantise(cp, sp, rows, cols, _packed(out, "out", rows * cols, _BYTES.get(dtype, 0)), dtype,
+    _check((_lib or load()).moe_mx4_dequantise(cp, sp, rows, cols, _packed(out, "out", rows * cols, _BYTES.get(dtype, 0)), dtype,
                                     _stream(stream)), "moe_mx4_dequantise")
 
 
@@ -432,7 +435,7 @@ def moe_mx4_matmul(w_codes, w_scales, E, N, K, x_codes, x_scales, rows, offsets,
     """out[p] = x[p] W_e^T (or silu(gate) * up of it) for the rows p of each group e; offsets None: one group (E = 1)."""
     wc, ws = _mx4(w_codes, w_scales, "w_", E * N * (2 if epilogue == MOE_MX4_SWIGLU else 1), K)
     xc, xs = _mx4(x_codes, x_scales, "x_", rows, K)
-    _check(lib().moe_mx4_matmul(wc, ws, E, N, K, xc, xs, rows, _packed(offsets, "offsets", E + 1, 4),
+    _check((_lib or load()).moe_mx4_matmul(wc, ws, E, N, K, xc, xs, rows, _packed(offsets, "offsets", E + 1, 4),
                                 _packed(out, "out", rows * N, _BYTES.get(out_dtype, 0)), out_dtype, epilogue,
                                 _ptr(dev_status), _stream(stream)), "moe_mx4_matmul")
 
@@ -447,14 +450,14 @@ def moe_block_norm(x, res_dtype, b, dtype, T, H, w_post, w_pre, gate, gate_kind,
     """y = x + alpha * gate * w_post * rmsnorm(b), u = w_pre * rmsnorm(y).  x and b: packed rows at any row stride."""
     xp, xs = _rows(x, "x", T, H, res_dtype)
     bp, bs = _rows(b, "b", T, H, dtype)
-    _check(lib().moe_block_norm(xp, res_dtype, xs, bp, dtype, bs, T, H, _packed(w_post, "w_post", H, 4),
+    _check((_lib or load()).moe_block_norm(xp, res_dtype, xs, bp, dtype, bs, T, H, _packed(w_post, "w_post", H, 4),
                                 _packed(w_pre, "w_pre", H, 4), _packed(gate, "gate", _gate_size(gate_kind, T, H), 4),
                                 gate_kind, alpha, eps, _packed(y, "y", T * H, _BYTES.get(res_dtype, 0)),
                                 _packed(u, "u", T * H, _BYTES.get(dtype, 0)), _stream(stream)), "moe_block_norm")
 
 
 def moe_block_norm_backward_workspace_size(T, H, gate_kind=MOE_GATE_NONE):
-    return _size(lib().moe_block_norm_backward_workspace_size, T, H, gate_kind)
+    return _size((_lib or load()).moe_block_norm_backward_workspace_size, T, H, gate_kind)
 
 
 def moe_block_norm_backward(x, res_dtype, b, dtype, T, H, w_post, w_pre, gate, gate_kind, alpha, eps, dy, du, dx, db,
@@ -463,7 +466,7 @@ def moe_block_norm_backward(x, res_dtype, b, dtype, T, H, w_post, w_pre, gate, g
     xp, xs = _rows(x, "x", T, H, res_dtype)
     bp, bs = _rows(b, "b", T, H, dtype)
     rb, ab, n = _BYTES.get(res_dtype, 0), _BYTES.get(dtype, 0), _gate_size(gate_kind, T, H)
-    _check(lib().moe_block_norm_backward(
+    _check((_lib or load()).moe_block_norm_backward(
         xp, res_dtype, xs, bp, dtype, bs, T, H, _packed(w_post, "w_post", H, 4), _packed(w_pre, "w_pre", H, 4),
         _packed(gate, "gate", n, 4), gate_kind, alpha, eps, _packed(dy, "dy", T * H, rb), _packed(du, "du", T * H, ab),
         _packed(dx, "dx", T * H, rb), _packed(db, "db", T * H, ab), _packed(dw_post, "dw_post", H, 4),

@@ -55,7 +55,9 @@ struct Params {
     int E, N, w_rows, rows;      // w_rows: weight rows per expert (N or 2N)
     int nk, n_mma;               // steps, and MMAs of K = 64, over the whole K
     int n_tiles, bn, stages, splits, swiglu;
+    uint32_t tiles_m, tiles_shift;  // item / n_tiles = (item * tiles_m high) >> tiles_shift (tiles_m 0: n_tiles is 1)
     const int32_t *offsets;      // NULL: one group of all rows
+    int total;                   // its items
     const uint8_t *w_scales, *x_scales;
     int pitch;                   // bytes of scales per row, a multiple of 32: four steps
     void *out;
@@ -99,23 +101,29 @@ struct Item {
 __device__ __forceinline__ Item item_of(const Params &p, const Shared &S, int item, int split)
 {
     Item it;
-    const int lane = lane_id(), tt = item / p.n_tiles;
+    const int lane = lane_id();
+    const int tt = p.tiles_m ? (int)(__umulhi((uint32_t)item, p.tiles_m) >> p.tiles_shift) : item;
     it.n0 = (item - tt * p.n_tiles) * (p.swiglu ? BM / 2 : BM);
-    int e = __popc(__ballot_sync(0xffffffffu, lane * 32 < p.E && S.tile0[min(lane * 32, p.E)] <= tt)) - 1;
-    e *= 32;
-    e += __popc(__ballot_sync(0xffffffffu, e + lane < p.E && S.tile0[min(e + lane, p.E)] <= tt)) - 1;
-    it.e = e;
-    const int cnt = S.count[e], t0 = S.tile0[e], nt = S.tile0[e + 1] - t0;
-    it.p0 = S.start[e];
-    it.cnt = cnt;
-    if (nt > 1) {
-        const int w = ((cnt + nt - 1) / nt + 15) & ~15;
-        it.p0 += (tt - t0) * w;
-        it.cnt = min(w, cnt - (tt - t0) * w);
+    if (!p.offsets) {  // bn is a tile's rows as they are
+        it.e = 0;
+        it.p0 = tt * p.bn;
+        it.cnt = min(p.bn, p.rows - it.p0);
+    } else {
+        int e = __popc(__ballot_sync(0xffffffffu, lane * 32 < p.E && S.tile0[min(lane * 32, p.E)] <= tt)) - 1;
+        e *= 32;
+        e += __popc(__ballot_sync(0xffffffffu, e + lane < p.E && S.tile0[min(e + lane, p.E)] <= tt)) - 1;
+        const int cnt = S.count[e], t0 = S.tile0[e], nt = S.tile0[e + 1] - t0;
+        it.p0 = S.start[e];
+        it.cnt = cnt;
+        if (nt > 1) {
+            const int w = ((cnt + nt - 1) / nt + 15) & ~15;
+            it.p0 += (tt - t0) * w;
+            it.cnt = min(w, cnt - (tt - t0) * w);
+        }
+        it.e = uniform(e);
+        it.p0 = uniform(it.p0);
+        it.cnt = uniform(it.cnt);
     }
-    it.e = uniform(it.e);
-    it.p0 = uniform(it.p0);
-    it.cnt = uniform(it.cnt);
     it.kb0 = 0;
     it.kb1 = p.nk;
     if (p.splits > 1) {
@@ -369,11 +377,11 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
     }
     if (warp == THREADS / 32 - 1) tc::tmem_alloc(&S.tmem, 512);
     // row tiles before each expert: four experts per thread, then a scan
-    if (threadIdx.x < MAX_E / 4) {
+    if (p.offsets && threadIdx.x < MAX_E / 4) {
         int off[5], n[4], sum = 0;
         const int e0 = threadIdx.x * 4;
 #pragma unroll
-        for (int i = 0; i < 5; i++) off[i] = p.offsets && e0 + i <= p.E ? __ldg(p.offsets + e0 + i) : (e0 + i ? p.rows : 0);
+        for (int i = 0; i < 5; i++) off[i] = e0 + i <= p.E ? __ldg(p.offsets + e0 + i) : 0;
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             // both ends clipped first, so that no offsets lead out of the rows
@@ -408,7 +416,7 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
     tc::tc_fence_after();
     const uint32_t tmem = (uint32_t)uniform((int)S.tmem);
     // (a cluster that splits K takes one item; the grid holds them all)
-    const int tiles = uniform(S.tile0[p.E]) * p.n_tiles;
+    const int tiles = p.offsets ? uniform(S.tile0[p.E]) * p.n_tiles : p.total;
     const int total = p.splits > 1 ? min(tiles, step) : tiles;
 
     if (warp == 0) {
@@ -698,6 +706,13 @@ extern "C" moe_status moe_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_sc
     // (item numbers stay in 32 bits whatever the offsets say)
     MOE_REQUIRE((int64_t)E * ((rows + p.bn - 1) / p.bn) * p.n_tiles <= (1 << 30), "too many tiles (rows=%d N=%d E=%d)", rows,
                 N, E);
+    p.total = (int)items;
+    uint32_t sh = 0;  // as for the rows of a matrix's blocks: items stay below 2^31
+    while ((1 << sh) < p.n_tiles) sh++;
+    if (sh > 0) {
+        p.tiles_m = (uint32_t)((1ull << (31 + sh)) / p.n_tiles + 1);
+        p.tiles_shift = sh - 1;
+    }
     p.splits = 1;
     while (p.splits < 8 && items * p.splits * 2 <= sms && p.nk >= 2 * p.splits) p.splits *= 2;
     const int64_t grid = p.splits > 1 ? items * p.splits : std::min<int64_t>(items, sms);
