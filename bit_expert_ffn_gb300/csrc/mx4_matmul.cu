@@ -40,7 +40,7 @@ namespace mx {
 constexpr int BM = 128;            // weight rows per tile
 constexpr int BK = 256;            // K per step
 constexpr int MAX_BN = 224;        // rows per tile: two accumulators and the scales fill tensor memory
-constexpr int MAX_STAGES = 12;
+constexpr int MAX_STAGES = 12, MAX_STAGE_BYTES = 200 * 1024;
 constexpr int A_BYTES = BM * BK / 2;
 constexpr int SF_BYTES = 2 * 512 + 4 * 512;  // scales of a step: weights, then rows (two chunks of 128 rows)
 constexpr int SF_COL = 2 * MAX_BN;           // tensor memory columns of the scales (two sets of 32)
@@ -699,7 +699,7 @@ extern "C" moe_status moe_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_sc
     const int sms = sm_count();
     p.bn = offsets ? grouped_rows(rows, E) : dense_rows(rows, p.n_tiles, p.nk, sms);
     const int stage = A_BYTES + (p.bn + 31) / 32 * 32 * (BK / 2) + SF_BYTES;
-    p.stages = std::min(MAX_STAGES, (200 * 1024) / stage);
+    p.stages = std::min(MAX_STAGES, MAX_STAGE_BYTES / stage);
     // at most this many items: every group's last row tile may be short
     const int64_t row_tiles = offsets ? std::min(E, rows) + rows / p.bn : (rows + p.bn - 1) / p.bn;
     const int64_t items = row_tiles * p.n_tiles;
@@ -736,7 +736,8 @@ extern "C" moe_status moe_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_sc
     return with_dtype(out_dtype, [&](auto o) {
         using O = decltype(o);
         auto fn = swiglu ? mx4_matmul_kernel<O, true> : mx4_matmul_kernel<O, false>;
-        MOE_CUDA_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+        // (the most that any call takes: calls of several threads do not undo each other's)
+        MOE_CUDA_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_STAGE_BYTES + 1024));
         MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, fn, p, mw, mxm));
         return check_launch("mx4_matmul");
     });

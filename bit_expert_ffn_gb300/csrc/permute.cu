@@ -251,8 +251,8 @@ extern "C" moe_status moe_permute(const int32_t *ids, int T, int k, int E, int32
     }
     MOE_REQUIRE(ids && perm && inv_perm, "NULL pointer");
     if (n <= kPermSmallMax) {
-        // as many runs of 32 or more pairs as 48 KB of counters hold
-        const int most = (int)std::min<int64_t>(std::min(32, 12288 / E), (n + 31) / 32);
+        // as many runs of 32 or more pairs as 48,000 bytes of counters hold
+        const int most = (int)std::min<int64_t>(std::min(32, 12000 / E), (n + 31) / 32);
         const int seg = (int)((n + most * 32 - 1) / (most * 32)) * 32;
         const int warps = (int)((n + seg - 1) / seg);
         permute_small_kernel<<<1, 1024, (size_t)warps * E * sizeof(int32_t), s>>>(ids, (int)n, E, warps, seg, offsets, perm,

@@ -205,8 +205,8 @@ static bool vec_rows(moe_dtype t, int H, const void *p) { return aligned16(p) &&
 
 static moe_status check_rows(int T, int H, int k, moe_dtype dtype)
 {
-    MOE_REQUIRE(T >= 0 && H >= 1 && k >= 1 && k <= kMaxK, "T >= 0, H >= 1 and 1 <= k <= %d (got T=%d H=%d k=%d)", kMaxK,
-                T, H, k);
+    MOE_REQUIRE(T >= 0 && H >= 1 && H <= (1 << 24) && k >= 1 && k <= kMaxK,
+                "T >= 0, H in [1, 2^24] and 1 <= k <= %d (got T=%d H=%d k=%d)", kMaxK, T, H, k);
     MOE_REQUIRE((int64_t)T * k <= INT32_MAX, "T*k too large (T=%d k=%d)", T, k);
     MOE_REQUIRE(dtype_ok(dtype), "dtype must be MOE_F32, MOE_BF16 or MOE_F16 (got %d)", (int)dtype);
     return MOE_OK;

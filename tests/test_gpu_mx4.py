@@ -224,6 +224,24 @@ def test_bad_offsets_are_clipped_and_reported(moe):
         assert bool((out[rows * N:] == 0).all())
 
 
+def test_products_on_several_streams(moe):
+    rng = np.random.default_rng(18)
+    cases = [product(rng, 1, 700, 1024, None, 300, torch.float32, False), product(rng, 1, 256, 4096, None, 3, torch.float32, False)]
+    sizes = [(1, 700, 1024, 300), (1, 256, 4096, 3)]
+    torch.cuda.synchronize()
+    outs, streams = [], [torch.cuda.Stream() for _ in range(4)]
+    for i in range(24):
+        (wc, ws, xc, xs), want = cases[i % 2]
+        E, N, K, rows = sizes[i % 2]
+        with torch.cuda.stream(streams[i % 4]):
+            o = torch.empty_like(want)
+            m.moe_mx4_matmul(wc, ws, E, N, K, xc, xs, rows, None, o)
+        outs.append((o, want))
+    torch.cuda.synchronize()
+    for o, want in outs:
+        assert torch.equal(o, want)
+
+
 def test_captured_in_a_graph(moe):
     rng = np.random.default_rng(16)
     rows, N, K = 12, 256, 512

@@ -190,6 +190,22 @@ def test_same_bits_every_time_and_on_another_stream(moe):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T,k,E", [(1, 1, 1), (3, 2, 1024), (32, 16, 1024), (256, 16, 1024), (409, 10, 1024), (410, 10, 1000),
+                                   (1365, 3, 375), (1366, 3, 375), (4096, 1, 7), (5000, 3, 33)])
+def test_sort_of_the_pairs(moe, T, k, E):
+    """The sort that the rows go by, at the sizes where its runs and chunks change, with pairs left out."""
+    rng = np.random.default_rng(T * k + E)
+    ids = rng.integers(0, E, (T, k)).astype(np.int32)
+    ids[rng.random((T, k)) < 0.1] = -1
+    off, perm, inv = (torch.full((n,), -7, dtype=torch.int32, device=DEV) for n in (E + 1, T * k, T * k))
+    nb = m.moe_permute_workspace_size(T, k, E)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    m.moe_permute(dev(ids), T, k, E, off, perm, inv, torch.empty(max(nb, 1), dtype=torch.uint8, device=DEV), nb, st)
+    assert m.moe_check_status(st) == m.MOE_OK
+    for got, want in zip((off, perm, inv), R.sorted_pairs(ids, E)):
+        assert np.array_equal(got.cpu().numpy(), want)
+
+
 def test_no_tokens(moe):
     m.moe_dispatch(torch.empty(0, 8, device=DEV), m.MOE_F32, 0, 8, 2, 4, torch.zeros(5, dtype=torch.int32, device=DEV),
                    torch.empty(0, dtype=torch.int32, device=DEV), torch.empty(0, 8, device=DEV))
