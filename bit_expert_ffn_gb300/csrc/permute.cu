@@ -21,10 +21,15 @@ __device__ void place_pairs(const int32_t *__restrict__ ids, int64_t f0, int64_t
 {
     int lane = lane_id();
     unsigned lt = (1u << lane) - 1u;
+    // the ids of the next two rounds are on their way
+    auto at = [&](int64_t f) { return f < f1 ? ids[f] : -1; };
+    int id0 = at(f0 + lane), id1 = at(f0 + 32 + lane);
     for (int64_t base = f0; base < f1; base += 32) {
         int64_t f = base + lane;
         bool in = f < f1;
-        int id = in ? ids[f] : -1;
+        const int id = id0;
+        id0 = id1;
+        id1 = at(f + 64);
         bool valid = in && id >= 0 && id < E;
         int key = valid ? id : (in ? -1 : -2);  // invalid lanes never match a valid id
         unsigned m = __match_any_sync(0xffffffffu, key);
