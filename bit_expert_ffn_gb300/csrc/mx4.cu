@@ -85,6 +85,8 @@ __global__ void __launch_bounds__(kMxThreads) mx4_quantise_kernel(const typename
                                                                   Blocks n, uint8_t *__restrict__ codes,
                                                                   uint8_t *__restrict__ scales, int32_t *status)
 {
+    // A kernel that is launched to overlap this one (the product) may set itself up; it waits for the codes.
+    asm volatile("griddepcontrol.launch_dependents;");
     // (the four threads of a block are in or out together)
     const uint32_t b0 = blockIdx.x * (kMxThreads / 4 * kQuantPieces) + threadIdx.x / 4, lane4 = threadIdx.x & 3;
     typename A::Raw8 q[kQuantPieces];

@@ -376,6 +376,9 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
         tc::tma_prefetch_desc(&mx);
     }
     if (warp == THREADS / 32 - 1) tc::tmem_alloc(&S.tmem, 512);
+    // (launched while the kernel before it may still run: nothing above reads what that one writes)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
     // row tiles before each expert: four experts per thread, then a scan
     if (p.offsets && threadIdx.x < MAX_E / 4) {
         int off[5], n[4], sum = 0;
@@ -727,12 +730,15 @@ extern "C" moe_status moe_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_sc
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = to_cuda(stream);
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)p.splits;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    // The set-up overlaps the end of the kernel before (as a rule the one that quantised the rows).
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)p.splits;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = p.splits > 1 ? 1 : 0;
+    cfg.numAttrs = p.splits > 1 ? 2 : 1;
     return with_dtype(out_dtype, [&](auto o) {
         using O = decltype(o);
         auto fn = swiglu ? mx4_matmul_kernel<O, true> : mx4_matmul_kernel<O, false>;
