@@ -133,6 +133,18 @@ __device__ __forceinline__ Item item_of(const Params &p, const Shared &S, int it
     return it;
 }
 
+// Whether the phase is complete now (try_wait may sleep for microseconds).
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Whether the whole warp sees the phase complete (no waiting).
 __device__ __forceinline__ bool warp_peek(uint64_t *bar, uint32_t parity)
 {
@@ -476,10 +488,15 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
             const int n16 = (m.cnt + 15) & ~15;
             const uint32_t d = tmem + (uint32_t)(acc * MAX_BN);
             const uint32_t id0 = idesc_mxf4(n16, 0), id2 = idesc_mxf4(n16, 2);
+            bool ready = mbar_test(&S.full[s], phase);
             for (int kb = m.kb0; kb < m.kb1; kb++, it++) {
-                ok = warp_wait(S, &S.full[s], phase);
+                if (!__all_sync(0xffffffffu, ready)) ok = warp_wait(S, &S.full[s], phase);
                 if (!ok) break;
                 tc::tc_fence_after();
+                // (the next step's answer comes while this one's instructions are issued)
+                const int sn = s + 1 == p.stages ? 0 : s + 1;
+                const uint32_t phase_n = sn ? phase : phase ^ 1;
+                ready = mbar_test(&S.full[sn], phase_n);
                 if (elect_one()) {
                     const uint32_t sfa = tmem + SF_COL + (it & 1) * 32, sfb = sfa + 8;
                     const uint32_t f = tc::smem_u32(sF + s * SF_BYTES);
@@ -500,7 +517,8 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
                     tc::mma_commit(&S.empty[s]);
                     if (kb + 1 == m.kb1) tc::mma_commit(&S.acc_full[acc]);
                 }
-                if (++s == p.stages) s = 0, phase ^= 1;
+                s = sn;
+                phase = phase_n;
             }
         }
         if (!ok && lane == 0) {
@@ -665,6 +683,25 @@ static int dense_rows(int rows, int n_tiles, int nk, int sms)
     return best;
 }
 
+// CTAs per item.  A step takes some 0.29 us where little else runs; adding the
+// parts takes 1.8 us and 0.025 us per row.  (One row, 2048 columns: K = 2048
+// takes 5.0 us whole and 5.1 in four parts, K = 8192 11.9 and 7.7; in eight, 16
+// items take 8.7, since a cluster of eight needs its SMs in one group of them
+// and they are not all there at once.)
+static int split_k(int64_t items, int nk, int rows, int sms)
+{
+    int best = 1, best_cost = 29 * nk;
+    for (int s = 2; s <= 8 && s <= nk; s *= 2) {
+        if (items * s > (s < 8 ? sms - 24 : sms - 56)) break;
+        const int cost = 29 * ((nk + s - 1) / s) + 180 + 5 * rows / 2;
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
 }  // namespace mx
 
 }  // namespace moe
@@ -716,8 +753,7 @@ extern "C" moe_status moe_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_sc
         p.tiles_m = (uint32_t)((1ull << (31 + sh)) / p.n_tiles + 1);
         p.tiles_shift = sh - 1;
     }
-    p.splits = 1;
-    while (p.splits < 8 && items * p.splits * 2 <= sms && p.nk >= 2 * p.splits) p.splits *= 2;
+    p.splits = split_k(items, p.nk, std::min(p.bn, rows), sms);
     const int64_t grid = p.splits > 1 ? items * p.splits : std::min<int64_t>(items, sms);
     const size_t smem = (size_t)p.stages * stage + 1024;
     CUtensorMap mw, mxm;
