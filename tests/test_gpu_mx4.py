@@ -224,6 +224,34 @@ def test_bad_offsets_are_clipped_and_reported(moe):
         assert bool((out[rows * N:] == 0).all())
 
 
+def test_outputs_past_32_bits(moe):
+    """More than 2^31 values out (and in), the last rows against the same rows alone."""
+    rows, N, K = 1_060_000, 2050, 32
+    rng = np.random.default_rng(19)
+    wc, ws = [dev(a) for a in R.pack(rng.integers(0, 16, (N, K)).astype(np.uint8), rng.integers(125, 130, (N, 1)).astype(np.uint8))]
+    x = torch.randn(rows, K, device=DEV)
+    cb, sb = m.moe_mx4_size(rows, K)
+    xc, xs = torch.empty(rows, cb // rows, dtype=torch.uint8, device=DEV), torch.empty(rows, sb // rows, dtype=torch.uint8, device=DEV)
+    m.moe_mx4_quantise(x, m.MOE_F32, rows, K, xc, xs)
+    out = torch.empty(rows, N, dtype=torch.bfloat16, device=DEV)
+    m.moe_mx4_matmul(wc, ws, 1, N, K, xc, xs, rows, None, out, m.MOE_BF16)
+    assert out.numel() > 2 ** 31
+    for a in (0, 524_288, rows - 40):
+        one = torch.empty(40, N, dtype=torch.bfloat16, device=DEV)
+        m.moe_mx4_matmul(wc, ws, 1, N, K, xc[a:a + 40].contiguous(), xs[a:a + 40].contiguous(), 40, None, one, m.MOE_BF16)
+        assert torch.equal(out[a:a + 40], one)
+    wide = torch.empty(rows, 2048, dtype=torch.bfloat16, device=DEV)  # quantise and back past 2^31 values
+    wide[:] = out[:, :2048]
+    cb, sb = m.moe_mx4_size(rows, 2048)
+    c, s = torch.empty(cb, dtype=torch.uint8, device=DEV), torch.empty(sb, dtype=torch.uint8, device=DEV)
+    m.moe_mx4_quantise(wide, m.MOE_BF16, rows, 2048, c, s)
+    back = torch.empty_like(wide)
+    m.moe_mx4_dequantise(c, s, rows, 2048, back)
+    for a in (0, rows - 8):
+        code, byte = R.quantise(R.f64(wide[a:a + 8]))
+        assert np.array_equal(R.f64(back[a:a + 8]), R.values(code, byte))
+
+
 def test_products_on_several_streams(moe):
     rng = np.random.default_rng(18)
     cases = [product(rng, 1, 700, 1024, None, 300, torch.float32, False), product(rng, 1, 256, 4096, None, 3, torch.float32, False)]
