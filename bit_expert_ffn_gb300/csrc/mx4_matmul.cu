@@ -28,6 +28,7 @@
 //
 // Every wait is bounded: after about 2 s the CTA records MOE_ERR_TIMEOUT and
 // stops.
+#include "cluster.cuh"
 #include "dense_tc.cuh"
 #include "rows.cuh"
 #include "tc.cuh"
@@ -159,29 +160,6 @@ __device__ __forceinline__ bool warp_wait(Shared &S, uint64_t *bar, uint32_t par
     return __all_sync(0xffffffffu, ok && !S.abort);
 }
 
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
-}
-
-// The float at the same shared-memory address in CTA `rank` of the cluster.
-__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank)
-{
-    float v;
-    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-                 : "=f"(v)
-                 : "r"(addr), "r"(rank)
-                 : "memory");
-    return v;
-}
-
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar)
 {
     asm volatile(
@@ -219,13 +197,13 @@ __device__ __forceinline__ uint32_t idesc_mxf4(int n, uint32_t id)
            (id << 29);
 }
 
-// silu(g) u.  With t = e^-|g| <= 1 nothing overflows; 16-bit outputs take the
-// fast exponential and quotient (some 2^-21 relative for |g| < 8).
+// silu(g) u.  With t = e^-|g| <= 1 nothing overflows, and the quotient's
+// divisor lies in [1, 2], where the fast one is within 2 ulp.  16-bit outputs take
+// the fast exponential too (some 2^-21 relative for |g| < 8).
 template <class O>
 __device__ __forceinline__ float swiglu(float g, float u)
 {
-    if (O::kBytes == 4) return g / (1.0f + expf(-g)) * u;
-    const float t = __expf(-fabsf(g)), r = __fdividef(1.0f, 1.0f + t);
+    const float t = O::kBytes == 4 ? expf(-fabsf(g)) : __expf(-fabsf(g)), r = __fdividef(1.0f, 1.0f + t);
     return g * (g >= 0.f ? r : t * r) * u;
 }
 
@@ -302,34 +280,37 @@ __device__ __forceinline__ void write_rows(const Params &p, const Item &m, int q
 #pragma unroll
         for (int i = 0; i < 8; i++) a[i] = swiglu<O>(a[i], b[i]);
     }
+    // (fp32 with SwiGLU: 16 columns are 64 bytes, a row of the staging block with 16 bytes between)
+    constexpr int P = kSwiglu && O::kBytes == 2 ? 48 : STAGE_PITCH;
     if (O::kBytes == 4) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const int row = (i >> 2) * 8 + 2 * (lane & 3) + (i & 1), n = n0 + lane / 4 + (i & 2) * 4;
-            if (row < rows && n < p.N) O::store(out + (int64_t)row * p.N + n, a[i]);
-        }
-        return;
+        for (int i = 0; i < 8; i++)
+            *reinterpret_cast<float *>(stage + ((i >> 2) * 8 + 2 * (lane & 3) + (i & 1)) * P + (lane / 4 + (i & 2) * 4) * 4) = a[i];
+    } else {
+        const uint32_t base = tc::smem_u32(stage) + ((lane >> 4) * 8 + (lane & 7)) * P + ((lane >> 3) & 1) * 16;
+        stmatrix_x4_trans(base, pack2<O>(a[0], a[1]), pack2<O>(a[2], a[3]), pack2<O>(a[4], a[5]), pack2<O>(a[6], a[7]));
+        if (!kSwiglu)
+            stmatrix_x4_trans(base + 32, pack2<O>(b[0], b[1]), pack2<O>(b[2], b[3]), pack2<O>(b[4], b[5]), pack2<O>(b[6], b[7]));
     }
-    constexpr int P = kSwiglu ? 48 : STAGE_PITCH;
-    const uint32_t base = tc::smem_u32(stage) + ((lane >> 4) * 8 + (lane & 7)) * P + ((lane >> 3) & 1) * 16;
-    stmatrix_x4_trans(base, pack2<O>(a[0], a[1]), pack2<O>(a[2], a[3]), pack2<O>(a[4], a[5]), pack2<O>(a[6], a[7]));
-    if (!kSwiglu)
-        stmatrix_x4_trans(base + 32, pack2<O>(b[0], b[1]), pack2<O>(b[2], b[3]), pack2<O>(b[4], b[5]), pack2<O>(b[6], b[7]));
     __syncwarp();
     if (p.vec && n0 + W <= p.N) {
-        constexpr int L = W / 8;  // lanes per row
+        constexpr int L = W * O::kBytes / 16;  // lanes per row
         const int row0 = lane / L, part = lane % L;
-        T *o = out + (int64_t)row0 * p.N + n0 + part * 8;
+        T *o = out + (int64_t)row0 * p.N + n0 + part * (16 / O::kBytes);
 #pragma unroll
         for (int i = 0; i < L / 2; i++, o += (int64_t)(32 / L) * p.N) {
             const int row = row0 + i * (32 / L);
             if (row < rows) *reinterpret_cast<uint4 *>(o) = *reinterpret_cast<const uint4 *>(stage + row * P + part * 16);
         }
-    } else {
-        const int in = lane < W && n0 + lane < p.N ? min(rows, 16) : 0;
-        T *o = out + n0 + lane;
-        for (int i = 0; i < in; i++, o += p.N) *o = *reinterpret_cast<const T *>(stage + i * P + lane * 2);
+    } else {  // one element a lane: a row, or two rows of 16
+        constexpr int R = 32 / W;
+        const int col = lane % W, row0 = lane / W, in = n0 + col < p.N ? min(rows, 16) : 0;
+        T *o = out + (int64_t)row0 * p.N + n0 + col;
+#pragma unroll
+        for (int i = 0; i < 16; i += R, o += R * (int64_t)p.N)
+            if (i + row0 < in) *o = *reinterpret_cast<const T *>(stage + (i + row0) * P + col * O::kBytes);
     }
+    __syncwarp();
 }
 
 // One row's sums of this warp's lanes (the parts of a cluster, added up).
@@ -645,7 +626,7 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
             for (int c = split * per + half; c < c1; c += 2) {
                 const uint32_t a = tc::smem_u32(reinterpret_cast<float *>(dyn) + c * BM + q * 32 + lane);
                 float v = 0.f;
-                for (int r = 0; r < p.splits; r++) v += ld_cluster(a, r);
+                for (int r = 0; r < p.splits; r++) v += __uint_as_float(ld_cluster(a, r));
                 write_row<O, kSwiglu>(p, m, q, lane, c, v);
             }
         }
@@ -654,25 +635,24 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
 }
 
 // Rows per tile (a multiple of 16, at most MAX_BN).  Several groups: twice the
-// mean, since their sizes are known on the device only; a larger group takes
-// more tiles.
-static int grouped_rows(int rows, int E)
+// mean, since their sizes are known on the device only (a larger group takes
+// more tiles), but no more than what gives every SM a tile.
+static int grouped_rows(int rows, int E, int n_tiles, int sms)
 {
     const int64_t groups = std::min(E, rows), want = 2 * ((rows + groups - 1) / groups);
-    return (int)std::min<int64_t>(MAX_BN, (want + 31) / 32 * 32);
+    const int64_t share = ((int64_t)rows * n_tiles + sms - 1) / sms;
+    return (int)std::min<int64_t>(MAX_BN, (std::min(want, std::max<int64_t>(share, 32)) + 31) / 32 * 32);
 }
 
-// One group: the count of equal tiles that takes the fewest rounds of the SMs
-// times the cost of a tile, counted in 128-byte rows moved: a step's rows of
-// both operands (measured: it moves about 0.4 a cycle), and leaving tensor
-// memory (a row's 128 columns cost about as much as eight).
+// One group: the width that takes the fewest rounds of the SMs times the cost of
+// a tile, counted in 128-byte rows moved: a step's rows of both operands
+// (measured: 0.4 a cycle), and leaving tensor memory (a row's 128 columns cost
+// about as much as eight).
 static int dense_rows(int rows, int n_tiles, int nk, int sms)
 {
     int best = MAX_BN;
     int64_t best_cost = INT64_MAX;
-    const int least = (rows + MAX_BN - 1) / MAX_BN;
-    for (int nt = least; nt <= least * 2 + 1; nt++) {
-        const int bn = ((rows + nt - 1) / nt + 15) / 16 * 16;
+    for (int bn = MAX_BN; bn >= 16; bn -= 16) {
         const int64_t rounds = ((int64_t)((rows + bn - 1) / bn) * n_tiles + sms - 1) / sms;
         const int64_t cost = rounds * ((int64_t)nk * (BM + 24 + bn) + 8 * bn + 400);
         if (cost < best_cost) {
@@ -737,7 +717,7 @@ extern "C" moe_status moe_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_sc
     p.offsets = offsets, p.w_scales = w_scales, p.x_scales = x_scales, p.pitch = (p.nk + 3) / 4 * 32;
     p.out = out, p.vec = aligned16(out) && N % 8 == 0, p.status = dev_status;
     const int sms = sm_count();
-    p.bn = offsets ? grouped_rows(rows, E) : dense_rows(rows, p.n_tiles, p.nk, sms);
+    p.bn = offsets ? grouped_rows(rows, E, p.n_tiles, sms) : dense_rows(rows, p.n_tiles, p.nk, sms);
     const int stage = A_BYTES + (p.bn + 31) / 32 * 32 * (BK / 2) + SF_BYTES;
     p.stages = std::min(MAX_STAGES, MAX_STAGE_BYTES / stage);
     // at most this many items: every group's last row tile may be short

@@ -6,6 +6,7 @@
 // The pages group the tokens of a verify window that share an expert
 // ("Strata serves a 125B MoE at 94 tokens/s from a 12 GB card and 64 GB of
 // RAM", section "Six billion active parameters per token").
+#include "cluster.cuh"
 #include "common.cuh"
 
 namespace moe {
@@ -13,6 +14,10 @@ namespace moe {
 constexpr int kPermChunk = 2048;     // pairs per chunk in the multi-CTA path
 constexpr int kPermSmallMax = 4096;  // single-CTA path up to this many pairs
 constexpr int kPlaceWarps = 8;       // warps per chunk in the multi-CTA path
+// A cluster in between: 4,000 pairs over 512 experts take it 5.3 us, a single CTA
+// 8.9; 20,480 take it 8.3, the three passes 11.9 (40,960: 12.0 and 11.5).
+constexpr int kClusterCtas = 8;
+constexpr int kPermClusterMin = 1025, kPermClusterMax = 32768;
 
 // Warp-serial stable placement of pairs [f0, f1) starting from per-expert
 // cursors `cur` (shared memory).  Lanes take 32 pairs at a time in order.
@@ -135,6 +140,54 @@ __global__ void __launch_bounds__(1024) permute_small_kernel(const int32_t *__re
     }
 }
 
+// One cluster of CTAs, a share of the pairs each (per_cta, a multiple of 32):
+// as the single CTA, but an expert's start also counts the CTAs before, whose
+// counts are read from their shared memory.
+__global__ void __launch_bounds__(1024) permute_cluster_kernel(const int32_t *__restrict__ ids, int n, int E, int per_cta,
+                                                               int warps, int seg, int32_t *__restrict__ offsets,
+                                                               int32_t *__restrict__ perm, int32_t *__restrict__ inv,
+                                                               int32_t *status)
+{
+    extern __shared__ int32_t hist[];
+    __shared__ int32_t mine[1024];
+    __shared__ int32_t warp_tot[33];
+    const int tid = threadIdx.x, rank = (int)cluster_rank();
+    const int64_t f0 = min((int64_t)n, (int64_t)rank * per_cta), f1 = min((int64_t)n, f0 + per_cta);
+    count_runs(ids, f0, f1, seg, E, warps, hist, status);
+    if (tid < E) {
+        int v = 0;
+        for (int w = 0; w < warps; w++) v += hist[w * E + tid];
+        mine[tid] = v;
+    }
+    cluster_sync();
+    int before = 0, all = 0;
+    if (tid < E) {
+        const uint32_t a = (uint32_t)__cvta_generic_to_shared(&mine[tid]);
+        int v[kClusterCtas];
+#pragma unroll
+        for (int r = 0; r < kClusterCtas; r++) v[r] = (int)ld_cluster(a, r);
+#pragma unroll
+        for (int r = 0; r < kClusterCtas; r++) {
+            before += r < rank ? v[r] : 0;
+            all += v[r];
+        }
+    }
+    int total = 0;
+    const int excl = block_exclusive_scan(all, warp_tot, total);
+    if (tid < E) {
+        if (rank == 0) offsets[tid] = excl;
+        runs_to_cursors(tid, E, warps, excl + before, hist);
+    }
+    if (rank == 0 && tid == 0) offsets[E] = total;
+    for (int p = total + rank * (int)blockDim.x + tid; p < n; p += kClusterCtas * (int)blockDim.x) perm[p] = -1;
+    __syncthreads();
+    if (warp_id() < warps) {
+        const int64_t a = f0 + (int64_t)warp_id() * seg;
+        place_pairs(ids, a, min(f1, a + seg), E, hist + warp_id() * E, perm, inv);
+    }
+    cluster_sync();  // no CTA leaves while another reads its counts
+}
+
 // Multi-CTA pass 1: per-chunk histograms -> counts[chunk][E].
 __global__ void permute_count_kernel(const int32_t *__restrict__ ids, int64_t n, int E, int32_t *__restrict__ counts,
                                      int32_t *status)
@@ -255,6 +308,31 @@ extern "C" moe_status moe_permute(const int32_t *ids, int T, int k, int E, int32
         return MOE_OK;
     }
     MOE_REQUIRE(ids && perm && inv_perm, "NULL pointer");
+    int64_t c = n_chunks_for(n);
+    size_t part = align256((size_t)c * E * sizeof(int32_t));
+    if (n > kPermSmallMax && (!ws || ws_bytes < 2 * part))
+        return fail(MOE_ERR_WORKSPACE, "permute needs %zu bytes (%.2f MiB) of workspace, got %zu", 2 * part,
+                    mib(2.0 * part), ws ? ws_bytes : (size_t)0);
+    if (n >= kPermClusterMin && n <= kPermClusterMax) {
+        const int per_cta = (int)((n + kClusterCtas * 32 - 1) / (kClusterCtas * 32)) * 32;
+        const int most = std::min(std::min(32, 11000 / E), per_cta / 32);  // runs, in 44,000 bytes of counters
+        const int seg = (per_cta + most * 32 - 1) / (most * 32) * 32;
+        const int warps = (per_cta + seg - 1) / seg;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kClusterCtas);
+        cfg.blockDim = dim3(1024);
+        cfg.dynamicSmemBytes = (size_t)warps * E * sizeof(int32_t);
+        cfg.stream = s;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = kClusterCtas;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, permute_cluster_kernel, ids, (int)n, E, per_cta, warps, seg, offsets, perm,
+                                        inv_perm, dev_status));
+        return check_launch("permute_cluster");
+    }
     if (n <= kPermSmallMax) {
         // as many runs of 32 or more pairs as 48,000 bytes of counters hold
         const int most = (int)std::min<int64_t>(std::min(32, 12000 / E), (n + 31) / 32);
@@ -264,11 +342,6 @@ extern "C" moe_status moe_permute(const int32_t *ids, int T, int k, int E, int32
                                                                                 inv_perm, dev_status);
         return check_launch("permute_small");
     }
-    int64_t c = n_chunks_for(n);
-    size_t part = align256((size_t)c * E * sizeof(int32_t));
-    if (!ws || ws_bytes < 2 * part)
-        return fail(MOE_ERR_WORKSPACE, "permute needs %zu bytes (%.2f MiB) of workspace, got %zu", 2 * part,
-                    mib(2.0 * part), ws ? ws_bytes : (size_t)0);
     int32_t *counts = static_cast<int32_t *>(ws);
     int32_t *base = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + part);
     permute_count_kernel<<<(unsigned)c, 256, 0, s>>>(ids, n, E, counts, dev_status);
