@@ -644,41 +644,42 @@ static int grouped_rows(int rows, int E, int n_tiles, int sms)
     return (int)std::min<int64_t>(MAX_BN, (std::min(want, std::max<int64_t>(share, 32)) + 31) / 32 * 32);
 }
 
-// One group: the width that takes the fewest rounds of the SMs times the cost of
-// a tile, counted in 128-byte rows moved: a step's rows of both operands
-// (measured: 0.4 a cycle), and leaving tensor memory (a row's 128 columns cost
-// about as much as eight).
-static int dense_rows(int rows, int n_tiles, int nk, int sms)
+// What a plan costs, in units of 10 ns (measured).  A step of 256 K takes 0.29 us
+// with few rows (its instructions, one after the other), more when its bytes
+// take longer: 0.39 us for 160 rows, 0.47 for 224.  A row leaves tensor memory
+// in some 8 ns, hidden but for the last tile's.  Splitting K over s CTAs adds
+// 1.8 us and 25 ns a row; a cluster needs its SMs in one group of them, and all
+// clusters are to be there at once.  (One row, 2048 columns: K = 2048 takes 5.0 us
+// whole and 5.1 in four parts, K = 8192 11.9 and 7.7; 16 items in eight parts 8.7.)
+static int64_t plan_cost(int64_t items, int bn, int nk, int splits, int sms)
 {
-    int best = MAX_BN;
-    int64_t best_cost = INT64_MAX;
-    for (int bn = MAX_BN; bn >= 16; bn -= 16) {
-        const int64_t rounds = ((int64_t)((rows + bn - 1) / bn) * n_tiles + sms - 1) / sms;
-        const int64_t cost = rounds * ((int64_t)nk * (BM + 24 + bn) + 8 * bn + 400);
-        if (cost < best_cost) {
-            best_cost = cost;
-            best = bn;
-        }
-    }
-    return best;
+    if (splits > 1 && (splits > nk || items * splits > (splits < 8 ? sms - 24 : sms - 56))) return INT64_MAX;
+    const int64_t rounds = (items + sms - 1) / sms, step = std::max(29, (BM + 24 + bn) / 8);
+    return rounds * ((nk + splits - 1) / splits) * step + 4 * bn / 5 + 30 * rounds + (splits > 1 ? 180 + 5 * bn / 2 : 0);
 }
 
-// CTAs per item.  A step takes some 0.29 us where little else runs; adding the
-// parts takes 1.8 us and 0.025 us per row.  (One row, 2048 columns: K = 2048
-// takes 5.0 us whole and 5.1 in four parts, K = 8192 11.9 and 7.7; in eight, 16
-// items take 8.7, since a cluster of eight needs its SMs in one group of them
-// and they are not all there at once.)
-static int split_k(int64_t items, int nk, int rows, int sms)
+// Rows per tile (one group) and CTAs per item.
+static void plan_dense(int rows, int n_tiles, int nk, int sms, int *bn, int *splits)
 {
-    int best = 1, best_cost = 29 * nk;
-    for (int s = 2; s <= 8 && s <= nk; s *= 2) {
-        if (items * s > (s < 8 ? sms - 24 : sms - 56)) break;
-        const int cost = 29 * ((nk + s - 1) / s) + 180 + 5 * rows / 2;
-        if (cost < best_cost) {
-            best_cost = cost;
-            best = s;
+    int64_t best = INT64_MAX;
+    for (int b = MAX_BN; b >= 16; b -= 16) {
+        if (b - 16 >= rows) continue;  // wider than the rows
+        for (int s = 1; s <= 8; s *= 2) {
+            const int64_t cost = plan_cost((int64_t)((rows + b - 1) / b) * n_tiles, b, nk, s, sms);
+            if (cost < best) {
+                best = cost;
+                *bn = b;
+                *splits = s;
+            }
         }
     }
+}
+
+static int plan_splits(int64_t items, int bn, int nk, int sms)
+{
+    int best = 1;
+    for (int s = 2; s <= 8; s *= 2)
+        if (plan_cost(items, bn, nk, s, sms) < plan_cost(items, bn, nk, best, sms)) best = s;
     return best;
 }
 
@@ -717,7 +718,9 @@ extern "C" moe_status moe_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_sc
     p.offsets = offsets, p.w_scales = w_scales, p.x_scales = x_scales, p.pitch = (p.nk + 3) / 4 * 32;
     p.out = out, p.vec = aligned16(out) && N % 8 == 0, p.status = dev_status;
     const int sms = sm_count();
-    p.bn = offsets ? grouped_rows(rows, E, p.n_tiles, sms) : dense_rows(rows, p.n_tiles, p.nk, sms);
+    p.splits = 0;
+    if (offsets) p.bn = grouped_rows(rows, E, p.n_tiles, sms);
+    else plan_dense(rows, p.n_tiles, p.nk, sms, &p.bn, &p.splits);
     const int stage = A_BYTES + (p.bn + 31) / 32 * 32 * (BK / 2) + SF_BYTES;
     p.stages = std::min(MAX_STAGES, MAX_STAGE_BYTES / stage);
     // at most this many items: every group's last row tile may be short
@@ -733,7 +736,7 @@ extern "C" moe_status moe_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_sc
         p.tiles_m = (uint32_t)((1ull << (31 + sh)) / p.n_tiles + 1);
         p.tiles_shift = sh - 1;
     }
-    p.splits = split_k(items, p.nk, std::min(p.bn, rows), sms);
+    if (offsets) p.splits = plan_splits(items, std::min(p.bn, rows), p.nk, sms);
     const int64_t grid = p.splits > 1 ? items * p.splits : std::min<int64_t>(items, sms);
     const size_t smem = (size_t)p.stages * stage + 1024;
     CUtensorMap mw, mxm;
