@@ -62,7 +62,7 @@ struct Params {
     const uint8_t *w_scales, *x_scales;
     int pitch;                   // bytes of scales per row, a multiple of 32: four steps
     void *out;
-    int vec;  // rows of out are 16-byte pieces
+    int unit;  // bytes of the units that rows of out are made of: 16, 4 or 2
     int32_t *status;
 };
 
@@ -249,6 +249,21 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     return w;
 }
 
+// 16 staged rows of W columns to their place, in units that the rows' length and
+// alignment allow (so a unit is in the matrix or past its edge as a whole).
+template <class U, class T, int W, int P>
+__device__ __forceinline__ void copy_out(T *out, int N, int n0, int rows, int lane, const char *stage)
+{
+    if constexpr (sizeof(U) >= sizeof(T)) {
+        constexpr int E = sizeof(U) / sizeof(T), L = W / E, R = 32 / L;  // elements of a unit, lanes of a row, rows at once
+        const int row0 = lane / L, col = (lane % L) * E, in = n0 + col < N ? min(rows, 16) : 0;
+        T *o = out + (int64_t)row0 * N + n0 + col;
+#pragma unroll
+        for (int i = 0; i < 16; i += R, o += (int64_t)R * N)
+            if (i + row0 < in) *reinterpret_cast<U *>(o) = *reinterpret_cast<const U *>(stage + (i + row0) * P + (lane % L) * sizeof(U));
+    }
+}
+
 // Rows c .. c+15 of a tile, whose sums lie in columns of tensor memory from
 // `taddr` on, a weight row per lane: this warp's 32 (SwiGLU: 16) output
 // columns.  16-bit outputs are transposed in shared memory (stmatrix) and leave
@@ -293,23 +308,9 @@ __device__ __forceinline__ void write_rows(const Params &p, const Item &m, int q
             stmatrix_x4_trans(base + 32, pack2<O>(b[0], b[1]), pack2<O>(b[2], b[3]), pack2<O>(b[4], b[5]), pack2<O>(b[6], b[7]));
     }
     __syncwarp();
-    if (p.vec && n0 + W <= p.N) {
-        constexpr int L = W * O::kBytes / 16;  // lanes per row
-        const int row0 = lane / L, part = lane % L;
-        T *o = out + (int64_t)row0 * p.N + n0 + part * (16 / O::kBytes);
-#pragma unroll
-        for (int i = 0; i < L / 2; i++, o += (int64_t)(32 / L) * p.N) {
-            const int row = row0 + i * (32 / L);
-            if (row < rows) *reinterpret_cast<uint4 *>(o) = *reinterpret_cast<const uint4 *>(stage + row * P + part * 16);
-        }
-    } else {  // one element a lane: a row, or two rows of 16
-        constexpr int R = 32 / W;
-        const int col = lane % W, row0 = lane / W, in = n0 + col < p.N ? min(rows, 16) : 0;
-        T *o = out + (int64_t)row0 * p.N + n0 + col;
-#pragma unroll
-        for (int i = 0; i < 16; i += R, o += R * (int64_t)p.N)
-            if (i + row0 < in) *o = *reinterpret_cast<const T *>(stage + (i + row0) * P + col * O::kBytes);
-    }
+    if (p.unit == 16) copy_out<uint4, T, W, P>(out, p.N, n0, rows, lane, stage);
+    else if (p.unit == 4) copy_out<uint32_t, T, W, P>(out, p.N, n0, rows, lane, stage);
+    else copy_out<uint16_t, T, W, P>(out, p.N, n0, rows, lane, stage);
     __syncwarp();
 }
 
@@ -603,10 +604,8 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
         }
         if (p.offsets) {  // rows of no group
             const int z0 = max(0, min(p.rows, __ldg(p.offsets + p.E)));
-            const int64_t n = (int64_t)(p.rows - z0) * p.N;
-            constexpr int kThreads = EPI_WARPS * 32;
-            for (int64_t i = (int64_t)blockIdx.x * kThreads + (threadIdx.x - EPI_WARP0 * 32); i < n; i += (int64_t)gridDim.x * kThreads)
-                O::store(static_cast<typename O::T *>(p.out) + (int64_t)z0 * p.N + i, 0.f);
+            zero_bytes(static_cast<typename O::T *>(p.out) + (int64_t)z0 * p.N, (int64_t)(p.rows - z0) * p.N * O::kBytes,
+                       (int64_t)blockIdx.x * (EPI_WARPS * 32) + (threadIdx.x - EPI_WARP0 * 32), (int64_t)gridDim.x * (EPI_WARPS * 32));
         }
     }
     tc::tc_fence_before();
@@ -716,7 +715,9 @@ extern "C" moe_status moe_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_sc
     p.n_tiles = (N + tn - 1) / tn;
     p.swiglu = swiglu;
     p.offsets = offsets, p.w_scales = w_scales, p.x_scales = x_scales, p.pitch = (p.nk + 3) / 4 * 32;
-    p.out = out, p.vec = aligned16(out) && N % 8 == 0, p.status = dev_status;
+    p.out = out, p.status = dev_status;
+    const int64_t row_bytes = (int64_t)N * dtype_bytes(out_dtype);
+    p.unit = aligned16(out) && row_bytes % 16 == 0 ? 16 : aligned_to(out, 4) && row_bytes % 4 == 0 ? 4 : 2;
     const int sms = sm_count();
     p.splits = 0;
     if (offsets) p.bn = grouped_rows(rows, E, p.n_tiles, sms);

@@ -64,14 +64,7 @@ __global__ void __launch_bounds__(kRowThreads, kDispatchPerSm) dispatch_kernel(c
     }
     // rows of no pair
     const int64_t z0 = first_tail_row(offsets, E, n_pairs);
-    const int64_t zn = (n_pairs - z0) * pieces;
-    for (int64_t u = w0; u < zn; u += wn) {
-        const int64_t r = z0 + u / pieces;
-        const int c0 = (int)(u % pieces) * 32 * kUnroll + lane;
-#pragma unroll
-        for (int i = 0; i < kUnroll; i++)
-            if (c0 + 32 * i < row) out[r * row + c0 + 32 * i] = V{};
-    }
+    zero_bytes(out + z0 * row, (n_pairs - z0) * row * (int64_t)sizeof(V), w0 * 32 + lane, wn * 32);
 }
 
 // ---------------------------------------------------------------- combine
@@ -201,9 +194,7 @@ __global__ void __launch_bounds__(kRowThreads, kBackPerSm) combine_backward_kern
         if (lane == 0) dw[q] = sum;
     }
     const int64_t z0 = first_tail_row(offsets, E, n_pairs);
-    for (int64_t r = z0 + w0; r < n_pairs; r += wn) {
-        for (int c = lane; c < H; c += 32) A::store(dy + r * H + c, 0.f);
-    }
+    zero_bytes(dy + z0 * H, (n_pairs - z0) * H * A::kBytes, w0 * 32 + lane, wn * 32);
 }
 
 static unsigned row_grid(int64_t warps, int per_sm)

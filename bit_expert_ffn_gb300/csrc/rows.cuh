@@ -128,6 +128,17 @@ struct Fp16 {
     }
 };
 
+// Zeros n bytes from p (both even) with the threads `rank` of `count`: 16 bytes
+// at a time between the first and the last 16-byte boundary.
+__device__ __forceinline__ void zero_bytes(void *p, int64_t n, int64_t rank, int64_t count)
+{
+    char *b = static_cast<char *>(p);
+    const int64_t head = min(n, (int64_t)(-reinterpret_cast<uintptr_t>(b) & 15)), pieces = (n - head) / 16, tail = n - head - pieces * 16;
+    for (int64_t i = rank; i < pieces; i += count) reinterpret_cast<uint4 *>(b + head)[i] = make_uint4(0, 0, 0, 0);
+    for (int64_t i = rank; i < (head + tail) / 2; i += count)
+        *reinterpret_cast<uint16_t *>(i * 2 < head ? b + i * 2 : b + pieces * 16 + i * 2) = 0;
+}
+
 inline bool dtype_ok(moe_dtype t) { return t == MOE_F32 || t == MOE_BF16 || t == MOE_F16; }
 inline int dtype_bytes(moe_dtype t) { return t == MOE_F32 ? 4 : 2; }
 inline bool aligned_to(const void *p, int n) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(n - 1)) == 0; }

@@ -145,6 +145,20 @@ def test_combine_gradient_is_the_difference_quotient(moe):
     assert abs(got - want) <= (H / 32 + 14) * R.U32 * mag + 1e-9 * mag
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_dispatch_gradient_is_its_adjoint(moe, dtype):
+    """<dispatch(x), g> = <x, dispatch_backward(g)>: the difference quotient of a linear map, without its rounding."""
+    T, H, E, k = 21, 136, 9, 4
+    rng, ids, (offsets, perm, inv) = case(T, H, E, k, 0.3, seed=8)
+    x, g = (dev(rng.standard_normal(s).astype(np.float32)).to(dtype) for s in ((T, H), (T * k, H)))
+    rows, dx = torch.empty_like(g), torch.empty_like(x)
+    m.moe_dispatch(x, TYPES[dtype], T, H, k, E, dev(offsets), dev(inv), rows)
+    m.moe_dispatch_backward(g, TYPES[dtype], T, H, k, dev(inv), dx)
+    a, b = (R.f64(rows) * R.f64(g)).sum(), (R.f64(x) * R.f64(dx)).sum()
+    mag = np.abs(R.f64(rows) * R.f64(g)).sum()  # dx is off by k roundings of its sum and one to its type, at most of mag
+    assert abs(a - b) <= (k * R.U32 + R.HALF[dtype]) * mag * 1.01
+
+
 def test_dispatch_takes_rows_at_a_stride_and_one_row_for_all(moe):
     T, H, E, k = 13, 48, 5, 2
     rng, ids, (offsets, perm, inv) = case(T, H, E, k, 0.0, seed=5)
