@@ -454,11 +454,12 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
                 set_status(p.status, MOE_ERR_TIMEOUT);
                 S.abort = 1;
             }
-            // no copy may still be in flight when the CTA leaves (a full
-            // barrier that never got its scales' arrival runs out of time)
+            // no copy may still be in flight when the CTA leaves (after a
+            // stop a barrier may lack its scales' arrivals: the copies
+            // themselves land long before the shorter limit)
             for (int i = 0; i < p.stages && i < it; i++) {
                 const int u = (it - 1 - i) / p.stages;
-                if (!tc::mbar_wait(&S.full[i], u & 1, kWaitNs)) set_status(p.status, MOE_ERR_TIMEOUT);
+                if (!tc::mbar_wait(&S.full[i], u & 1, ok && !S.abort ? kWaitNs : kWaitNs / 100)) set_status(p.status, MOE_ERR_TIMEOUT);
             }
         }
     } else if (warp == 1) {

@@ -19,7 +19,8 @@ constexpr int kRowThreads = 256;
 // us), and combine's gradient with some (106 against 113 us at 8192 tokens).
 // combine: more CTAs with a row or two on their way per lane each do better
 // than fewer with four or five (16-bit rows: 64 against 83 us at 8192 tokens).
-constexpr int kDispatchPerSm = 6, kCombinePerSm = 8, kBackPerSm = 4, kBackGrid = 32;
+constexpr int kDispatchPerSm = 6, kBackPerSm = 4, kBackGrid = 32;
+constexpr int combine_per_sm(int bytes, int unit) { return bytes == 2 && unit == 2 ? 6 : 8; }  // (63 against 97 us with eight, 2046 columns)
 constexpr int kMaxK = 16;
 
 // inv_perm of a token's slot (lane j of the warp), -1 for left-out pairs; an
@@ -72,17 +73,19 @@ __global__ void __launch_bounds__(kRowThreads, kDispatchPerSm) dispatch_kernel(c
 
 // ---------------------------------------------------------------- combine
 // out[t] = (out[t]) + sum_j w[t][j] y[inv[t][j]] in slot order, fp32 sums,
-// one rounding at the end.  Unit of work: 256 columns of one token (eight per
-// lane; scalar columns where rows are not 16-byte aligned).
+// one rounding at the end.  Unit of work: 256 columns of one token, eight per
+// lane, in accesses of kUnit columns (8, or 2 or 1 where rows are not aligned).
 // kBatch rows are on their way per lane: one where the pieces fill the GPU
 // (more CTAs do better than more loads each), several where few warps run and
 // each waits for its rows in turn otherwise.
-template <class A, class O, bool kVec, int kBatch>
-__global__ void __launch_bounds__(kRowThreads, kBatch == 1 ? kCombinePerSm : 2) combine_kernel(const typename A::T *__restrict__ y, int64_t T, int H,
-                                                              int k, const float *__restrict__ w,
-                                                              const int32_t *__restrict__ inv,
-                                                              typename O::T *__restrict__ out, int accumulate)
+template <class A, class O, int kUnit, int kBatch>
+__global__ void __launch_bounds__(kRowThreads, kBatch == 1 ? combine_per_sm(A::kBytes, kUnit) : 2)
+    combine_kernel(const typename A::T *__restrict__ y, int64_t T, int H, int k, const float *__restrict__ w,
+                   const int32_t *__restrict__ inv, typename O::T *__restrict__ out, int accumulate)
 {
+    using UA = Unit<A, kUnit>;
+    using UO = Unit<O, kUnit>;
+    constexpr int P = 8 / kUnit;
     const int lane = lane_id();
     const int pieces = (H + 255) / 256;
     const int64_t n_pairs = T * k, units = T * pieces;
@@ -91,63 +94,72 @@ __global__ void __launch_bounds__(kRowThreads, kBatch == 1 ? kCombinePerSm : 2) 
         const int64_t t = u / pieces;
         const int32_t p = pair_row(inv, t, k, n_pairs, lane);
         const float f = w && lane < k ? w[t * k + lane] : 1.0f;
-        const int c0 = (int)(u % pieces) * 256;
-        float acc[8] = {};
-        typename O::T *o = out + t * H;
-        if (kVec) {
-            const int c = c0 + lane * 8;
-            if (accumulate && c < H) O::load8(o + c, acc);
-            for (int j0 = 0; j0 < k; j0 += kBatch) {
-                typename A::Raw8 q[kBatch];
-                int32_t r[kBatch];
+        const int c = (int)(u % pieces) * 256 + lane * kUnit;  // and every 32 kUnit from there
+        float acc[P][kUnit] = {};
+        typename O::T *o = out + t * H + c;
+        if (accumulate) {
 #pragma unroll
-                for (int j = 0; j < kBatch; j++) {  // (lanes from k on hold -1)
-                    r[j] = __shfl_sync(0xffffffffu, p, min(j0 + j, 31));
-                    if (r[j] >= 0 && c < H) q[j] = A::raw8(y + (int64_t)r[j] * H + c);
-                }
-#pragma unroll
-                for (int j = 0; j < kBatch; j++) {
-                    const float g = __shfl_sync(0xffffffffu, f, min(j0 + j, 31));
-                    if (r[j] < 0 || c >= H) continue;
-                    float v[8];
-                    A::unpack8(q[j], v);
-#pragma unroll
-                    for (int i = 0; i < 8; i++) acc[i] = fmaf(g, v[i], acc[i]);
-                }
-            }
-            if (c < H) O::store8(o + c, acc);
-        } else {
-            const int c = c0 + lane;
-            if (accumulate) {
-#pragma unroll
-                for (int i = 0; i < 8; i++)
-                    if (c + 32 * i < H) acc[i] = O::load(o + c + 32 * i);
-            }
+            for (int i = 0; i < P; i++)
+                if (c + i * 32 * kUnit < H) UO::unpack(UO::raw(o + i * 32 * kUnit), acc[i]);
+        }
+        if constexpr (kBatch == 1) {
             for (int j = 0; j < k; j++) {
                 const int32_t r = __shfl_sync(0xffffffffu, p, j);
                 const float g = __shfl_sync(0xffffffffu, f, j);
                 if (r < 0) continue;
+                const typename A::T *row = y + (int64_t)r * H + c;
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-                    if (c + 32 * i < H) acc[i] = fmaf(g, A::load(y + (int64_t)r * H + c + 32 * i), acc[i]);
+                for (int i = 0; i < P; i++) {
+                    if (c + i * 32 * kUnit >= H) continue;
+                    float v[kUnit];
+                    UA::unpack(UA::raw(row + i * 32 * kUnit), v);
+#pragma unroll
+                    for (int e = 0; e < kUnit; e++) acc[i][e] = fmaf(g, v[e], acc[i][e]);
+                }
+            }
+        }
+        for (int j0 = 0; kBatch > 1 && j0 < k; j0 += kBatch) {
+            typename UA::Raw q[kBatch][P];
+            int32_t r[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; j++) {  // (lanes from k on hold -1)
+                r[j] = __shfl_sync(0xffffffffu, p, min(j0 + j, 31));
+                const typename A::T *row = y + (int64_t)r[j] * H + c;
+#pragma unroll
+                for (int i = 0; i < P; i++)
+                    if (r[j] >= 0 && c + i * 32 * kUnit < H) q[j][i] = UA::raw(row + i * 32 * kUnit);
             }
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-                if (c + 32 * i < H) O::store(o + c + 32 * i, acc[i]);
+            for (int j = 0; j < kBatch; j++) {
+                const float g = __shfl_sync(0xffffffffu, f, min(j0 + j, 31));
+                if (r[j] < 0) continue;
+#pragma unroll
+                for (int i = 0; i < P; i++) {
+                    if (c + i * 32 * kUnit >= H) break;
+                    float v[kUnit];
+                    UA::unpack(q[j][i], v);
+#pragma unroll
+                    for (int e = 0; e < kUnit; e++) acc[i][e] = fmaf(g, v[e], acc[i][e]);
+                }
+            }
         }
+#pragma unroll
+        for (int i = 0; i < P; i++)
+            if (c + i * 32 * kUnit < H) UO::store(o + i * 32 * kUnit, acc[i]);
     }
 }
 
 // ---------------------------------------------------------------- combine's gradients
 // One warp per (token, slot): dy[inv] = w dout[t] and dw = <dout[t], y[inv]>,
 // the dot product in fp32 (lane sums over strided pieces, then a fixed tree).
-template <class A, bool kVec>
+template <class A, int kUnit>
 __global__ void __launch_bounds__(kRowThreads, kBackPerSm) combine_backward_kernel(
     const typename A::T *__restrict__ dout, const typename A::T *__restrict__ y, int64_t T, int H, int k, int E,
     const int32_t *__restrict__ offsets, const float *__restrict__ w, const int32_t *__restrict__ inv,
     typename A::T *__restrict__ dy, float *__restrict__ dw)
 {
-    constexpr int kBatch = A::kBytes == 2 ? 4 : 2;  // pieces of both rows on their way per lane
+    using U = Unit<A, kUnit>;
+    constexpr int kBatch = kUnit < 8 ? 8 : A::kBytes == 2 ? 4 : 2;  // accesses of both rows on their way per lane
     const int lane = lane_id();
     const int64_t n_pairs = T * k;
     const int64_t w0 = (int64_t)blockIdx.x * (kRowThreads / 32) + warp_id(), wn = (int64_t)gridDim.x * (kRowThreads / 32);
@@ -161,35 +173,26 @@ __global__ void __launch_bounds__(kRowThreads, kBackPerSm) combine_backward_kern
         const typename A::T *d = dout + q / k * H, *yr = y + (int64_t)r * H;
         typename A::T *o = dy + (int64_t)r * H;
         float sum = 0.f;
-        if (kVec) {
-            for (int c0 = lane * 8; c0 < H; c0 += kBatch * 256) {
-                typename A::Raw8 dq[kBatch], yq[kBatch];
+        for (int c0 = lane * kUnit; c0 < H; c0 += kBatch * 32 * kUnit) {
+            typename U::Raw dq[kBatch], yq[kBatch];
 #pragma unroll
-                for (int i = 0; i < kBatch; i++)
-                    if (c0 + i * 256 < H) {
-                        yq[i] = A::raw8(yr + c0 + i * 256);
-                        dq[i] = A::raw8(d + c0 + i * 256);
-                    }
-#pragma unroll
-                for (int i = 0; i < kBatch; i++) {
-                    if (c0 + i * 256 >= H) break;
-                    float a[8], b[8];
-                    A::unpack8(dq[i], a);
-                    A::unpack8(yq[i], b);
-#pragma unroll
-                    for (int e = 0; e < 8; e++) {
-                        sum = fmaf(a[e], b[e], sum);
-                        a[e] *= f;
-                    }
-                    A::store8(o + c0 + i * 256, a);
+            for (int i = 0; i < kBatch; i++)
+                if (c0 + i * 32 * kUnit < H) {
+                    yq[i] = U::raw(yr + c0 + i * 32 * kUnit);
+                    dq[i] = U::raw(d + c0 + i * 32 * kUnit);
                 }
-            }
-        } else {
-#pragma unroll 4
-            for (int c = lane; c < H; c += 32) {
-                const float a = A::load(d + c);
-                sum = fmaf(a, A::load(yr + c), sum);
-                A::store(o + c, a * f);
+#pragma unroll
+            for (int i = 0; i < kBatch; i++) {
+                if (c0 + i * 32 * kUnit >= H) break;
+                float a[kUnit], b[kUnit];
+                U::unpack(dq[i], a);
+                U::unpack(yq[i], b);
+#pragma unroll
+                for (int e = 0; e < kUnit; e++) {
+                    sum = fmaf(a[e], b[e], sum);
+                    a[e] *= f;
+                }
+                U::store(o + c0 + i * 32 * kUnit, a);
             }
         }
 #pragma unroll
@@ -206,8 +209,11 @@ static unsigned row_grid(int64_t warps, int per_sm)
     return (unsigned)std::max<int64_t>(1, std::min<int64_t>(blocks, (int64_t)sm_count() * per_sm));
 }
 
-// 16-byte accesses of eight (or four) elements need aligned rows.
-static bool vec_rows(moe_dtype t, int H, const void *p) { return aligned16(p) && H % 8 == 0 && dtype_ok(t); }
+// Elements per access that rows of H allow from p on: 8, 2 or 1.
+static int row_unit(moe_dtype t, int H, const void *p)
+{
+    return H % 8 == 0 && aligned16(p) ? 8 : H % 2 == 0 && aligned_to(p, 2 * dtype_bytes(t)) ? 2 : 1;
+}
 
 static moe_status check_rows(int T, int H, int k, moe_dtype dtype)
 {
@@ -234,9 +240,9 @@ static moe_status combine_any(const void *y, moe_dtype dtype, int T, int H, int 
                               const int32_t *inv, void *out, moe_dtype out_dtype, int accumulate, cudaStream_t s,
                               const char *what)
 {
-    const bool vec = vec_rows(dtype, H, y) && vec_rows(out_dtype, H, out);
+    const int unit = std::min(row_unit(dtype, H, y), row_unit(out_dtype, H, out));
     const int64_t pieces = (int64_t)T * ((H + 255) / 256);
-    const unsigned grid = row_grid(pieces, kCombinePerSm);
+    const unsigned grid = row_grid(pieces, combine_per_sm(dtype_bytes(dtype), unit));
     // (ten bf16 rows of 2048 columns: 3.6 against 4.4 us at 256 tokens, 5.6 against 5.0 at 512)
     const bool few = pieces <= (int64_t)sm_count() * 16;
     return with_dtype(dtype, [&](auto a) {
@@ -245,7 +251,8 @@ static moe_status combine_any(const void *y, moe_dtype dtype, int T, int H, int 
             using O = decltype(o);
             auto *yp = static_cast<const typename A::T *>(y);
             auto *op = static_cast<typename O::T *>(out);
-            auto fn = !vec ? combine_kernel<A, O, false, 1> : few ? combine_kernel<A, O, true, 5> : combine_kernel<A, O, true, 1>;
+            auto fn = unit == 1 ? combine_kernel<A, O, 1, 1> : unit == 2 ? combine_kernel<A, O, 2, 1>
+                      : few ? combine_kernel<A, O, 8, 5> : combine_kernel<A, O, 8, 1>;
             fn<<<grid, kRowThreads, 0, s>>>(yp, T, H, k, w, inv, op, accumulate);
             return check_launch(what);
         };
@@ -320,11 +327,11 @@ extern "C" moe_status moe_combine_backward(const void *dout, const void *y, moe_
                     aligned_to(dy, dtype_bytes(dtype)),
                 "dout, y and dy must be aligned to their type");
     const unsigned grid = row_grid((int64_t)T * k, kBackGrid);
-    const bool vec = vec_rows(dtype, H, dout) && vec_rows(dtype, H, y) && vec_rows(dtype, H, dy);
+    const int unit = std::min(std::min(row_unit(dtype, H, dout), row_unit(dtype, H, y)), row_unit(dtype, H, dy));
     return with_dtype(dtype, [&](auto a) {
         using A = decltype(a);
         using E1 = typename A::T;
-        auto fn = vec ? combine_backward_kernel<A, true> : combine_backward_kernel<A, false>;
+        auto fn = unit == 8 ? combine_backward_kernel<A, 8> : unit == 2 ? combine_backward_kernel<A, 2> : combine_backward_kernel<A, 1>;
         fn<<<grid, kRowThreads, 0, to_cuda(stream)>>>(static_cast<const E1 *>(dout), static_cast<const E1 *>(y), T, H, k,
                                                       E, offsets, w, inv_perm, static_cast<E1 *>(dy), dw);
         return check_launch("combine_backward");

@@ -3,6 +3,8 @@
 // as they lie, so that several loads fit into registers before any is used).
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace moe {
@@ -126,6 +128,41 @@ struct Fp16 {
         for (int i = 0; i < 2; i++) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
         *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
     }
+};
+
+// N = 8, 2 or 1 elements of a row as one access: as they lie (Raw), in fp32.
+template <class A, int N>
+struct Unit;
+template <class A>
+struct Unit<A, 8> {
+    using Raw = typename A::Raw8;
+    __device__ static Raw raw(const typename A::T *p) { return A::raw8(p); }
+    __device__ static void unpack(const Raw &q, float (&v)[8]) { A::unpack8(q, v); }
+    __device__ static void store(typename A::T *p, const float (&v)[8]) { A::store8(p, v); }
+};
+template <class A>
+struct Unit<A, 2> {
+    using Raw = std::conditional_t<A::kBytes == 4, uint2, uint32_t>;
+    __device__ static Raw raw(const typename A::T *p) { return *reinterpret_cast<const Raw *>(p); }
+    __device__ static void unpack(const Raw &q, float (&v)[2])
+    {
+        const typename A::T *e = reinterpret_cast<const typename A::T *>(&q);
+        v[0] = A::load(e), v[1] = A::load(e + 1);
+    }
+    __device__ static void store(typename A::T *p, const float (&v)[2])
+    {
+        Raw q;
+        A::store(reinterpret_cast<typename A::T *>(&q), v[0]);
+        A::store(reinterpret_cast<typename A::T *>(&q) + 1, v[1]);
+        *reinterpret_cast<Raw *>(p) = q;
+    }
+};
+template <class A>
+struct Unit<A, 1> {
+    using Raw = typename A::T;
+    __device__ static Raw raw(const typename A::T *p) { return *p; }
+    __device__ static void unpack(const Raw &q, float (&v)[1]) { v[0] = A::load(&q); }
+    __device__ static void store(typename A::T *p, const float (&v)[1]) { A::store(p, v[0]); }
 };
 
 // Zeros n bytes from p (both even) with the threads `rank` of `count`: 16 bytes

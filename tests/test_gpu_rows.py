@@ -13,7 +13,7 @@ TYPES = {torch.float32: m.MOE_F32, torch.bfloat16: m.MOE_BF16, torch.float16: m.
 SHAPES = [  # T, H, E, k, part of the pairs left out
     (1, 8, 2, 1, 0.0), (1, 2048, 512, 10, 0.0), (4, 2048, 512, 10, 0.3), (3, 1, 4, 2, 0.0), (5, 33, 4, 3, 0.5),
     (7, 250, 1, 1, 0.0), (64, 1001, 60, 4, 0.5), (33, 264, 16, 16, 0.1), (700, 768, 64, 6, 0.0), (129, 8192, 8, 2, 0.9),
-    (40, 100, 8, 8, 1.0),
+    (40, 100, 8, 8, 1.0), (300, 2046, 24, 5, 0.2), (9, 6, 4, 2, 0.0),
 ]
 
 
