@@ -27,8 +27,7 @@ struct NormArgs {
 // How a group of threads shares a row.  kWarp: a warp per row, four rows a CTA;
 // else the CTA.  A thread holds 8 NV columns: fours, strided by the group's
 // width, when kVec (a warp's access is 256 or 512 bytes in a row; eights gave
-// fp32 rows half sectors, 156 against 100 us for the gradient of 16384 x 2048), else single
-// ones.
+// fp32 rows half sectors, 156 against 100 us for the gradient of 16384 x 2048), else twos.
 template <int NV_, bool kVec_, bool kWarp_>
 struct Group {
     static constexpr int NV = NV_, N = NV_ * 8;
@@ -85,31 +84,55 @@ struct Group {
         }
     }
 
-    __device__ static int col(int i) { return kVec ? ((i >> 2) * width() + rank()) * 4 + (i & 3) : rank() + i * width(); }
+    __device__ static int col(int i)
+    {
+        return kVec ? ((i >> 2) * width() + rank()) * 4 + (i & 3) : ((i >> 1) * width() + rank()) * 2 + (i & 1);
+    }
+    // Unaligned rows go by pairs where their length is even.
+    template <class A>
+    __device__ static bool pairs(const typename A::T *p, int H)
+    {
+        return H % 2 == 0 && (reinterpret_cast<uintptr_t>(p) & (2 * A::kBytes - 1)) == 0;
+    }
 
     template <class A>
     __device__ static void load(const typename A::T *p, int H, float (&v)[N])
     {
+        if constexpr (kVec) {
 #pragma unroll
-        for (int i = 0; i < N; i += kVec ? 4 : 1) {
-            const int c = col(i);
-            if constexpr (kVec) {
+            for (int i = 0; i < N; i += 4) {
                 v[i] = v[i + 1] = v[i + 2] = v[i + 3] = 0.f;
-                if (c < H) A::load4(p + c, v + i);
-            } else {
-                v[i] = c < H ? A::load(p + c) : 0.f;
+                if (col(i) < H) A::load4(p + col(i), v + i);
             }
+        } else if (pairs<A>(p, H)) {
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                float t[2] = {};
+                if (col(i) < H) Unit<A, 2>::unpack(Unit<A, 2>::raw(p + col(i)), t);
+                v[i] = t[0], v[i + 1] = t[1];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i++) v[i] = col(i) < H ? A::load(p + col(i)) : 0.f;
         }
     }
     template <class A>
     __device__ static void store(typename A::T *p, int H, const float (&v)[N])
     {
+        if constexpr (kVec) {
 #pragma unroll
-        for (int i = 0; i < N; i += kVec ? 4 : 1) {
-            const int c = col(i);
-            if (c >= H) continue;
-            if constexpr (kVec) A::store4(p + c, v + i);
-            else A::store(p + c, v[i]);
+            for (int i = 0; i < N; i += 4)
+                if (col(i) < H) A::store4(p + col(i), v + i);
+        } else if (pairs<A>(p, H)) {
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const float t[2] = {v[i], v[i + 1]};
+                if (col(i) < H) Unit<A, 2>::store(p + col(i), t);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i++)
+                if (col(i) < H) A::store(p + col(i), v[i]);
         }
     }
     // w (NULL: ones), times the channel gate if there is one
