@@ -152,7 +152,7 @@ extern "C" moe_status moe_block_norm(const void *x, moe_dtype res_dtype, int64_t
     return with_norm_types(res_dtype, dtype, [&](auto r, auto a) {
         return with_norm_group(q, [&](auto g) {
             auto fn = block_norm_kernel<decltype(r), decltype(a), decltype(g)>;
-            if (q.smem > 48 * 1024) MOE_CUDA_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormRingBytes));
+            if (q.smem > kNormPlainBytes) MOE_CUDA_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormRingBytes));
             fn<<<q.grid, q.threads, q.smem, to_cuda(stream)>>>(p);
             return check_launch("block_norm");
         });

@@ -10,6 +10,7 @@ namespace moe {
 constexpr int kNormMaxH = 16384;   // 512 threads x 32 columns
 constexpr int kNormWarpH = 512;    // rows up to here take one warp, four rows a CTA
 constexpr int kNormRingBytes = 200 * 1024;
+constexpr size_t kNormPlainBytes = 40 * 1024;  // more needs the larger limit (48 KB count the kernels' own, too)
 
 struct NormArgs {
     const void *x, *b, *dy, *du;

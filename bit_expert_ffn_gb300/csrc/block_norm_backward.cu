@@ -240,7 +240,7 @@ extern "C" moe_status moe_block_norm_backward(const void *x, moe_dtype res_dtype
     st = with_norm_types(res_dtype, dtype, [&](auto r, auto a) {
         return with_norm_group(q, [&](auto g) {
             auto fn = block_norm_backward_kernel<decltype(r), decltype(a), decltype(g)>;
-            if (q.smem > 48 * 1024) MOE_CUDA_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormRingBytes));
+            if (q.smem > kNormPlainBytes) MOE_CUDA_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormRingBytes));
             fn<<<q.grid, q.threads, q.smem, s>>>(p);
             return check_launch("block_norm_backward");
         });

@@ -72,7 +72,8 @@ def values(code, byte):
 
 
 def silu(g):
-    return g / (1.0 + np.exp(-g))
+    with np.errstate(over="ignore"):
+        return g / (1.0 + np.exp(-g))
 
 
 def matmul(x, w, offsets, swiglu):

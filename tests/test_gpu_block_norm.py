@@ -14,7 +14,9 @@ TYPES = {torch.float32: m.MOE_F32, torch.bfloat16: m.MOE_BF16, torch.float16: m.
 PAIRS = [(torch.float32, torch.float32), (torch.bfloat16, torch.bfloat16), (torch.float16, torch.float16),
          (torch.float32, torch.bfloat16), (torch.float32, torch.float16)]
 SHAPES = [(1, 1), (1, 2048), (3, 8), (2, 33), (5, 264), (4, 1001), (700, 128), (6, 4096), (3, 4104), (2, 8200), (2, 16384),
-          (2, 16383), (470, 24), (9, 256), (9, 257), (6, 512), (6, 513), (2, 8192), (5, 1002), (7, 70), (2, 6006)]
+          (2, 16383), (470, 24), (9, 256), (9, 257), (6, 512), (6, 513), (2, 8192), (5, 1002), (7, 70), (2, 6006),
+          # where the rows ahead take just below 48 KB of shared memory, for one pair of types or another
+          (4, 366), (5, 486), (2, 1532), (2, 2040), (2, 3064), (2, 4088), (2, 6136)]
 GATES = {"none": m.MOE_GATE_NONE, "token": m.MOE_GATE_TOKEN, "channel": m.MOE_GATE_CHANNEL}
 # A mean's 32-bit sum: at most 32 terms per thread, a tree of 5, 16 warps in turn; the root and the products after
 # it are a few roundings more.
