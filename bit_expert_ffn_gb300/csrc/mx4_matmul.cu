@@ -151,16 +151,10 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
     return ok != 0;
 }
 
-// Whether the whole warp sees the phase complete (no waiting).
-__device__ __forceinline__ bool warp_peek(uint64_t *bar, uint32_t parity)
-{
-    return __all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity));
-}
-
 // A whole warp waits; false for all of it when the time is up or the CTA stops.
 __device__ __forceinline__ bool warp_wait(Shared &S, uint64_t *bar, uint32_t parity)
 {
-    if (warp_peek(bar, parity)) return true;
+    if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
     const bool ok = tc::mbar_wait(bar, parity, kWaitNs);
     return __all_sync(0xffffffffu, ok && !S.abort);
 }
@@ -272,7 +266,9 @@ __device__ __forceinline__ void copy_out(T *out, int N, int n0, int rows, int la
 // Rows c .. c+15 of a tile, whose sums lie in columns of tensor memory from
 // `taddr` on, a weight row per lane: this warp's 32 (SwiGLU: 16) output
 // columns.  16-bit outputs are transposed in shared memory (stmatrix) and leave
-// in pieces of 16 bytes; fp32 ones leave from the registers.
+// in pieces of 16 bytes, fp32 ones of SwiGLU too (from the registers they left in
+// pieces of 32 bytes, at a third of the speed); other fp32 sums leave from the
+// registers, a row's 128 bytes at once.
 template <class O, bool kSwiglu>
 __device__ __forceinline__ void write_rows(const Params &p, const Item &m, int q, int lane, uint32_t taddr, int c, char *stage)
 {
