@@ -206,45 +206,65 @@ __global__ void permute_count_kernel(const int32_t *__restrict__ ids, int64_t n,
     for (int e = threadIdx.x; e < E; e += blockDim.x) counts[(int64_t)blockIdx.x * E + e] = h[e];
 }
 
-// Multi-CTA pass 2 (one CTA of 1024 threads): offsets and per-chunk bases.
-__global__ void __launch_bounds__(1024) permute_scan_kernel(const int32_t *__restrict__ counts, int n_chunks, int E,
-                                                            int64_t n, int32_t *__restrict__ base,
-                                                            int32_t *__restrict__ offsets, int32_t *__restrict__ perm)
+// Multi-CTA pass 2: base[chunk][e] = expert e's pairs in the chunks before.  A CTA
+// takes 32 experts, its 32 warps runs of chunks.
+__global__ void __launch_bounds__(1024) permute_prefix_kernel(const int32_t *__restrict__ counts, int n_chunks, int E,
+                                                              int32_t *__restrict__ base)
 {
-    __shared__ int32_t warp_tot[33];
-    int tid = threadIdx.x;
+    __shared__ int32_t sum[32][33];
+    const int e = blockIdx.x * 32 + lane_id(), w = warp_id();
+    const int run = (n_chunks + 31) / 32, c0 = min(n_chunks, w * run), c1 = min(n_chunks, c0 + run);
     int v = 0;
-    if (tid < E) {
-#pragma unroll 16
-        for (int c = 0; c < n_chunks; c++) v += counts[(int64_t)c * E + tid];
+    if (e < E) {
+#pragma unroll 8
+        for (int c = c0; c < c1; c++) v += counts[(int64_t)c * E + e];
     }
-    int total = 0;
-    int excl = block_exclusive_scan(v, warp_tot, total);
-    if (tid < E) {
-        offsets[tid] = excl;
-        int run = excl;
-#pragma unroll 16
-        for (int c = 0; c < n_chunks; c++) {
-            base[(int64_t)c * E + tid] = run;
-            run += counts[(int64_t)c * E + tid];
-        }
+    sum[w][lane_id()] = v;
+    __syncthreads();
+    if (e >= E) return;
+    int before = 0;
+    for (int i = 0; i < w; i++) before += sum[i][lane_id()];
+#pragma unroll 8
+    for (int c = c0; c < c1; c++) {
+        base[(int64_t)c * E + e] = before;
+        before += counts[(int64_t)c * E + e];
     }
-    if (tid == 0) offsets[E] = total;
-    for (int64_t p = total + tid; p < n; p += blockDim.x) perm[p] = -1;
 }
 
-// Multi-CTA pass 3: a CTA of kPlaceWarps warps per chunk places its pairs in order.
+// Multi-CTA pass 3: a CTA of kPlaceWarps warps per chunk places its pairs in
+// order.  Each scans the experts' totals (the last chunk's base and count) for
+// itself; the first writes the offsets.
 __global__ void __launch_bounds__(kPlaceWarps * 32) permute_place_kernel(const int32_t *__restrict__ ids, int64_t n, int E,
+                                                                         const int32_t *__restrict__ counts,
                                                                          const int32_t *__restrict__ base,
+                                                                         int32_t *__restrict__ offsets,
                                                                          int32_t *__restrict__ perm,
                                                                          int32_t *__restrict__ inv)
 {
     __shared__ int32_t hist[kPlaceWarps * 1024];
-    constexpr int seg = kPermChunk / kPlaceWarps;
+    __shared__ int32_t warp_tot[33];
+    constexpr int seg = kPermChunk / kPlaceWarps, kThreads = kPlaceWarps * 32, kPer = 1024 / kThreads;
     const int64_t f0 = (int64_t)blockIdx.x * kPermChunk, f1 = min(n, f0 + kPermChunk);
+    const int64_t last = ((int64_t)gridDim.x - 1) * E;
+    int start[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; i++) {
+        const int e = threadIdx.x * kPer + i;
+        start[i] = sum;
+        if (e < E) sum += base[last + e] + counts[last + e];
+    }
     count_runs(ids, f0, f1, seg, E, kPlaceWarps, hist, nullptr);
-    for (int e = threadIdx.x; e < E; e += blockDim.x)
-        runs_to_cursors(e, E, kPlaceWarps, base[(int64_t)blockIdx.x * E + e], hist);
+    int total = 0;
+    const int excl = block_exclusive_scan(sum, warp_tot, total);
+#pragma unroll
+    for (int i = 0; i < kPer; i++) {
+        const int e = threadIdx.x * kPer + i;
+        if (e >= E) break;
+        if (blockIdx.x == 0) offsets[e] = excl + start[i];
+        runs_to_cursors(e, E, kPlaceWarps, excl + start[i] + base[(int64_t)blockIdx.x * E + e], hist);
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) offsets[E] = total;
+    for (int64_t p = total + (int64_t)blockIdx.x * kThreads + threadIdx.x; p < n; p += (int64_t)gridDim.x * kThreads) perm[p] = -1;
     __syncthreads();
     const int64_t a = f0 + (int64_t)warp_id() * seg;
     place_pairs(ids, a, min(f1, a + seg), E, hist + warp_id() * E, perm, inv);
@@ -347,10 +367,10 @@ extern "C" moe_status moe_permute(const int32_t *ids, int T, int k, int E, int32
     permute_count_kernel<<<(unsigned)c, 256, 0, s>>>(ids, n, E, counts, dev_status);
     moe_status st = check_launch("permute_count");
     if (st != MOE_OK) return st;
-    permute_scan_kernel<<<1, 1024, 0, s>>>(counts, (int)c, E, n, base, offsets, perm);
-    st = check_launch("permute_scan");
+    permute_prefix_kernel<<<(E + 31) / 32, 1024, 0, s>>>(counts, (int)c, E, base);
+    st = check_launch("permute_prefix");
     if (st != MOE_OK) return st;
-    permute_place_kernel<<<(unsigned)c, kPlaceWarps * 32, 0, s>>>(ids, n, E, base, perm, inv_perm);
+    permute_place_kernel<<<(unsigned)c, kPlaceWarps * 32, 0, s>>>(ids, n, E, counts, base, offsets, perm, inv_perm);
     return check_launch("permute_place");
 }
 
@@ -443,9 +463,9 @@ extern "C" moe_status moe_permute_noalloc(const int32_t *ids, int T, int k, int 
     permute_count_kernel<<<(unsigned)c, 256, 0, s>>>(ids, n, E, counts, dev_status);
     st = check_launch("permute_count (no-alloc)");
     if (st != MOE_OK) return st;
-    permute_scan_kernel<<<1, 1024, 0, s>>>(counts, (int)c, E, n, base, offsets, perm);
-    st = check_launch("permute_scan (no-alloc)");
+    permute_prefix_kernel<<<(E + 31) / 32, 1024, 0, s>>>(counts, (int)c, E, base);
+    st = check_launch("permute_prefix (no-alloc)");
     if (st != MOE_OK) return st;
-    permute_place_kernel<<<(unsigned)c, kPlaceWarps * 32, 0, s>>>(ids, n, E, base, perm, inv_perm);
+    permute_place_kernel<<<(unsigned)c, kPlaceWarps * 32, 0, s>>>(ids, n, E, counts, base, offsets, perm, inv_perm);
     return check_launch("permute_place (no-alloc)");
 }

@@ -205,7 +205,8 @@ def test_same_bits_every_time_and_on_another_stream(moe):
 
 
 @pytest.mark.parametrize("T,k,E", [(1, 1, 1), (3, 2, 1024), (32, 16, 1024), (256, 16, 1024), (409, 10, 1024), (410, 10, 1000),
-                                   (1365, 3, 375), (1366, 3, 375), (4096, 1, 7), (5000, 3, 33)])
+                                   (1365, 3, 375), (1366, 3, 375), (4096, 1, 7), (5000, 3, 33), (3276, 10, 512),
+                                   (3277, 10, 512), (8200, 10, 1000), (40000, 10, 1024), (70000, 3, 5)])
 def test_sort_of_the_pairs(moe, T, k, E):
     """The sort that the rows go by, at the sizes where its runs and chunks change, with pairs left out."""
     rng = np.random.default_rng(T * k + E)
