@@ -61,7 +61,7 @@ struct Params {
     int E, N, w_rows, rows;      // w_rows: weight rows per expert (N or 2N)
     int nk, n_mma;               // steps, and MMAs of K = 64, over the whole K
     int n_tiles, bn, stages, splits, swiglu;
-    uint32_t tiles_m, tiles_shift;  // item / n_tiles = (item * tiles_m high) >> tiles_shift (tiles_m 0: n_tiles is 1)
+    uint32_t tiles_m, tiles_shift, bn_m, bn_shift;  // reciprocals of n_tiles and bn
     const int32_t *offsets;      // NULL: one group of all rows
     int total;                   // its items
     const uint8_t *w_scales, *x_scales;
@@ -103,12 +103,18 @@ struct Item {
     int kb0, kb1;    // steps of this CTA
 };
 
+// x / d for x < 2^31: the high half of x m, shifted (m 0: d is 1).
+__device__ __forceinline__ int quotient(int x, uint32_t m, uint32_t shift)
+{
+    return m ? (int)(__umulhi((uint32_t)x, m) >> shift) : x;
+}
+
 // The whole warp finds the last expert with tile0 <= tt: 32 ranges, then one.
 __device__ __forceinline__ Item item_of(const Params &p, const Shared &S, int item, int split)
 {
     Item it;
     const int lane = lane_id();
-    const int tt = p.tiles_m ? (int)(__umulhi((uint32_t)item, p.tiles_m) >> p.tiles_shift) : item;
+    const int tt = quotient(item, p.tiles_m, p.tiles_shift);
     it.n0 = (item - tt * p.n_tiles) * (p.swiglu ? BM / 2 : BM);
     if (!p.offsets) {  // bn is a tile's rows as they are
         it.e = 0;
@@ -392,7 +398,7 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
                 S.count[e0 + i] = cnt;
             }
             n[i] = sum;
-            sum += (cnt + p.bn - 1) / p.bn;
+            sum += quotient(cnt + p.bn - 1, p.bn_m, p.bn_shift);
         }
         int incl = sum;
 #pragma unroll
@@ -635,6 +641,16 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
     }
 }
 
+// m = floor(2^(31 + s) / d) + 1 with s = ceil(log2 d): x m is at most 2^31 2^s off
+// 2^(31 + s) x / d, less than its next multiple.
+static void reciprocal(int d, uint32_t *m, uint32_t *shift)
+{
+    uint32_t s = 0;
+    while ((1ll << s) < d) s++;
+    *m = s ? (uint32_t)((1ull << (31 + s)) / (uint32_t)d + 1) : 0;
+    *shift = s ? s - 1 : 0;
+}
+
 // Rows per tile (a multiple of 16, at most MAX_BN).  Several groups: twice the
 // mean, since their sizes are known on the device only (a larger group takes
 // more tiles), but no more than what gives every SM a tile.
@@ -733,12 +749,8 @@ extern "C" moe_status moe_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_sc
     MOE_REQUIRE((int64_t)E * ((rows + p.bn - 1) / p.bn) * p.n_tiles <= (1 << 30), "too many tiles (rows=%d N=%d E=%d)", rows,
                 N, E);
     p.total = (int)items;
-    uint32_t sh = 0;  // as for the rows of a matrix's blocks: items stay below 2^31
-    while ((1 << sh) < p.n_tiles) sh++;
-    if (sh > 0) {
-        p.tiles_m = (uint32_t)((1ull << (31 + sh)) / p.n_tiles + 1);
-        p.tiles_shift = sh - 1;
-    }
+    reciprocal(p.n_tiles, &p.tiles_m, &p.tiles_shift);
+    reciprocal(p.bn, &p.bn_m, &p.bn_shift);
     if (offsets) p.splits = plan_splits(items, std::min(p.bn, rows), p.nk, sms);
     const int64_t grid = p.splits > 1 ? items * p.splits : std::min<int64_t>(items, sms);
     const size_t smem = (size_t)p.stages * stage + 1024;
