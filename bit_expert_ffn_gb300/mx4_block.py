@@ -20,10 +20,10 @@ import sys
 
 import torch
 
-from . import (MOE_BF16, MOE_F32, MOE_GATE_CHANNEL, MOE_MX4_PLAIN, MOE_MX4_SWIGLU, RMS_EPS, load, moe_block_norm,
-               moe_block_norm_backward, moe_block_norm_backward_workspace_size, moe_check_status, moe_combine,
-               moe_combine_backward, moe_dispatch, moe_dispatch_backward, moe_mx4_matmul, moe_mx4_quantise, moe_mx4_size,
-               moe_permute, moe_permute_workspace_size, moe_router_topk, moe_router_workspace_size)
+from . import (MOE_BF16, MOE_ERR_INVALID_ARG, MOE_F32, MOE_GATE_CHANNEL, MOE_MX4_PLAIN, MOE_MX4_SWIGLU, RMS_EPS, MoeError,
+               load, moe_block_norm, moe_block_norm_backward, moe_block_norm_backward_workspace_size, moe_check_status,
+               moe_combine, moe_combine_backward, moe_dispatch, moe_dispatch_backward, moe_mx4_matmul, moe_mx4_quantise,
+               moe_mx4_size, moe_permute, moe_permute_workspace_size, moe_router_topk, moe_router_workspace_size)
 from .model import LayerShape, Workspace
 
 
@@ -31,23 +31,24 @@ class Mx4Matrix:
     """[rows][cols] in MXFP4 on the device, quantised from fp32, bf16 or fp16 values."""
 
     def __init__(self, rows: int, cols: int, dev="cuda"):
-        cb, sb = moe_mx4_size(rows, cols)
+        cb, sb = moe_mx4_size(1, cols)  # a row's bytes
         self.rows, self.cols = rows, cols
-        self.codes = torch.empty(rows, cb // max(rows, 1), dtype=torch.uint8, device=dev)
-        self.scales = torch.empty(rows, sb // max(rows, 1), dtype=torch.uint8, device=dev)
+        self.codes = torch.empty(rows, cb, dtype=torch.uint8, device=dev)
+        self.scales = torch.empty(rows, sb, dtype=torch.uint8, device=dev)
 
-    def put(self, values: torch.Tensor, dtype: int, status=None) -> "Mx4Matrix":
-        moe_mx4_quantise(values, dtype, self.rows, self.cols, self.codes, self.scales, status)
+    def put(self, values: torch.Tensor, dtype: int, status=None, rows=None) -> "Mx4Matrix":
+        """Quantises values into the first `rows` rows (all of them by default)."""
+        moe_mx4_quantise(values, dtype, self.rows if rows is None else rows, self.cols, self.codes, self.scales, status)
         return self
 
 
 class Mx4BlockBuffers:
-    """What a block's forward pass writes for T tokens, and its backward pass reads."""
+    """What a block's forward pass writes for up to T tokens, and its backward pass reads."""
 
     def __init__(self, s: LayerShape, T: int, dev="cuda"):
         d, P, n = torch.device(dev), T * s.k, max(T, 1)
         i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
-        self.T = T
+        self.s, self.T = s, T
         self.logits = torch.empty(n, s.E, dtype=f32, device=d)
         self.ids = torch.empty(n, s.k, dtype=i32, device=d)
         self.w = torch.empty(n, s.k, dtype=f32, device=d)
@@ -70,6 +71,8 @@ class Mx4Block:
         """gate_up [E][2I][H] (gate rows first) and down [E][H][I] in bf16, quantised here; router_w [E][H], w_post, w_pre
         and gate [H] in fp32."""
         load()
+        self._require(router_w.dtype == torch.float32 and router_w.is_contiguous() and router_w.numel() >= s.E * s.H,
+                      f"router_w must be a packed fp32 tensor of {s.E} x {s.H} (got {tuple(router_w.shape)}, {router_w.dtype})")
         self.s, self.dev, self.alpha = s, gate_up.device, float(alpha)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.dev)
         self.gate_up = Mx4Matrix(s.E * 2 * s.I, s.H, self.dev).put(gate_up, MOE_BF16, self.status)
@@ -77,23 +80,38 @@ class Mx4Block:
         self.router_w, self.w_post, self.w_pre, self.gate = router_w, w_post, w_pre, gate
         self.ws = Workspace(self.dev)
 
+    @staticmethod
+    def _require(ok: bool, what: str):
+        if not ok:
+            raise MoeError(MOE_ERR_INVALID_ARG, f"Mx4Block: {what}")
+
+    def _check(self, T: int, bufs: Mx4BlockBuffers):
+        """Before the first launch: some of the calls take addresses and could not tell that a buffer ends too early."""
+        s, b = self.s, bufs.s
+        self._require(0 <= T <= bufs.T, f"T={T}, but the buffers are for at most {bufs.T} tokens")
+        self._require((s.H, s.I, s.E, s.k) == (b.H, b.I, b.E, b.k),
+                      f"the buffers are for H={b.H} I={b.I} E={b.E} k={b.k}, the block has H={s.H} I={s.I} E={s.E} k={s.k}")
+
     def forward(self, x, u, T, y, u_next, bufs: Mx4BlockBuffers):
-        """y, u_next <- the block on x [T][H] fp32 and u [T][H] bf16 (y may be x, u_next may be u)."""
+        """y, u_next <- the block on x [T][H] fp32 and u [T][H] bf16 (y may be x, u_next may be u); T at most the buffers'."""
         s, B = self.s, bufs
+        self._check(T, B)
+        self._require(u.dtype == torch.bfloat16 and u.is_contiguous() and u.numel() >= T * s.H,
+                      f"u must be a packed bf16 tensor of at least {T} x {s.H} (got {tuple(u.shape)}, {u.dtype})")
         rws, pws = moe_router_workspace_size(T, s.H, s.E, True), moe_permute_workspace_size(T, s.k, s.E)
         ws = self.ws.get(max(rws, pws))
         moe_router_topk(u, T, s.H, self.router_w, None, s.E, s.k, B.logits, B.ids, B.w, ws, rws, self.status)
         moe_permute(B.ids, T, s.k, s.E, B.offsets, B.perm, B.inv, ws, pws, self.status)
         # a token's codes and scales are rows of bytes like any other: a tenth of the quantising, a quarter of the
         # bytes that its bf16 rows would be
-        B.u_q.put(u, MOE_BF16, self.status)
+        B.u_q.put(u, MOE_BF16, self.status, T)
         for a, b in ((B.u_q.codes, B.rows_q.codes), (B.u_q.scales, B.rows_q.scales)):
             moe_dispatch(a.view(torch.bfloat16), MOE_BF16, T, a.shape[1] // 2, s.k, s.E, B.offsets, B.inv,
                          b.view(torch.bfloat16))
         P = T * s.k
         moe_mx4_matmul(self.gate_up.codes, self.gate_up.scales, s.E, s.I, s.H, B.rows_q.codes, B.rows_q.scales, P, B.offsets,
                        B.h, MOE_BF16, MOE_MX4_SWIGLU, self.status)
-        B.h_q.put(B.h, MOE_BF16, self.status)
+        B.h_q.put(B.h, MOE_BF16, self.status, P)
         moe_mx4_matmul(self.down.codes, self.down.scales, s.E, s.H, s.I, B.h_q.codes, B.h_q.scales, P, B.offsets, B.rows,
                        MOE_BF16, MOE_MX4_PLAIN, self.status)
         moe_combine(B.rows, MOE_BF16, T, s.H, s.k, B.w, B.inv, B.b, MOE_BF16)
@@ -105,11 +123,12 @@ class Mx4Block:
         x, w_post, w_pre, gate, w (routing weights) and rows (the experts' outputs); with drows, the gradient of the
         dispatched rows as the caller's own experts give it, also u."""
         s, B, d = self.s, bufs, self.dev
+        self._check(T, B)
         f32 = torch.float32
         g = {"x": torch.empty_like(x), "w_post": torch.empty(s.H, dtype=f32, device=d),
              "w_pre": torch.empty(s.H, dtype=f32, device=d), "gate": torch.empty(s.H, dtype=f32, device=d),
-             "rows": torch.empty_like(B.rows), "w": torch.empty_like(B.w)}
-        db = torch.empty_like(B.b)
+             "rows": torch.empty_like(B.rows[:T * s.k]), "w": torch.empty_like(B.w[:T])}
+        db = torch.empty_like(B.b[:T])
         nb = moe_block_norm_backward_workspace_size(T, s.H, MOE_GATE_CHANNEL)
         moe_block_norm_backward(x, MOE_F32, B.b, MOE_BF16, T, s.H, self.w_post, self.w_pre, self.gate, MOE_GATE_CHANNEL,
                                 self.alpha, RMS_EPS, dy, du_next, g["x"], db, g["w_post"], g["w_pre"], g["gate"],
