@@ -228,7 +228,7 @@ extern "C" moe_status moe_mx4_quantise(const void *x, moe_dtype dtype, int64_t x
     if (rows == 0) return MOE_OK;
     MOE_REQUIRE(x && codes && scales, "NULL pointer");
     MOE_REQUIRE(aligned16(codes) && aligned_to(scales, 32), "codes must be 16-byte, scales 32-byte aligned");
-    MOE_REQUIRE(aligned_to(x, dtype_bytes(dtype)), "x must be aligned to its type");
+    MOE_REQUIRE(aligned_to(x, dtype_bytes(dtype)) && aligned_to(dev_status, 4), "x and dev_status must be aligned to their types");
     const bool vec = aligned16(x) && (x_stride * dtype_bytes(dtype)) % 16 == 0;
     return with_dtype(dtype, [&](auto a) {
         using A = decltype(a);

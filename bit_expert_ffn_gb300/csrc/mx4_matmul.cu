@@ -724,7 +724,8 @@ extern "C" moe_status moe_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_sc
     MOE_REQUIRE(w_codes && w_scales && x_codes && x_scales && out, "NULL pointer");
     MOE_REQUIRE(aligned16(w_codes) && aligned16(x_codes), "codes must be 16-byte aligned");
     MOE_REQUIRE(aligned_to(w_scales, 32) && aligned_to(x_scales, 32), "scales must be 32-byte aligned");
-    MOE_REQUIRE(aligned_to(out, dtype_bytes(out_dtype)) && aligned_to(offsets, 4), "out and offsets must be aligned to their types");
+    MOE_REQUIRE(aligned_to(out, dtype_bytes(out_dtype)) && aligned_to(offsets, 4) && aligned_to(dev_status, 4),
+                "out, offsets and dev_status must be aligned to their types");
     const bool swiglu = epilogue == MOE_MX4_SWIGLU;
     Params p = {};
     p.E = E, p.N = N, p.w_rows = swiglu ? 2 * N : N, p.rows = rows;

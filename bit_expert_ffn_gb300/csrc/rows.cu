@@ -276,7 +276,8 @@ extern "C" moe_status moe_dispatch(const void *x, moe_dtype dtype, int64_t x_str
     MOE_REQUIRE(x && offsets && inv_perm && out, "NULL pointer");
     const int b = dtype_bytes(dtype);
     const int64_t rb = (int64_t)H * b, sb = x_stride * b;
-    MOE_REQUIRE(aligned_to(x, b) && aligned_to(out, b), "x and out must be aligned to their type");
+    MOE_REQUIRE(aligned_to(x, b) && aligned_to(out, b) && aligned_to(offsets, 4) && aligned_to(inv_perm, 4),
+                "x, out, offsets and inv_perm must be aligned to their types");
     cudaStream_t s = to_cuda(stream);
     if (rb % 16 == 0 && sb % 16 == 0 && aligned16(x) && aligned16(out))
         launch_dispatch<uint4>(x, sb, T, rb, k, E, offsets, inv_perm, out, s);
@@ -294,8 +295,8 @@ extern "C" moe_status moe_dispatch_backward(const void *drows, moe_dtype dtype, 
     if (st != MOE_OK) return st;
     if (T == 0) return MOE_OK;
     MOE_REQUIRE(drows && inv_perm && dx, "NULL pointer");
-    MOE_REQUIRE(aligned_to(drows, dtype_bytes(dtype)) && aligned_to(dx, dtype_bytes(dtype)),
-                "drows and dx must be aligned to their type");
+    MOE_REQUIRE(aligned_to(drows, dtype_bytes(dtype)) && aligned_to(dx, dtype_bytes(dtype)) && aligned_to(inv_perm, 4),
+                "drows, dx and inv_perm must be aligned to their types");
     return combine_any(drows, dtype, T, H, k, nullptr, inv_perm, dx, dtype, 0, to_cuda(stream), "dispatch_backward");
 }
 
@@ -309,8 +310,9 @@ extern "C" moe_status moe_combine(const void *y, moe_dtype dtype, int T, int H, 
                 (int)out_dtype, (int)dtype);
     if (T == 0) return MOE_OK;
     MOE_REQUIRE(y && w && inv_perm && out, "NULL pointer");
-    MOE_REQUIRE(aligned_to(y, dtype_bytes(dtype)) && aligned_to(out, dtype_bytes(out_dtype)),
-                "y and out must be aligned to their type");
+    MOE_REQUIRE(aligned_to(y, dtype_bytes(dtype)) && aligned_to(out, dtype_bytes(out_dtype)) && aligned_to(w, 4) &&
+                    aligned_to(inv_perm, 4),
+                "y, out, w and inv_perm must be aligned to their types");
     return combine_any(y, dtype, T, H, k, w, inv_perm, out, out_dtype, accumulate, to_cuda(stream), "combine");
 }
 
@@ -324,8 +326,9 @@ extern "C" moe_status moe_combine_backward(const void *dout, const void *y, moe_
     if (T == 0) return MOE_OK;
     MOE_REQUIRE(dout && y && offsets && w && inv_perm && dy && dw, "NULL pointer");
     MOE_REQUIRE(aligned_to(dout, dtype_bytes(dtype)) && aligned_to(y, dtype_bytes(dtype)) &&
-                    aligned_to(dy, dtype_bytes(dtype)),
-                "dout, y and dy must be aligned to their type");
+                    aligned_to(dy, dtype_bytes(dtype)) && aligned_to(offsets, 4) && aligned_to(w, 4) &&
+                    aligned_to(inv_perm, 4) && aligned_to(dw, 4),
+                "dout, y, dy, offsets, w, inv_perm and dw must be aligned to their types");
     const unsigned grid = row_grid((int64_t)T * k, kBackGrid);
     const int unit = std::min(std::min(row_unit(dtype, H, dout), row_unit(dtype, H, y)), row_unit(dtype, H, dy));
     return with_dtype(dtype, [&](auto a) {
