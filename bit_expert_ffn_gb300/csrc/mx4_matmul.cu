@@ -347,6 +347,26 @@ __device__ __forceinline__ void load32(const uint8_t *src, bool in, uint32_t (&v
                      : "l"(src));
 }
 
+// Groups of offsets that decrease or leave the rows: each begins no earlier than
+// the one before it ends, so no row is in two of them, and their tiles are no
+// more than good offsets' (which the launch counts on).  One thread, from the
+// clipped starts in S.
+__device__ __noinline__ void end_to_end(const Params &p, Shared &S)
+{
+    if (blockIdx.x == 0) set_status(p.status, MOE_ERR_BOUNDS);
+    const int last = min(max(__ldg(p.offsets + p.E), 0), p.rows);
+    int end = S.start[0], tiles = 0;
+    for (int e = 0; e < p.E; e++) {
+        const int next = max(end, e + 1 < p.E ? S.start[e + 1] : last);
+        S.start[e] = end;
+        S.count[e] = next - end;
+        S.tile0[e] = tiles;
+        tiles += quotient(next - end + p.bn - 1, p.bn_m, p.bn_shift);
+        end = next;
+    }
+    S.tile0[p.E] = tiles;
+}
+
 template <class O, bool kSwiglu>
 __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_constant__ Params p,
                                                                 const __grid_constant__ CUtensorMap mw,
@@ -383,6 +403,7 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
     // row tiles before each expert: four experts per thread, then a scan
     if (p.offsets && threadIdx.x < MAX_E / 4) {
         int off[5], n[4], sum = 0;
+        bool bad = false;
         const int e0 = threadIdx.x * 4;
 #pragma unroll
         for (int i = 0; i < 5; i++) off[i] = e0 + i <= p.E ? __ldg(p.offsets + e0 + i) : 0;
@@ -392,28 +413,30 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
             const int a = min(max(off[i], 0), p.rows), b = min(max(off[i + 1], 0), p.rows);
             const int cnt = e0 + i < p.E ? max(0, b - a) : 0;
             if (e0 + i < p.E) {
-                if (blockIdx.x == 0 && (off[i] < 0 || off[i + 1] < off[i] || off[i + 1] > p.rows))
-                    set_status(p.status, MOE_ERR_BOUNDS);
+                bad |= off[i] < 0 || off[i + 1] < off[i] || off[i + 1] > p.rows;
                 S.start[e0 + i] = a;
                 S.count[e0 + i] = cnt;
             }
             n[i] = sum;
             sum += quotient(cnt + p.bn - 1, p.bn_m, p.bn_shift);
         }
-        int incl = sum;
+        uint32_t incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += v;
         }
-        if (lane == 31) S.warp_tot[warp] = incl;
-        tc::named_sync(1, MAX_E / 4);
-        int base = incl - sum;
-        for (int i = 0; i < warp; i++) base += S.warp_tot[i];
+        if (lane == 31) S.warp_tot[warp] = (int)incl;
+        if (tc::named_sync_or(1, MAX_E / 4, bad)) {
+            if (threadIdx.x == 0) end_to_end(p, S);
+        } else {
+            int base = (int)incl - sum;
+            for (int i = 0; i < warp; i++) base += S.warp_tot[i];
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-            if (e0 + i <= p.E) S.tile0[e0 + i] = base + n[i];
-        if (p.E == MAX_E && e0 + 4 == MAX_E) S.tile0[MAX_E] = base + sum;
+            for (int i = 0; i < 4; i++)
+                if (e0 + i <= p.E) S.tile0[e0 + i] = base + n[i];
+            if (p.E == MAX_E && e0 + 4 == MAX_E) S.tile0[MAX_E] = base + sum;
+        }
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -611,7 +634,7 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
             if (lane == 0) tc::mbar_arrive(&S.acc_empty[acc]);
         }
         if (p.offsets) {  // rows of no group
-            const int z0 = max(0, min(p.rows, __ldg(p.offsets + p.E)));
+            const int z0 = S.start[p.E - 1] + S.count[p.E - 1];
             zero_bytes(static_cast<typename O::T *>(p.out) + (int64_t)z0 * p.N, (int64_t)(p.rows - z0) * p.N * O::kBytes,
                        (int64_t)blockIdx.x * (EPI_WARPS * 32) + (threadIdx.x - EPI_WARP0 * 32), (int64_t)gridDim.x * (EPI_WARPS * 32));
         }
@@ -746,9 +769,7 @@ extern "C" moe_status moe_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_sc
     // at most this many items: every group's last row tile may be short
     const int64_t row_tiles = offsets ? std::min(E, rows) + rows / p.bn : (rows + p.bn - 1) / p.bn;
     const int64_t items = row_tiles * p.n_tiles;
-    // (item numbers stay in 32 bits whatever the offsets say)
-    MOE_REQUIRE((int64_t)E * ((rows + p.bn - 1) / p.bn) * p.n_tiles <= (1 << 30), "too many tiles (rows=%d N=%d E=%d)", rows,
-                N, E);
+    MOE_REQUIRE(items <= (1 << 30), "too many tiles (rows=%d N=%d E=%d)", rows, N, E);
     p.total = (int)items;
     reciprocal(p.n_tiles, &p.tiles_m, &p.tiles_shift);
     reciprocal(p.bn, &p.bn_m, &p.bn_shift);

@@ -576,7 +576,9 @@ typedef enum moe_mx4_epilogue {
  * offsets [E+1] as moe_permute gives them, or NULL when E = 1 (all rows).  Rows
  * at and past offsets[E] are set to zero.  out [rows][N], any N >= 1.  Offsets
  * that decrease or leave [0, rows] set *dev_status = MOE_ERR_BOUNDS and are
- * clipped; a wait that runs out (about 2 s) sets MOE_ERR_TIMEOUT.  E <= 1024.
+ * clipped, and a group then begins no earlier than the one before it ends; a
+ * wait that runs out (about 2 s) sets MOE_ERR_TIMEOUT.  E <= 1024, and at most
+ * 2^30 tiles (128 columns, or 64 with SwiGLU, times a tile's rows).
  */
 moe_status moe_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_scales, int E, int N, int K,
                           const uint8_t *x_codes, const uint8_t *x_scales, int rows, const int32_t *offsets,
