@@ -633,10 +633,13 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_matmul_kernel(const __grid_con
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&S.acc_empty[acc]);
         }
-        if (p.offsets) {  // rows of no group
+        if (p.offsets) {  // rows of no group: before the first and after the last
             const int z0 = S.start[p.E - 1] + S.count[p.E - 1];
-            zero_bytes(static_cast<typename O::T *>(p.out) + (int64_t)z0 * p.N, (int64_t)(p.rows - z0) * p.N * O::kBytes,
-                       (int64_t)blockIdx.x * (EPI_WARPS * 32) + (threadIdx.x - EPI_WARP0 * 32), (int64_t)gridDim.x * (EPI_WARPS * 32));
+            const int64_t rank = (int64_t)blockIdx.x * (EPI_WARPS * 32) + (threadIdx.x - EPI_WARP0 * 32);
+            const int64_t threads = (int64_t)gridDim.x * (EPI_WARPS * 32);
+            auto *out = static_cast<typename O::T *>(p.out);
+            zero_bytes(out + (int64_t)z0 * p.N, (int64_t)(p.rows - z0) * p.N * O::kBytes, rank, threads);
+            if (S.start[0]) zero_bytes(out, (int64_t)S.start[0] * p.N * O::kBytes, rank, threads);
         }
     }
     tc::tc_fence_before();

@@ -573,11 +573,12 @@ typedef enum moe_mx4_epilogue {
  *   out[p][n] = sum_k x[p][k] W_e[n][k],  e the group with offsets[e] <= p <
  *   offsets[e+1]
  * x is a [rows][K] and W one [E * N (or 2N)][K] matrix of the format above;
- * offsets [E+1] as moe_permute gives them, or NULL when E = 1 (all rows).  Rows
- * at and past offsets[E] are set to zero.  out [rows][N], any N >= 1.  Offsets
- * that decrease or leave [0, rows] set *dev_status = MOE_ERR_BOUNDS and are
- * clipped, and a group then begins no earlier than the one before it ends; a
- * wait that runs out (about 2 s) sets MOE_ERR_TIMEOUT.  E <= 1024, and at most
+ * offsets [E+1] as moe_permute gives them (or a slice of them: offsets[0] need
+ * not be 0), or NULL when E = 1 (all rows).  Rows of no group, before offsets[0]
+ * or at and past offsets[E], are set to zero.  out [rows][N], any N >= 1.
+ * Offsets that decrease or leave [0, rows] set *dev_status = MOE_ERR_BOUNDS and
+ * are clipped, and a group then begins no earlier than the one before it ends;
+ * a wait that runs out (about 2 s) sets MOE_ERR_TIMEOUT.  E <= 1024, and at most
  * 2^30 tiles (128 columns, or 64 with SwiGLU, times a tile's rows).
  */
 moe_status moe_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_scales, int E, int N, int K,

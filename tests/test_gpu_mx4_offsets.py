@@ -72,3 +72,15 @@ def test_most_groups_out_of_order(moe):
     m.moe_mx4_matmul(*bufs[:2], E, N, K, *bufs[2:], rows, dev(np.array([0, rows] * (E // 2) + [0], np.int32)), out, dev_status=st)
     assert m.moe_check_status(st) == m.MOE_ERR_BOUNDS
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("offsets,rows,N,K", [
+    ([3, 7, 7, 12], 12, 96, 160), ([1, 1, 2, 2], 5, 33, 288), ([40, 300, 300, 301], 310, 70, 64), ([6, 6, 6, 6], 6, 130, 96),
+    ([1000, 1002, 1003, 1040], 1040, 257, 4096),
+])
+def test_a_slice_of_offsets(moe, offsets, rows, N, K, dtype, swiglu):
+    """The first group begins past row 0: the rows before it are zero as those after the last."""
+    rng = np.random.default_rng(rows + N)
+    product(rng, 3, N, K, np.array(offsets, np.int32), rows, dtype, swiglu, spread=0)
