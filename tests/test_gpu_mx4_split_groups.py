@@ -1,6 +1,6 @@
 """Grouped products of few rows and a long K, whose K a cluster of CTAs shares: groups empty, of one to three rows, of
 more rows than a tile, fewer rows than CTAs, rows of no group.  (On 152 SMs the plan gives 64 of the 90 shapes eight
-CTAs, 20 four and 5 two, three in four of them at less than 0.75 of the unsplit cost.)"""
+CTAs, 20 four and 5 two, 78 of the 90 at less than 0.75 of the unsplit cost.)"""
 import numpy as np
 import pytest
 import torch
