@@ -101,7 +101,7 @@ NormPlan norm_plan(int T, int H, int res_bytes, int act_bytes, bool backward, bo
     const int per_sm = q.nv > 1 ? 512 : backward ? 768 : 1024;
     int resident = std::max(1, std::min(32, per_sm / q.threads));
     if (q.smem) resident = std::max(1, std::min<int>(resident, (int)((kNormRingBytes + 20 * 1024) / (q.smem + 1024))));
-    q.grid = (int)std::min<int64_t>((T + groups - 1) / groups, (int64_t)sm_count() * resident);
+    q.grid = (int)std::min<int64_t>(((int64_t)T + groups - 1) / groups, (int64_t)sm_count() * resident);
     return q;
 }
 
