@@ -180,31 +180,66 @@ def _ptr(t):
     return t.data_ptr() if t.numel() else None
 
 
-_BYTES = {MOE_F32: 4, MOE_BF16: 2, MOE_F16: 2}
+_INT32, _BYTE = "int32", "uint8"  # element kinds of _packed, beside the moe_dtypes
 
 
-def _packed(t, name, n, size):
-    """The pointer of a packed buffer of at least n elements of `size` bytes (a tensor), or of a raw address."""
-    if t.__class__ is int or t is None:
+class _Kinds(dict):
+    """Element kind -> the torch types that hold it (the calls also take 16-bit values as bit patterns)."""
+
+    def __missing__(self, kind):
+        import torch
+
+        bits = (torch.int16, torch.uint16)
+        small = [getattr(torch, n) for n in ("float8_e8m0fnu", "float4_e2m1fn_x2") if hasattr(torch, n)]
+        self.update({MOE_F32: (torch.float32,), MOE_BF16: (torch.bfloat16, *bits), MOE_F16: (torch.float16, *bits),
+                     _INT32: (torch.int32,), _BYTE: (torch.uint8, torch.int8, *small)})
+        return self.get(kind, ())
+
+
+_KINDS = _Kinds()
+
+
+class _Host:
+    """In an address's place: a tensor that is not on the GPU.  It cannot be passed, and _call reports it, by which time
+    the other arguments are known to be of the right types and sizes."""
+
+    def __init__(self, name, t):
+        self.what = f"{name} must be on the GPU (got a tensor on {t.device})"
+
+
+def _packed(t, name, n, kind):
+    """The pointer of a packed buffer of at least n elements of a kind (a tensor), or of a raw address."""
+    if t is None or t.__class__ is int:
         return t
-    if t.is_contiguous() and t.element_size() == size and t.numel() >= n:
-        return t.data_ptr() if n else None
-    raise MoeError(MOE_ERR_INVALID_ARG, f"{name} must be a packed tensor of at least {n} elements of {size} bytes "
+    if t.dtype in _KINDS[kind] and t.is_contiguous() and t.numel() >= n:
+        return (t.data_ptr() if t.is_cuda else _Host(name, t)) if n else None
+    want = " or ".join(str(d)[6:] for d in _KINDS[kind]) or f"dtype {kind}"
+    raise MoeError(MOE_ERR_INVALID_ARG, f"{name} must be a packed tensor of at least {n} elements of {want} "
                                         f"(got {tuple(t.shape)}, strides {t.stride()}, {t.dtype})")
 
 
 def _rows(t, name, n, cols, dtype):
     """Pointer and row stride of n rows of `cols` elements: a packed tensor, a 2D one whose rows are packed (stride 0
     repeats one row), or a raw address of packed rows."""
-    if t.__class__ is int or t is None:
+    if t is None or t.__class__ is int:
         return t, cols
-    size = _BYTES.get(dtype, 0)
-    if t.is_contiguous() and t.element_size() == size and t.numel() >= n * cols:
-        return t.data_ptr() if n else None, cols
-    if t.dim() == 2 and t.element_size() == size and t.shape[0] >= n and t.shape[1] == cols and (t.stride(1) == 1
-                                                                                                or cols == 1):
-        return (t.data_ptr(), t.stride(0) if n > 1 else cols) if n else (None, cols)
-    return _packed(t, name, n * cols, size), cols
+    if t.dtype in _KINDS[dtype]:
+        if t.is_contiguous():
+            if t.numel() >= n * cols:
+                return (t.data_ptr() if t.is_cuda else _Host(name, t)) if n else None, cols
+        elif t.dim() == 2 and t.shape[0] >= n and t.shape[1] == cols and (t.stride(1) == 1 or cols == 1):
+            return (t.data_ptr() if t.is_cuda else _Host(name, t)) if n else None, t.stride(0) if n > 1 else cols
+    return _packed(t, name, n * cols, dtype), cols
+
+
+def _workspace(t, size):
+    """The pointer of a workspace said to hold `size` bytes (a tensor of any type), or of a raw address."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.is_contiguous() and t.numel() * t.element_size() >= size:
+        return (t.data_ptr() if t.is_cuda else _Host("ws", t)) if size else None
+    raise MoeError(MOE_ERR_INVALID_ARG, f"ws must be a packed tensor of at least ws_bytes = {size} bytes "
+                                        f"(got {tuple(t.shape)}, strides {t.stride()}, {t.dtype})")
 
 
 _raw_stream = None  # torch's current stream handle of a device, and the current device, once a GPU is there
@@ -225,6 +260,18 @@ def _stream(stream=None):
         if None not in fns:
             _raw_stream = fns
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _call(fn, *args):
+    try:
+        status = fn(*args)
+    except ctypes.ArgumentError:
+        for a in args:
+            if a.__class__ is _Host:
+                raise MoeError(MOE_ERR_INVALID_ARG, f"{fn.__name__}: {a.what}") from None
+        raise
+    if status:
+        _check(status, fn.__name__)
 
 
 def _size(fn, *args) -> int:
@@ -369,34 +416,29 @@ def moe_selftest_barrier(extra_arrivals, timeout_ms, ws, ws_bytes, dev_status=No
 def moe_dispatch(x, dtype, T, H, k, E, offsets, inv_perm, out, stream=None):
     """out[inv_perm[t, j]] = x[t]; rows of no pair are zero.  x: [T][H], packed rows at any row stride."""
     xp, xs = _rows(x, "x", T, H, dtype)
-    _check((_lib or load()).moe_dispatch(xp, dtype, xs, T, H, k, E, _packed(offsets, "offsets", E + 1, 4),
-                              _packed(inv_perm, "inv_perm", T * k, 4), _packed(out, "out", T * k * H, _BYTES.get(dtype, 0)),
-                              _stream(stream)), "moe_dispatch")
+    _call((_lib or load()).moe_dispatch, xp, dtype, xs, T, H, k, E, _packed(offsets, "offsets", E + 1, _INT32),
+          _packed(inv_perm, "inv_perm", T * k, _INT32), _packed(out, "out", T * k * H, dtype), _stream(stream))
 
 
 def moe_dispatch_backward(drows, dtype, T, H, k, inv_perm, dx, stream=None):
     """dx[t] = sum_j drows[inv_perm[t, j]]."""
-    b = _BYTES.get(dtype, 0)
-    _check((_lib or load()).moe_dispatch_backward(_packed(drows, "drows", T * k * H, b), dtype, T, H, k,
-                                       _packed(inv_perm, "inv_perm", T * k, 4), _packed(dx, "dx", T * H, b),
-                                       _stream(stream)), "moe_dispatch_backward")
+    _call((_lib or load()).moe_dispatch_backward, _packed(drows, "drows", T * k * H, dtype), dtype, T, H, k,
+          _packed(inv_perm, "inv_perm", T * k, _INT32), _packed(dx, "dx", T * H, dtype), _stream(stream))
 
 
 def moe_combine(y, dtype, T, H, k, w, inv_perm, out, out_dtype=MOE_F32, accumulate=False, stream=None):
     """out[t] (+)= sum_j w[t, j] * y[inv_perm[t, j]]."""
-    _check((_lib or load()).moe_combine(_packed(y, "y", T * k * H, _BYTES.get(dtype, 0)), dtype, T, H, k, _packed(w, "w", T * k, 4),
-                             _packed(inv_perm, "inv_perm", T * k, 4),
-                             _packed(out, "out", T * H, _BYTES.get(out_dtype, 0)), out_dtype, int(accumulate),
-                             _stream(stream)), "moe_combine")
+    _call((_lib or load()).moe_combine, _packed(y, "y", T * k * H, dtype), dtype, T, H, k, _packed(w, "w", T * k, MOE_F32),
+          _packed(inv_perm, "inv_perm", T * k, _INT32), _packed(out, "out", T * H, out_dtype), out_dtype, int(accumulate),
+          _stream(stream))
 
 
 def moe_combine_backward(dout, y, dtype, T, H, k, E, offsets, w, inv_perm, dy, dw, stream=None):
     """dy[inv_perm[t, j]] = w[t, j] * dout[t], dw[t, j] = <dout[t], y[inv_perm[t, j]]>."""
-    b = _BYTES.get(dtype, 0)
-    _check((_lib or load()).moe_combine_backward(_packed(dout, "dout", T * H, b), _packed(y, "y", T * k * H, b), dtype, T, H, k, E,
-                                      _packed(offsets, "offsets", E + 1, 4), _packed(w, "w", T * k, 4),
-                                      _packed(inv_perm, "inv_perm", T * k, 4), _packed(dy, "dy", T * k * H, b),
-                                      _packed(dw, "dw", T * k, 4), _stream(stream)), "moe_combine_backward")
+    _call((_lib or load()).moe_combine_backward, _packed(dout, "dout", T * H, dtype), _packed(y, "y", T * k * H, dtype),
+          dtype, T, H, k, E, _packed(offsets, "offsets", E + 1, _INT32), _packed(w, "w", T * k, MOE_F32),
+          _packed(inv_perm, "inv_perm", T * k, _INT32), _packed(dy, "dy", T * k * H, dtype), _packed(dw, "dw", T * k, MOE_F32),
+          _stream(stream))
 
 
 # ----------------------------------------------------------------- 4-bit floating point matrices
@@ -409,25 +451,23 @@ def moe_mx4_size(rows: int, cols: int):
 
 
 def _mx4(codes, scales, name, rows, cols):
-    return (_packed(codes, name + "codes", rows * (cols // 2), 1),
-            _packed(scales, name + "scales", rows * ((cols + 1023) // 1024) * 32, 1))
+    return (_packed(codes, name + "codes", rows * (cols // 2), _BYTE),
+            _packed(scales, name + "scales", rows * ((cols + 1023) // 1024) * 32, _BYTE))
 
 
 def moe_mx4_quantise(x, dtype, rows, cols, codes, scales, dev_status=None, stream=None):
     """x [rows][cols] (rows packed, any row stride) to e2m1 codes and e8m0 scales (uint8 tensors of moe_mx4_size)."""
-    if not isinstance(x, int) and x is not None and x.dim() > 2 and x.is_contiguous():
-        x = x.view(-1, cols) if x.shape[-1] == cols else x
     xp, xs = _rows(x, "x", rows, cols, dtype)
     cp, sp = _mx4(codes, scales, "", rows, cols)
-    _check((_lib or load()).moe_mx4_quantise(xp, dtype, xs, rows, cols, cp, sp, _ptr(dev_status), _stream(stream)),
-           "moe_mx4_quantise")
+    _call((_lib or load()).moe_mx4_quantise, xp, dtype, xs, rows, cols, cp, sp, _packed(dev_status, "dev_status", 1, _INT32),
+          _stream(stream))
 
 
 def moe_mx4_dequantise(codes, scales, rows, cols, out, dtype=MOE_BF16, stream=None):
     """The values that codes and scales stand for."""
     cp, sp = _mx4(codes, scales, "", rows, cols)
-    _check((_lib or load()).moe_mx4_dequantise(cp, sp, rows, cols, _packed(out, "out", rows * cols, _BYTES.get(dtype, 0)), dtype,
-                                    _stream(stream)), "moe_mx4_dequantise")
+    _call((_lib or load()).moe_mx4_dequantise, cp, sp, rows, cols, _packed(out, "out", rows * cols, dtype), dtype,
+          _stream(stream))
 
 
 def moe_mx4_matmul(w_codes, w_scales, E, N, K, x_codes, x_scales, rows, offsets, out, out_dtype=MOE_F32,
@@ -435,9 +475,9 @@ def moe_mx4_matmul(w_codes, w_scales, E, N, K, x_codes, x_scales, rows, offsets,
     """out[p] = x[p] W_e^T (or silu(gate) * up of it) for the rows p of each group e; offsets None: one group (E = 1)."""
     wc, ws = _mx4(w_codes, w_scales, "w_", E * N * (2 if epilogue == MOE_MX4_SWIGLU else 1), K)
     xc, xs = _mx4(x_codes, x_scales, "x_", rows, K)
-    _check((_lib or load()).moe_mx4_matmul(wc, ws, E, N, K, xc, xs, rows, _packed(offsets, "offsets", E + 1, 4),
-                                _packed(out, "out", rows * N, _BYTES.get(out_dtype, 0)), out_dtype, epilogue,
-                                _ptr(dev_status), _stream(stream)), "moe_mx4_matmul")
+    _call((_lib or load()).moe_mx4_matmul, wc, ws, E, N, K, xc, xs, rows, _packed(offsets, "offsets", E + 1, _INT32),
+          _packed(out, "out", rows * N, out_dtype), out_dtype, epilogue, _packed(dev_status, "dev_status", 1, _INT32),
+          _stream(stream))
 
 
 # ----------------------------------------------------------------- norms around a block
@@ -450,10 +490,9 @@ def moe_block_norm(x, res_dtype, b, dtype, T, H, w_post, w_pre, gate, gate_kind,
     """y = x + alpha * gate * w_post * rmsnorm(b), u = w_pre * rmsnorm(y).  x and b: packed rows at any row stride."""
     xp, xs = _rows(x, "x", T, H, res_dtype)
     bp, bs = _rows(b, "b", T, H, dtype)
-    _check((_lib or load()).moe_block_norm(xp, res_dtype, xs, bp, dtype, bs, T, H, _packed(w_post, "w_post", H, 4),
-                                _packed(w_pre, "w_pre", H, 4), _packed(gate, "gate", _gate_size(gate_kind, T, H), 4),
-                                gate_kind, alpha, eps, _packed(y, "y", T * H, _BYTES.get(res_dtype, 0)),
-                                _packed(u, "u", T * H, _BYTES.get(dtype, 0)), _stream(stream)), "moe_block_norm")
+    _call((_lib or load()).moe_block_norm, xp, res_dtype, xs, bp, dtype, bs, T, H, _packed(w_post, "w_post", H, MOE_F32),
+          _packed(w_pre, "w_pre", H, MOE_F32), _packed(gate, "gate", _gate_size(gate_kind, T, H), MOE_F32), gate_kind, alpha,
+          eps, _packed(y, "y", T * H, res_dtype), _packed(u, "u", T * H, dtype), _stream(stream))
 
 
 def moe_block_norm_backward_workspace_size(T, H, gate_kind=MOE_GATE_NONE):
@@ -465,13 +504,13 @@ def moe_block_norm_backward(x, res_dtype, b, dtype, T, H, w_post, w_pre, gate, g
     """Gradients of moe_block_norm for dy and du (either may be None)."""
     xp, xs = _rows(x, "x", T, H, res_dtype)
     bp, bs = _rows(b, "b", T, H, dtype)
-    rb, ab, n = _BYTES.get(res_dtype, 0), _BYTES.get(dtype, 0), _gate_size(gate_kind, T, H)
-    _check((_lib or load()).moe_block_norm_backward(
-        xp, res_dtype, xs, bp, dtype, bs, T, H, _packed(w_post, "w_post", H, 4), _packed(w_pre, "w_pre", H, 4),
-        _packed(gate, "gate", n, 4), gate_kind, alpha, eps, _packed(dy, "dy", T * H, rb), _packed(du, "du", T * H, ab),
-        _packed(dx, "dx", T * H, rb), _packed(db, "db", T * H, ab), _packed(dw_post, "dw_post", H, 4),
-        _packed(dw_pre, "dw_pre", H, 4), _packed(dgate, "dgate", n, 4), _ptr(ws), ws_bytes, _stream(stream)),
-        "moe_block_norm_backward")
+    n = _gate_size(gate_kind, T, H)
+    _call((_lib or load()).moe_block_norm_backward, xp, res_dtype, xs, bp, dtype, bs, T, H,
+          _packed(w_post, "w_post", H, MOE_F32), _packed(w_pre, "w_pre", H, MOE_F32), _packed(gate, "gate", n, MOE_F32),
+          gate_kind, alpha, eps,
+          _packed(dy, "dy", T * H, res_dtype), _packed(du, "du", T * H, dtype), _packed(dx, "dx", T * H, res_dtype),
+          _packed(db, "db", T * H, dtype), _packed(dw_post, "dw_post", H, MOE_F32), _packed(dw_pre, "dw_pre", H, MOE_F32),
+          _packed(dgate, "dgate", n, MOE_F32), _workspace(ws, ws_bytes), ws_bytes, _stream(stream))
 
 
 def header_functions():
