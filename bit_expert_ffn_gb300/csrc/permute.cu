@@ -12,12 +12,12 @@
 namespace moe {
 
 constexpr int kPermChunk = 2048;     // pairs per chunk in the multi-CTA path
-constexpr int kPermSmallMax = 4096;  // single-CTA path up to this many pairs
 constexpr int kPlaceWarps = 8;       // warps per chunk in the multi-CTA path
-// A cluster in between: 4,000 pairs over 512 experts take it 5.3 us, a single CTA
-// 8.9; 20,480 take it 8.3, the three passes 11.9 (40,960: 12.0 and 11.5).
+// A single CTA up to 1,024 pairs, a cluster from there: 4,000 pairs over 512
+// experts take it 5.3 us, a single CTA 8.9; 20,480 take it 8.3, the three passes
+// 11.9 (40,960: 12.0 and 11.5).  Only the three passes need a workspace.
 constexpr int kClusterCtas = 8;
-constexpr int kPermClusterMin = 1025, kPermClusterMax = 32768;
+constexpr int kPermSmallMax = 1024, kPermClusterMax = 32768;
 
 // Warp-serial stable placement of pairs [f0, f1) starting from per-expert
 // cursors `cur` (shared memory).  Lanes take 32 pairs at a time in order.
@@ -299,12 +299,64 @@ extern "C" moe_status moe_shard_ids(const int32_t *ids, int64_t n, int e0, int e
     return check_launch("shard_ids");
 }
 
+namespace moe {
+
+// The sort of up to kPermClusterMax pairs: no scratch in global memory.
+static moe_status permute_few(const int32_t *ids, int n, int E, int32_t *offsets, int32_t *perm, int32_t *inv_perm,
+                              int32_t *dev_status, cudaStream_t s)
+{
+    if (n <= kPermSmallMax) {
+        // as many runs of 32 or more pairs as 48,000 bytes of counters hold
+        const int most = std::min(std::min(32, 12000 / E), (n + 31) / 32);
+        const int seg = (n + most * 32 - 1) / (most * 32) * 32;
+        const int warps = (n + seg - 1) / seg;
+        permute_small_kernel<<<1, 1024, (size_t)warps * E * sizeof(int32_t), s>>>(ids, n, E, warps, seg, offsets, perm, inv_perm,
+                                                                                dev_status);
+        return check_launch("permute_small");
+    }
+    const int per_cta = (n + kClusterCtas * 32 - 1) / (kClusterCtas * 32) * 32;
+    const int most = std::min(std::min(32, 11000 / E), per_cta / 32);  // runs, in 44,000 bytes of counters
+    const int seg = (per_cta + most * 32 - 1) / (most * 32) * 32;
+    const int warps = (per_cta + seg - 1) / seg;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kClusterCtas);
+    cfg.blockDim = dim3(1024);
+    cfg.dynamicSmemBytes = (size_t)warps * E * sizeof(int32_t);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kClusterCtas;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, permute_cluster_kernel, ids, n, E, per_cta, warps, seg, offsets, perm, inv_perm,
+                                    dev_status));
+    return check_launch("permute_cluster");
+}
+
+// The sort of any number of pairs, in three passes over counts and base, [chunks][E] each.
+static moe_status permute_many(const int32_t *ids, int64_t n, int E, int32_t *counts, int32_t *base, int32_t *offsets,
+                               int32_t *perm, int32_t *inv_perm, int32_t *dev_status, cudaStream_t s)
+{
+    const int64_t c = n_chunks_for(n);
+    permute_count_kernel<<<(unsigned)c, 256, 0, s>>>(ids, n, E, counts, dev_status);
+    moe_status st = check_launch("permute_count");
+    if (st != MOE_OK) return st;
+    permute_prefix_kernel<<<(E + 31) / 32, 1024, 0, s>>>(counts, (int)c, E, base);
+    st = check_launch("permute_prefix");
+    if (st != MOE_OK) return st;
+    permute_place_kernel<<<(unsigned)c, kPlaceWarps * 32, 0, s>>>(ids, n, E, counts, base, offsets, perm, inv_perm);
+    return check_launch("permute_place");
+}
+
+}  // namespace moe
+
 extern "C" moe_status moe_permute_workspace_size(int T, int k, int E, size_t *bytes)
 {
     MOE_REQUIRE(bytes, "bytes is NULL");
     MOE_REQUIRE(T >= 0 && k >= 1 && E >= 1 && E <= 1024, "T >= 0, k >= 1, 1 <= E <= 1024");
     int64_t n = (int64_t)T * k;
-    if (n <= kPermSmallMax) {
+    if (n <= kPermClusterMax) {
         *bytes = 0;
         return MOE_OK;
     }
@@ -328,54 +380,18 @@ extern "C" moe_status moe_permute(const int32_t *ids, int T, int k, int E, int32
         return MOE_OK;
     }
     MOE_REQUIRE(ids && perm && inv_perm, "NULL pointer");
-    int64_t c = n_chunks_for(n);
-    size_t part = align256((size_t)c * E * sizeof(int32_t));
-    if (n > kPermSmallMax && (!ws || ws_bytes < 2 * part))
+    if (n <= kPermClusterMax) return permute_few(ids, (int)n, E, offsets, perm, inv_perm, dev_status, s);
+    size_t part = align256((size_t)n_chunks_for(n) * E * sizeof(int32_t));
+    if (!ws || ws_bytes < 2 * part)
         return fail(MOE_ERR_WORKSPACE, "permute needs %zu bytes (%.2f MiB) of workspace, got %zu", 2 * part,
                     mib(2.0 * part), ws ? ws_bytes : (size_t)0);
-    if (n >= kPermClusterMin && n <= kPermClusterMax) {
-        const int per_cta = (int)((n + kClusterCtas * 32 - 1) / (kClusterCtas * 32)) * 32;
-        const int most = std::min(std::min(32, 11000 / E), per_cta / 32);  // runs, in 44,000 bytes of counters
-        const int seg = (per_cta + most * 32 - 1) / (most * 32) * 32;
-        const int warps = (per_cta + seg - 1) / seg;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(kClusterCtas);
-        cfg.blockDim = dim3(1024);
-        cfg.dynamicSmemBytes = (size_t)warps * E * sizeof(int32_t);
-        cfg.stream = s;
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = kClusterCtas;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-        MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, permute_cluster_kernel, ids, (int)n, E, per_cta, warps, seg, offsets, perm,
-                                        inv_perm, dev_status));
-        return check_launch("permute_cluster");
-    }
-    if (n <= kPermSmallMax) {
-        // as many runs of 32 or more pairs as 48,000 bytes of counters hold
-        const int most = (int)std::min<int64_t>(std::min(32, 12000 / E), (n + 31) / 32);
-        const int seg = (int)((n + most * 32 - 1) / (most * 32)) * 32;
-        const int warps = (int)((n + seg - 1) / seg);
-        permute_small_kernel<<<1, 1024, (size_t)warps * E * sizeof(int32_t), s>>>(ids, (int)n, E, warps, seg, offsets, perm,
-                                                                                inv_perm, dev_status);
-        return check_launch("permute_small");
-    }
     int32_t *counts = static_cast<int32_t *>(ws);
     int32_t *base = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + part);
-    permute_count_kernel<<<(unsigned)c, 256, 0, s>>>(ids, n, E, counts, dev_status);
-    moe_status st = check_launch("permute_count");
-    if (st != MOE_OK) return st;
-    permute_prefix_kernel<<<(E + 31) / 32, 1024, 0, s>>>(counts, (int)c, E, base);
-    st = check_launch("permute_prefix");
-    if (st != MOE_OK) return st;
-    permute_place_kernel<<<(unsigned)c, kPlaceWarps * 32, 0, s>>>(ids, n, E, counts, base, offsets, perm, inv_perm);
-    return check_launch("permute_place");
+    return permute_many(ids, n, E, counts, base, offsets, perm, inv_perm, dev_status, s);
 }
 
 // --------------------------------------------------------------------------
-// moe_permute_noalloc: the three-pass sort above with its scratch in a fixed
+// moe_permute_noalloc: the same sorts, the scratch of the three passes in a fixed
 // device array of this library instead of a caller workspace.
 // --------------------------------------------------------------------------
 #include <cuda.h>
@@ -455,17 +471,10 @@ extern "C" moe_status moe_permute_noalloc(const int32_t *ids, int T, int k, int 
         return MOE_OK;
     }
     MOE_REQUIRE(ids && perm && inv_perm, "NULL pointer");
+    if (n <= kPermClusterMax) return permute_few(ids, (int)n, E, offsets, perm, inv_perm, dev_status, s);
     int32_t *scratch = nullptr;
     moe_status st = permute_scratch_address(&scratch);
     if (st != MOE_OK) return st;
-    int32_t *counts = scratch;                      // every cell read below is written
-    int32_t *base = scratch + kNoAllocScratchInts;  // earlier in the same call
-    permute_count_kernel<<<(unsigned)c, 256, 0, s>>>(ids, n, E, counts, dev_status);
-    st = check_launch("permute_count (no-alloc)");
-    if (st != MOE_OK) return st;
-    permute_prefix_kernel<<<(E + 31) / 32, 1024, 0, s>>>(counts, (int)c, E, base);
-    st = check_launch("permute_prefix (no-alloc)");
-    if (st != MOE_OK) return st;
-    permute_place_kernel<<<(unsigned)c, kPlaceWarps * 32, 0, s>>>(ids, n, E, counts, base, offsets, perm, inv_perm);
-    return check_launch("permute_place (no-alloc)");
+    // (every cell read is written earlier in the same call)
+    return permute_many(ids, n, E, scratch, scratch + kNoAllocScratchInts, offsets, perm, inv_perm, dev_status, s);
 }

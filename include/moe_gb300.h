@@ -275,7 +275,8 @@ moe_status moe_permute(const int32_t *ids, int T, int k, int E, int32_t *offsets
  * allocation may synchronise the device or fail under memory pressure.  This
  * call allocates nothing and takes no workspace: its scratch is a fixed array
  * of 2 x 32,768 int32 (256 KiB) inside the library, which every GPU that
- * loads the library holds until the process exits.
+ * loads the library holds until the process exits.  (moe_permute itself needs
+ * a workspace above 32,768 pairs only; up to there the two are one.)
  *   - Limit: ceil(T*k / 2048) * E <= 32,768 (e.g. T*k <= 65,536 pairs for
  *     E = 1024, <= 131,072 for E = 512); larger requests return
  *     MOE_ERR_INVALID_ARG with the sizes in the message.
@@ -285,10 +286,10 @@ moe_status moe_permute(const int32_t *ids, int T, int k, int E, int32_t *offsets
  *     context; a call under a new context (after cudaDeviceReset, say) looks
  *     it up again.  Make the first call on a device, and the first after a
  *     reset, before any stream capture.
- *   - Every call on a device shares the one array, and each call overwrites
- *     the cells it reads (nothing needs clearing between calls); calls whose
- *     kernels overlap on the GPU (other streams, other host threads) race on
- *     it, so serialise them.
+ *   - Every call of more than 32,768 pairs on a device shares the one array,
+ *     and each such call overwrites the cells it reads (nothing needs clearing
+ *     between calls); those whose kernels overlap on the GPU (other streams,
+ *     other host threads) race on it, so serialise them.
  */
 moe_status moe_permute_noalloc(const int32_t *ids, int T, int k, int E, int32_t *offsets,
                                int32_t *perm, int32_t *inv_perm, int32_t *dev_status,
