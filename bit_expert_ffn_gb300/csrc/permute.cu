@@ -13,11 +13,13 @@ namespace moe {
 
 constexpr int kPermChunk = 2048;     // pairs per chunk in the multi-CTA path
 constexpr int kPlaceWarps = 8;       // warps per chunk in the multi-CTA path
-// A single CTA up to 1,024 pairs, a cluster from there: 4,000 pairs over 512
+// Up to 128 pairs by counting (10 of them over 512 experts take 1.6 us, a single
+// CTA 2.5; 128 take 2.1 and 2.7).  A single CTA up to 1,024, a cluster from there: 4,000 pairs over 512
 // experts take it 5.3 us, a single CTA 8.9; 20,480 take it 8.3, the three passes
 // 11.9 (40,960: 12.0 and 11.5).  Only the three passes need a workspace.
 constexpr int kClusterCtas = 8;
 constexpr int kPermSmallMax = 1024, kPermClusterMax = 32768;
+constexpr int kPermRankMax = 128, kRankThreads = 128;
 
 // Warp-serial stable placement of pairs [f0, f1) starting from per-expert
 // cursors `cur` (shared memory).  Lanes take 32 pairs at a time in order.
@@ -110,6 +112,42 @@ __device__ int block_exclusive_scan(int v, int32_t *warp_tot, int &total)
     total = warp_tot[32];
     __syncthreads();
     return excl;
+}
+
+// A few pairs: every expert's offset and every pair's place is a count of the
+// keys before its own, id * kPermRankMax + pair, all of them in shared memory.
+// The first CTA places the pairs, the others take kRankThreads experts each;
+// none waits for another.
+__global__ void __launch_bounds__(kRankThreads) permute_rank_kernel(const int32_t *__restrict__ ids, int n, int E,
+                                                                    int32_t *__restrict__ offsets, int32_t *__restrict__ perm,
+                                                                    int32_t *__restrict__ inv, int32_t *status)
+{
+    __shared__ __align__(16) int32_t key[kPermRankMax];
+    const int tid = threadIdx.x;
+    const int id = tid < n ? ids[tid] : MOE_ID_NOT_LOCAL;
+    const bool valid = id >= 0 && id < E;
+    const int mine = valid ? id * kPermRankMax + tid : INT32_MAX;  // after every expert
+    if (!valid && id != MOE_ID_NOT_LOCAL && blockIdx.x == 0) set_status(status, MOE_ERR_BOUNDS);
+    if (tid < kPermRankMax) key[tid] = mine;
+    const int total = __syncthreads_count(valid);
+    auto before = [&](int x) {
+        int c = 0;
+#pragma unroll 4
+        for (int i = 0; i < n; i += 4) {
+            const int4 k = *reinterpret_cast<const int4 *>(key + i);
+            c += (k.x < x) + (k.y < x) + (k.z < x) + (k.w < x);
+        }
+        return c;
+    };
+    if (blockIdx.x > 0) {
+        const int e = ((int)blockIdx.x - 1) * kRankThreads + tid;
+        if (e <= E) offsets[e] = before(e * kPermRankMax);
+    } else if (tid < n) {
+        const int pos = valid ? before(mine) : -1;
+        inv[tid] = pos;
+        if (valid) perm[pos] = tid;
+        if (tid >= total) perm[tid] = -1;
+    }
 }
 
 // Single CTA (1024 threads): count, scan, place.
@@ -305,6 +343,11 @@ namespace moe {
 static moe_status permute_few(const int32_t *ids, int n, int E, int32_t *offsets, int32_t *perm, int32_t *inv_perm,
                               int32_t *dev_status, cudaStream_t s)
 {
+    if (n <= kPermRankMax) {
+        permute_rank_kernel<<<1 + (E + kRankThreads) / kRankThreads, kRankThreads, 0, s>>>(ids, n, E, offsets, perm, inv_perm,
+                                                                                         dev_status);
+        return check_launch("permute_rank");
+    }
     if (n <= kPermSmallMax) {
         // as many runs of 32 or more pairs as 48,000 bytes of counters hold
         const int most = std::min(std::min(32, 12000 / E), (n + 31) / 32);
