@@ -14,9 +14,10 @@ namespace moe {
 constexpr int kPermChunk = 2048;     // pairs per chunk in the multi-CTA path
 constexpr int kPlaceWarps = 8;       // warps per chunk in the multi-CTA path
 // Up to 128 pairs by counting (10 of them over 512 experts take 1.6 us, a single
-// CTA 2.5; 128 take 2.1 and 2.7).  A single CTA up to 1,024, a cluster from there: 4,000 pairs over 512
-// experts take it 5.3 us, a single CTA 8.9; 20,480 take it 8.3, the three passes
-// 11.9 (40,960: 12.0 and 11.5).  Only the three passes need a workspace.
+// CTA 2.5; 128 take 2.2 and 2.7).  A single CTA up to 1,024, a cluster from
+// there: 4,000 pairs over 512 experts take it 5.3 us, a single CTA 8.9; 20,480
+// take it 8.3, the three passes 11.9 (40,960: 12.0 and 11.5).  Only the three
+// passes need a workspace.
 constexpr int kClusterCtas = 8;
 constexpr int kPermSmallMax = 1024, kPermClusterMax = 32768;
 constexpr int kPermRankMax = 128, kRankThreads = 128;

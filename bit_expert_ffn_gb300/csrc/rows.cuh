@@ -22,11 +22,6 @@ struct F32 {
     }
     __device__ static float load(const T *p) { return *p; }
     __device__ static void store(T *p, float v) { *p = v; }
-    __device__ static void load8(const T *p, float (&v)[8])
-    {
-        const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    }
     __device__ static void store8(T *p, const float (&v)[8])
     {
         reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -64,7 +59,6 @@ struct Bf16 {
             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    __device__ static void load8(const T *p, float (&v)[8]) { unpack8(*reinterpret_cast<const uint4 *>(p), v); }
     __device__ static void store8(T *p, const float (&v)[8]) { *reinterpret_cast<uint4 *>(p) = pack8(v); }
     __device__ static void load4(const T *p, float *v)
     {
@@ -109,7 +103,6 @@ struct Fp16 {
             asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    __device__ static void load8(const T *p, float (&v)[8]) { unpack8(*reinterpret_cast<const uint4 *>(p), v); }
     __device__ static void store8(T *p, const float (&v)[8]) { *reinterpret_cast<uint4 *>(p) = pack8(v); }
     __device__ static void load4(const T *p, float *v)
     {
