@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(G::kThreads) __maxnreg__(G::kBackRegs) block_n
         }
         G::sum(q2, slots + 1);
         const float r2 = rsqrtf(q2[0] * inv_h + p.eps);
-        // (the factor r2 stays outside, here and below: its cube leaves fp32's range where rows and gradients do not)
+        // (no r cubed, here or below: it leaves fp32's range where rows and gradients do not)
         const float m2 = r2 * (r2 * q2[1] * inv_h);
         q[0] = 0.f;
         read_du();
@@ -122,9 +122,9 @@ __global__ void __launch_bounds__(G::kThreads) __maxnreg__(G::kBackRegs) block_n
             if (++s == p.stages) s = 0;
         }
         G::template store<R>(static_cast<typename R::T *>(p.y) + t * H, H, y);
-        const float m1 = r1 * (r1 * q[0] * inv_h);
+        const float m1 = f * (r1 * q[0] * inv_h);
 #pragma unroll
-        for (int i = 0; i < N; i++) b[i] = f * (gp[i] * y[i] - b[i] * m1);
+        for (int i = 0; i < N; i++) b[i] = f * y[i] * gp[i] - b[i] * r1 * m1;
         G::template store<A>(static_cast<typename A::T *>(p.u) + t * H, H, b);
         if (p.dgate_token && G::rank() == 0) p.dgate_token[t] = p.alpha * r1 * q[0];
     }
