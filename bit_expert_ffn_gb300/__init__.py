@@ -450,22 +450,22 @@ def moe_mx4_size(rows: int, cols: int):
     return cb.value, sb.value
 
 
-def _mx4(codes, scales, name, rows, cols):
-    return (_packed(codes, name + "codes", rows * (cols // 2), _BYTE),
-            _packed(scales, name + "scales", rows * ((cols + 1023) // 1024) * 32, _BYTE))
+def _mx4(codes, codes_name, scales, scales_name, rows, cols):
+    return (_packed(codes, codes_name, rows * (cols // 2), _BYTE),
+            _packed(scales, scales_name, rows * ((cols + 1023) // 1024) * 32, _BYTE))
 
 
 def moe_mx4_quantise(x, dtype, rows, cols, codes, scales, dev_status=None, stream=None):
     """x [rows][cols] (rows packed, any row stride) to e2m1 codes and e8m0 scales (uint8 tensors of moe_mx4_size)."""
     xp, xs = _rows(x, "x", rows, cols, dtype)
-    cp, sp = _mx4(codes, scales, "", rows, cols)
+    cp, sp = _mx4(codes, "codes", scales, "scales", rows, cols)
     _call((_lib or load()).moe_mx4_quantise, xp, dtype, xs, rows, cols, cp, sp, _packed(dev_status, "dev_status", 1, _INT32),
           _stream(stream))
 
 
 def moe_mx4_dequantise(codes, scales, rows, cols, out, dtype=MOE_BF16, stream=None):
     """The values that codes and scales stand for."""
-    cp, sp = _mx4(codes, scales, "", rows, cols)
+    cp, sp = _mx4(codes, "codes", scales, "scales", rows, cols)
     _call((_lib or load()).moe_mx4_dequantise, cp, sp, rows, cols, _packed(out, "out", rows * cols, dtype), dtype,
           _stream(stream))
 
@@ -473,8 +473,8 @@ def moe_mx4_dequantise(codes, scales, rows, cols, out, dtype=MOE_BF16, stream=No
 def moe_mx4_matmul(w_codes, w_scales, E, N, K, x_codes, x_scales, rows, offsets, out, out_dtype=MOE_F32,
                    epilogue=MOE_MX4_PLAIN, dev_status=None, stream=None):
     """out[p] = x[p] W_e^T (or silu(gate) * up of it) for the rows p of each group e; offsets None: one group (E = 1)."""
-    wc, ws = _mx4(w_codes, w_scales, "w_", E * N * (2 if epilogue == MOE_MX4_SWIGLU else 1), K)
-    xc, xs = _mx4(x_codes, x_scales, "x_", rows, K)
+    wc, ws = _mx4(w_codes, "w_codes", w_scales, "w_scales", E * N * (2 if epilogue == MOE_MX4_SWIGLU else 1), K)
+    xc, xs = _mx4(x_codes, "x_codes", x_scales, "x_scales", rows, K)
     _call((_lib or load()).moe_mx4_matmul, wc, ws, E, N, K, xc, xs, rows, _packed(offsets, "offsets", E + 1, _INT32),
           _packed(out, "out", rows * N, out_dtype), out_dtype, epilogue, _packed(dev_status, "dev_status", 1, _INT32),
           _stream(stream))

@@ -27,9 +27,10 @@
 // shared memory, in order.
 //
 // Measured: 81,920 rows x 2048 x 768 over 512 experts 127 us (797 MB, 6.3 TB/s: the
-// weights' bytes bound it), SwiGLU of 768 x 2048 176 us (1,070 MB, 6.1 TB/s); 8192 x 8192 x 8192 191 us (5.8 PFLOP/s: shared memory, a
-// step moves 44 KB in and out of it in 730 cycles); one row x 2048 x 2048 4.8 us (a
-// launch, the set-up and eight steps of 0.3 us in turn).
+// weights' bytes bound it), SwiGLU of 768 x 2048 176 us (1,070 MB, 6.1 TB/s); 8192 x
+// 8192 x 8192 191 us (5.8 PFLOP/s: shared memory, a step moves 44 KB in and out of
+// it in 730 cycles); one row x 2048 x 2048 4.8 us (a launch, the set-up and eight
+// steps of 0.3 us in turn).
 //
 // Every wait is bounded: after about 2 s the CTA records MOE_ERR_TIMEOUT and
 // stops.
