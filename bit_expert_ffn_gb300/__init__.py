@@ -72,6 +72,37 @@ class moe_decode_options(ctypes.Structure):
     ]
 
 
+class moe_adamw_tensor(ctypes.Structure):
+    _fields_ = [
+        ("param", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("master", ctypes.c_void_p),
+        ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("param_dtype", ctypes.c_int32),
+        ("grad_dtype", ctypes.c_int32),
+        ("lr_factor", ctypes.c_float),
+        ("weight_decay", ctypes.c_float),
+    ]
+
+
+class moe_adamw_options(ctypes.Structure):
+    """lr, beta1, beta2, eps, step; and device addresses lr_dev (fp32), step_dev (int64), grad_scale (fp32) or None."""
+
+    _fields_ = [
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("step", ctypes.c_int64),
+        ("lr_dev", ctypes.c_void_p),
+        ("step_dev", ctypes.c_void_p),
+        ("grad_scale", ctypes.c_void_p),
+    ]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int
 _I64 = ctypes.c_int64
@@ -117,6 +148,15 @@ _SIGS = {
     "moe_block_norm_backward_workspace_size": [_I32, _I32, _I32, _PSZ],
     "moe_block_norm_backward": [_P, _I32, _I64, _P, _I32, _I64, _I32, _I32, _P, _P, _P, _I32, ctypes.c_float,
                                 ctypes.c_float, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P],
+    "moe_router_loss_workspace_size": [_I32, _I32, _PSZ],
+    "moe_router_loss": [_P, _I32, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _P, _SZ, _P, _P],
+    "moe_router_loss_backward": [_P, _I32, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _P, _P],
+    "moe_cross_entropy_workspace_size": [_I32, _I32, _I32, _PSZ],
+    "moe_cross_entropy": [_P, _I32, _I32, _I32, _P, _I32, _P, _P, _P, _P, _SZ, _P, _P],
+    "moe_cross_entropy_backward_workspace_size": [_I32, _I32, _I32, _PSZ],
+    "moe_cross_entropy_backward": [_P, _I32, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _P, _I32, _I32, _P, _SZ, _P, _P],
+    "moe_adamw_step": [ctypes.POINTER(moe_adamw_tensor), _I32, ctypes.POINTER(moe_adamw_options), _P, _P],
+    "moe_adamw_states": [ctypes.POINTER(moe_adamw_tensor), _I32, ctypes.POINTER(_P), ctypes.POINTER(_P), _P],
 }
 
 
@@ -511,6 +551,161 @@ def moe_block_norm_backward(x, res_dtype, b, dtype, T, H, w_post, w_pre, gate, g
           _packed(dy, "dy", T * H, res_dtype), _packed(du, "du", T * H, dtype), _packed(dx, "dx", T * H, res_dtype),
           _packed(db, "db", T * H, dtype), _packed(dw_post, "dw_post", H, MOE_F32), _packed(dw_pre, "dw_pre", H, MOE_F32),
           _packed(dgate, "dgate", n, MOE_F32), _workspace(ws, ws_bytes), ws_bytes, _stream(stream))
+
+
+# ----------------------------------------------------------------- the router's losses
+
+def moe_router_loss_workspace_size(T, E):
+    return _size((_lib or load()).moe_router_loss_workspace_size, T, E)
+
+
+def moe_router_loss(logits, dtype, T, E, ids, k, keep, loss, counts, mean_prob, lse, ws=None, ws_bytes=0, dev_status=None,
+                    stream=None):
+    """loss[0] = E sum_e f_e P_e, loss[1] = mean lse^2, counts [E + 1] (the last: tokens that count), mean_prob [E], lse [T].
+    keep: bytes or truth values [T], or None."""
+    if keep is not None and keep.__class__ is not int and str(keep.dtype) == "torch.bool":
+        import torch
+
+        keep = keep.view(torch.uint8)
+    _call((_lib or load()).moe_router_loss, _packed(logits, "logits", T * E, dtype), dtype, T, E,
+          _packed(ids, "ids", T * k, _INT32), k, _packed(keep, "keep", T, _BYTE), _packed(loss, "loss", 2, MOE_F32),
+          _packed(counts, "counts", E + 1, _INT32), _packed(mean_prob, "mean_prob", E, MOE_F32),
+          _packed(lse, "lse", T, MOE_F32), _workspace(ws, ws_bytes), ws_bytes, _packed(dev_status, "dev_status", 1, _INT32),
+          _stream(stream))
+
+
+def moe_router_loss_backward(logits, dtype, T, E, ids, k, counts, lse, dloss, w, dw, dlogits, stream=None):
+    """dlogits from dloss [2] (or None) and from the routing weights' gradient dw (w and dw, or both None)."""
+    _call((_lib or load()).moe_router_loss_backward, _packed(logits, "logits", T * E, dtype), dtype, T, E,
+          _packed(ids, "ids", T * k, _INT32), k, _packed(counts, "counts", E + 1, _INT32), _packed(lse, "lse", T, MOE_F32),
+          _packed(dloss, "dloss", 2, MOE_F32), _packed(w, "w", T * k, MOE_F32), _packed(dw, "dw", T * k, MOE_F32),
+          _packed(dlogits, "dlogits", T * E, dtype), _stream(stream))
+
+
+# ----------------------------------------------------------------- cross entropy over a vocabulary
+
+def moe_cross_entropy_workspace_size(T, H, V):
+    return _size((_lib or load()).moe_cross_entropy_workspace_size, T, H, V)
+
+
+def moe_cross_entropy(h, dtype, T, H, w, V, labels, loss, lse, ws=None, ws_bytes=0, dev_status=None, stream=None):
+    """loss[t] = lse[t] - z[t, labels[t]] of z = h w^T, h [T][H], w [V][H]; labels int32, negative: left out."""
+    _call((_lib or load()).moe_cross_entropy, _packed(h, "h", T * H, dtype), dtype, T, H, _packed(w, "w", V * H, dtype), V,
+          _packed(labels, "labels", T, _INT32), _packed(loss, "loss", T, MOE_F32), _packed(lse, "lse", T, MOE_F32),
+          _workspace(ws, ws_bytes), ws_bytes, _packed(dev_status, "dev_status", 1, _INT32), _stream(stream))
+
+
+def moe_cross_entropy_backward_workspace_size(T, H, V):
+    return _size((_lib or load()).moe_cross_entropy_backward_workspace_size, T, H, V)
+
+
+def moe_cross_entropy_backward(h, dtype, T, H, w, V, labels, lse, dloss, dlse, dh, dw, dw_dtype=None, accumulate=False, ws=None,
+                               ws_bytes=0, dev_status=None, stream=None):
+    """dh and dw (either may be None) for dloss [T] and dlse [T] (or None); dw_dtype: dtype (the default) or MOE_F32."""
+    wt = dtype if dw_dtype is None else dw_dtype
+    _call((_lib or load()).moe_cross_entropy_backward, _packed(h, "h", T * H, dtype), dtype, T, H,
+          _packed(w, "w", V * H, dtype), V, _packed(labels, "labels", T, _INT32), _packed(lse, "lse", T, MOE_F32),
+          _packed(dloss, "dloss", T, MOE_F32), _packed(dlse, "dlse", T, MOE_F32), _packed(dh, "dh", T * H, dtype),
+          _packed(dw, "dw", V * H, wt), wt, int(accumulate), _workspace(ws, ws_bytes), ws_bytes,
+          _packed(dev_status, "dev_status", 1, _INT32), _stream(stream))
+
+
+# ----------------------------------------------------------------- AdamW
+
+class AdamwTensors:
+    """The tensors of moe_adamw_step and moe_adamw_states: made once, used every step (make_adamw_tensors)."""
+
+    def __init__(self, array, held):
+        self.array, self.held = array, held  # (the torch tensors stay alive with their addresses)
+
+    def __len__(self):
+        return len(self.array)
+
+
+def _moe_dtype(t, name):
+    for d in (MOE_F32, MOE_BF16, MOE_F16):
+        if t.dtype == _KINDS[d][0]:
+            return d
+    raise MoeError(MOE_ERR_INVALID_ARG, f"{name} must be of float32, bfloat16 or float16 (got {t.dtype})")
+
+
+def make_adamw_tensors(tensors) -> AdamwTensors:
+    """tensors: dicts of torch tensors param, grad, m, v and, where there are, master (fp32) and scales (fp32 [ceil(n / 256)][2]:
+    m and v are then uint8), with lr_factor (1) and weight_decay (0)."""
+    array, ranges, host = (moe_adamw_tensor * len(tensors))(), [], None
+    for i, d in enumerate(tensors):
+        unknown = set(d) - {"param", "grad", "master", "m", "v", "scales", "lr_factor", "weight_decay"}
+        if unknown or any(d.get(k) is None for k in ("param", "grad", "m", "v")):
+            raise MoeError(MOE_ERR_INVALID_ARG, f"tensor {i}: param, grad, m and v are needed, beside them master, scales, "
+                                                f"lr_factor and weight_decay (got {sorted(d)})")
+        n, a = d["param"].numel(), array[i]
+        held = d.get("scales") is not None
+        kinds = {"param": _moe_dtype(d["param"], f"tensor {i}: param"), "grad": _moe_dtype(d["grad"], f"tensor {i}: grad"),
+                 "master": MOE_F32, "m": _BYTE if held else MOE_F32, "v": _BYTE if held else MOE_F32, "scales": MOE_F32}
+        for name, kind in kinds.items():
+            t = d.get(name)
+            if t is None:
+                continue
+            want = (n + 255) // 256 * 2 if name == "scales" else n
+            p = _packed(t, f"tensor {i}: {name}", want, kind)
+            if t.numel() != want:
+                raise MoeError(MOE_ERR_INVALID_ARG, f"tensor {i}: {name} must have {want} elements (got {t.numel()})")
+            if p.__class__ is _Host:
+                host = host or p
+            else:
+                setattr(a, name, p)
+            if want:
+                ranges.append((t.data_ptr(), t.data_ptr() + want * t.element_size(), name != "grad", f"tensor {i}: {name}"))
+        a.n, a.param_dtype, a.grad_dtype = n, kinds["param"], kinds["grad"]
+        a.lr_factor, a.weight_decay = d.get("lr_factor", 1.0), d.get("weight_decay", 0.0)
+    end = {True: (0, ""), False: (0, "")}  # how far what is written, and what is read, has come
+    for lo, hi, written, name in sorted(ranges):
+        for other in ((True, False) if written else (True,)):
+            if lo < end[other][0]:
+                raise MoeError(MOE_ERR_INVALID_ARG, f"{name} overlaps {end[other][1]}")
+        end[written] = max(end[written], (hi, name))
+    if host:
+        raise MoeError(MOE_ERR_INVALID_ARG, host.what)
+    return AdamwTensors(array, [dict(d) for d in tensors])
+
+
+def moe_adamw_step(tensors: AdamwTensors, options: moe_adamw_options, dev_status=None, stream=None):
+    """One AdamW step over all tensors, in place."""
+    _call((_lib or load()).moe_adamw_step, tensors.array, len(tensors.array), ctypes.byref(options),
+          _packed(dev_status, "dev_status", 1, _INT32), _stream(stream))
+
+
+class AdamwValues:
+    """Where moe_adamw_states writes: addresses of fp32 tensors (make_adamw_values)."""
+
+    def __init__(self, m, v, sizes, held):
+        self.m, self.v, self.sizes, self.held = m, v, sizes, held
+
+
+def make_adamw_values(m_values, v_values) -> AdamwValues:
+    """m_values and v_values: a packed fp32 tensor for each tensor's state (or None for a tensor, or in place of a list)."""
+    arrays, sizes = [], []
+    for what, values in (("m_values", m_values), ("v_values", v_values)):
+        if values is None:
+            arrays.append(None)
+            sizes.append(None)
+            continue
+        arrays.append((_P * len(values))())
+        sizes.append([None if t is None else t.numel() for t in values])
+        for i, t in enumerate(values):
+            p = _packed(t, f"{what}[{i}]", 0 if t is None else t.numel(), MOE_F32)
+            if p.__class__ is _Host:
+                raise MoeError(MOE_ERR_INVALID_ARG, p.what)
+            arrays[-1][i] = p
+    return AdamwValues(*arrays, sizes, (m_values, v_values))
+
+
+def moe_adamw_states(tensors: AdamwTensors, values: AdamwValues, stream=None):
+    """The values that the tensors' states stand for, in fp32."""
+    for what, sizes in zip(("m_values", "v_values"), values.sizes):
+        if sizes is not None and any(s is not None and s != a.n for s, a in zip(sizes, tensors.array)) or                 sizes is not None and len(sizes) != len(tensors):
+            raise MoeError(MOE_ERR_INVALID_ARG, f"{what} must have the tensors' sizes")
+    _call((_lib or load()).moe_adamw_states, tensors.array, len(tensors.array), values.m, values.v, _stream(stream))
 
 
 def header_functions():

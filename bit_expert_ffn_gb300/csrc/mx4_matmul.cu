@@ -44,6 +44,10 @@
 namespace moe {
 namespace mx {
 
+using tc::elect_one;
+using tc::mbar_test;
+using tc::uniform;
+
 constexpr int BM = 128;            // weight rows per tile
 constexpr int BK = 256;            // K per step
 constexpr int MAX_BN = 224;        // rows per tile: two accumulators and the scales fill tensor memory
@@ -83,20 +87,6 @@ struct Shared {
     int start[MAX_E], count[MAX_E];
     alignas(16) char stage[EPI_WARPS][16 * STAGE_PITCH];  // epilogue warps: 16 rows on their way out
 };
-
-// The value of lane 0, which the compiler then knows to be the same in the
-// whole warp: descriptors and coordinates stay in uniform registers, which the
-// TMA and tcgen05 instructions take.  (With values that might differ between
-// lanes each such instruction cost 120 to 140 cycles to issue.)
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
-
-// True in one lane of the (converged) warp.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
 
 struct Item {
     int e, p0, cnt;  // expert, first row, rows
@@ -144,18 +134,6 @@ __device__ __forceinline__ Item item_of(const Params &p, const Shared &S, int it
         it.kb1 = p.nk * (split + 1) / p.splits;
     }
     return it;
-}
-
-// Whether the phase is complete now (try_wait may sleep for microseconds).
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(tc::smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
 }
 
 // A whole warp waits; false for all of it when the time is up or the CTA stops.

@@ -1,0 +1,497 @@
+// router_loss.cu -- moe_router_loss: the balance loss, the squared log-sum loss
+// and the counts per expert of a batch of router logits; and their gradient
+// together with the routing weights'.
+//
+//   p = softmax(l_t), n tokens, P_e = sum_t p_te / n, f_e = count_e / (n k)
+//   loss0 = E sum_e f_e P_e, loss1 = sum_t lse_t^2 / n
+//   dl_te = p_te (g_e - sum p g + z lse_t) + [the weights' part],
+//   g_e = dloss0 E count_e / (n^2 k), z = 2 dloss1 / n
+//
+// A warp takes a row whole into registers (a lane four columns side by side, or
+// one where rows are not aligned), with the next row on its way; the logits are
+// read once.  The forward sums over tokens stay in the lanes' registers, then
+// go warp by warp, CTA by CTA, in a fixed order: through shared memory, then
+// through the cluster's shared memory (few tokens, one launch) or the
+// workspace (a second, small launch).  The gradient needs the counts and lse of
+// the whole batch, so the logits come a second time.
+#include "cluster.cuh"
+#include "rows.cuh"
+
+namespace moe {
+namespace rl {
+
+constexpr int MAX_E = 1024, MAX_K = 16;
+constexpr int WARPS = 16, THREADS = WARPS * 32;
+constexpr int MAX_CLUSTER = 8;
+constexpr int CLUSTER_ROWS = 1024;  // up to this many tokens are one cluster's
+constexpr float LOG2E = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// A row's columns of a lane: 4 (lane + 32 j) + 0..3 (kVec), or lane + 32 i.
+template <bool kVec>
+__device__ __forceinline__ int column(int i, int lane)
+{
+    return kVec ? 4 * (lane + 32 * (i >> 2)) + (i & 3) : lane + 32 * i;
+}
+
+// The lane's columns of a row; those past E as `fill`.
+template <class A, int NV, bool kVec>
+__device__ __forceinline__ void load_row(const typename A::T *row, int E, int lane, float fill, float (&v)[NV])
+{
+    if (kVec) {
+#pragma unroll
+        for (int i = 0; i < NV; i += 4) {
+            const int c = column<kVec>(i, lane);
+            v[i] = v[i + 1] = v[i + 2] = v[i + 3] = fill;
+            if (c < E) A::load4(row + c, v + i);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = column<kVec>(i, lane);
+            v[i] = c < E ? A::load(row + c) : fill;
+        }
+    }
+}
+
+struct Params {
+    const void *logits;
+    int T, E, k;
+    const int32_t *ids;
+    const uint8_t *keep;
+    float *loss, *mean, *lse;
+    int32_t *counts;
+    float *part;  // [CTAs][E] sums of p, [CTAs][E] counts, [CTAs][2] sum of lse^2 and tokens; NULL: one cluster
+    int32_t *status;
+};
+
+// Sums over `parts` parts in order, a slice of the experts per CTA of the
+// cluster.  get(part, i): word i of the part's E sums, E counts, lse^2, tokens.
+template <class G>
+__device__ __forceinline__ void finish(const Params &p, int parts, G get, float *red, float *slot)
+{
+    const int C = gridDim.x, r = C > 1 ? (int)cluster_rank() : 0, tid = threadIdx.x;
+    const int E = p.E, e0 = (int)((int64_t)E * r / C), e1 = (int)((int64_t)E * (r + 1) / C), w = e1 - e0;
+    __shared__ float s_n, s_z;
+    __shared__ int s_tok;
+    if (tid < 32) {  // tokens and the squares, by every CTA
+        int n = 0;
+        float z = 0.f;
+        for (int i = tid; i < parts; i += 32) {
+            z += get(i, 2 * E);
+            n += __float_as_int(get(i, 2 * E + 1));
+        }
+        z = warp_sum(z);
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (tid == 0) s_tok = n, s_n = n > 0 ? (float)n : 1.f, s_z = z;
+    }
+    // groups of threads take every G-th part of a column
+    const int wide = (w + 31) & ~31, groups = max(1, min(THREADS / max(wide, 32), parts));
+    float *sum = red;
+    int *cnt = reinterpret_cast<int *>(red + THREADS);
+    __syncthreads();
+    float dot = 0.f;
+    for (int c0 = 0; c0 < w; c0 += THREADS / groups) {  // (one round, unless a slice is wider than the CTA)
+        const int per = THREADS / groups, g = tid / per, c = c0 + tid % per;
+        float a = 0.f;
+        int b = 0;
+        if (g < groups && c < w) {
+#pragma unroll 4
+            for (int i = g; i < parts; i += groups) {
+                a += get(i, e0 + c);
+                b += __float_as_int(get(i, E + e0 + c));
+            }
+        }
+        sum[tid] = a;
+        cnt[tid] = b;
+        __syncthreads();
+        if (g == 0 && c < w) {
+            for (int i = 1; i < groups; i++) {
+                a += sum[tid + i * per];
+                b += cnt[tid + i * per];
+            }
+            const float m = a / s_n;
+            p.mean[e0 + c] = m;
+            p.counts[e0 + c] = b;
+            dot += (float)b * m;
+        }
+        __syncthreads();
+    }
+    dot = warp_sum(dot);
+    if ((tid & 31) == 0) sum[tid >> 5] = dot;
+    __syncthreads();
+    if (tid == 0) {
+        dot = 0.f;
+        for (int i = 0; i < WARPS; i++) dot += sum[i];
+        *slot = dot;
+    }
+    if (C > 1) cluster_sync();
+    else __syncthreads();
+    if (r == 0 && tid == 0) {
+        dot = 0.f;
+        for (int i = 0; i < C; i++) dot += C > 1 ? __uint_as_float(ld_cluster((uint32_t)__cvta_generic_to_shared(slot), i)) : *slot;
+        p.loss[0] = (float)E * (dot / (s_n * (float)p.k));
+        p.loss[1] = s_z / s_n;
+        p.counts[E] = s_tok;
+    }
+    if (C > 1) cluster_sync();  // no CTA leaves while another reads its slot
+}
+
+template <class A, int NV, bool kVec>
+__global__ void __launch_bounds__(THREADS, NV <= 16 ? 2 : 1) loss_kernel(const __grid_constant__ Params p)
+{
+    extern __shared__ float dyn[];  // [WARPS][E] sums of p, [E] sums of the CTA, [E] counts, 2; 2 THREADS words for finish
+    const int lane = lane_id(), warp = warp_id(), E = p.E, k = p.k;
+    float *rows = dyn, *cta = dyn + WARPS * E;
+    int *hist = reinterpret_cast<int *>(cta + E);
+    __shared__ float s_z[WARPS], s_slot;
+    __shared__ int s_tok[WARPS];
+    for (int i = threadIdx.x; i < E; i += THREADS) hist[i] = 0;
+    __syncthreads();
+
+    using T = typename A::T;
+    const T *logits = static_cast<const T *>(p.logits);
+    const int step = gridDim.x * WARPS;
+    float acc[NV], cur[NV], nxt[NV], z = 0.f;
+    int tokens = 0;
+#pragma unroll
+    for (int i = 0; i < NV; i++) acc[i] = 0.f;
+    int t = blockIdx.x * WARPS + warp, id = -1, idn = -1;
+    bool in = true, inn = true;
+    auto fetch = [&](int t, float (&v)[NV], int &id, bool &in) {
+        load_row<A, NV, kVec>(logits + (int64_t)t * E, E, lane, -INFINITY, v);
+        id = lane < k ? p.ids[(int64_t)t * k + lane] : MOE_ID_NOT_LOCAL;
+        in = !p.keep || p.keep[t] != 0;
+    };
+    if (t < p.T) fetch(t, cur, id, in);
+    for (; t < p.T; t += step) {
+        if (p.T - t > step) fetch(t + step, nxt, idn, inn);
+        if ((unsigned)id >= (unsigned)E) {
+            if (id != MOE_ID_NOT_LOCAL) set_status(p.status, MOE_ERR_BOUNDS);
+            id = -1;
+        }
+        float top = cur[0];
+#pragma unroll
+        for (int i = 1; i < NV; i++) top = fmaxf(top, cur[i]);
+        top = warp_max(top);
+        const float off = top == -INFINITY ? 0.f : top;
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            cur[i] = ex2((cur[i] - off) * LOG2E);
+            s += cur[i];
+        }
+        s = warp_sum(s);
+        // (s is NaN when a logit is NaN or +inf, 0 when all are -inf)
+        if (in && s != s && lane == 0) set_status(p.status, MOE_ERR_NONFINITE);
+        const bool counts = in && s > 0.f;
+        const float lse = counts ? top + logf(s) : -INFINITY;
+        if (lane == 0) p.lse[t] = lse;
+        if (counts) {
+            const float inv = 1.f / s;
+#pragma unroll
+            for (int i = 0; i < NV; i++) acc[i] = fmaf(cur[i], inv, acc[i]);
+            z = fmaf(lse, lse, z);
+            tokens++;
+            if (id >= 0) atomicAdd(&hist[id], 1);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; i++) cur[i] = nxt[i];
+        id = idn;
+        in = inn;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        const int c = column<kVec>(i, lane);
+        if (c < E) rows[warp * E + c] = acc[i];
+    }
+    if (lane == 0) s_z[warp] = z, s_tok[warp] = tokens;
+    __syncthreads();
+    for (int c = threadIdx.x; c < E; c += THREADS) {
+        float a = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; w++) a += rows[w * E + c];
+        cta[c] = a;
+    }
+    if (threadIdx.x == 0) {
+        float a = 0.f;
+        int n = 0;
+        for (int w = 0; w < WARPS; w++) a += s_z[w], n += s_tok[w];
+        cta[2 * E] = a;
+        reinterpret_cast<int *>(cta)[2 * E + 1] = n;
+    }
+    __syncthreads();
+    if (p.part) {
+        for (int c = threadIdx.x; c < 2 * E + 2; c += THREADS) p.part[(int64_t)blockIdx.x * (2 * E + 2) + c] = cta[c];
+        return;
+    }
+    const int C = gridDim.x;
+    if (C > 1) cluster_sync();
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(cta);
+    finish(p, C, [&](int i, int w) { return C > 1 ? __uint_as_float(ld_cluster(base + w * 4, i)) : cta[w]; },
+           cta + 2 * E + 2, &s_slot);
+}
+
+__global__ void __launch_bounds__(THREADS, 1) finish_kernel(const __grid_constant__ Params p, int parts)
+{
+    __shared__ float red[2 * THREADS], slot;
+    finish(p, parts, [&](int i, int w) { return p.part[(int64_t)i * (2 * p.E + 2) + w]; }, red, &slot);
+}
+
+struct GradParams {
+    const void *logits;
+    void *dlogits;
+    int T, E, k;
+    const int32_t *ids, *counts;
+    const float *lse, *dloss, *w, *dw;
+};
+
+template <class A, int NV, bool kVec>
+__global__ void __launch_bounds__(THREADS, NV <= 16 ? 2 : 1) grad_kernel(const __grid_constant__ GradParams p)
+{
+    extern __shared__ float dyn[];  // [WARPS][E rounded up to 4]: the weights' part of a warp's row
+    const int lane = lane_id(), warp = warp_id(), E = p.E, k = p.k;
+    using T = typename A::T;
+    const T *logits = static_cast<const T *>(p.logits);
+    T *out = static_cast<T *>(p.dlogits);
+    float *row = dyn + warp * ((E + 3) & ~3);
+    float g[NV], cur[NV], nxt[NV], zc = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; i++) g[i] = 0.f;
+    if (p.dloss) {
+        const float n = (float)max(p.counts[E], 1), c = p.dloss[0] * (float)E / n / (n * (float)k);
+        zc = 2.f * p.dloss[1] / n;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int e = column<kVec>(i, lane);
+            if (e < E) g[i] = c * (float)p.counts[e];
+        }
+    }
+    for (int i = lane; i < E; i += 32) row[i] = 0.f;
+    __syncwarp();
+    const int step = gridDim.x * WARPS;
+    int t = blockIdx.x * WARPS + warp, id = -1, idn = -1;
+    float lse = 0.f, lsen = 0.f, w = 0.f, wn = 0.f, d = 0.f, dn = 0.f;
+    auto fetch = [&](int t, float (&v)[NV], float &lse, int &id, float &w, float &d) {
+        if (p.dloss) {
+            load_row<A, NV, kVec>(logits + (int64_t)t * E, E, lane, -INFINITY, v);
+            lse = p.lse[t];
+        }
+        if (p.w && lane < k) {
+            id = p.ids[(int64_t)t * k + lane];
+            w = p.w[(int64_t)t * k + lane];
+            d = p.dw[(int64_t)t * k + lane];
+        }
+    };
+    if (t < p.T) fetch(t, cur, lse, id, w, d);
+    for (; t < p.T; t += step) {
+        if (p.T - t > step) fetch(t + step, nxt, lsen, idn, wn, dn);
+        const bool counts = p.dloss && lse - lse == 0.f;
+        float dot = 0.f;
+        if (counts) {
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                cur[i] = ex2((cur[i] - lse) * LOG2E);
+                dot = fmaf(cur[i], g[i], dot);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; i++) cur[i] = 0.f;
+        }
+        dot = warp_sum(dot);
+        const float add = zc * lse - dot;
+        if (counts) {
+#pragma unroll
+            for (int i = 0; i < NV; i++) cur[i] *= g[i] + add;
+        }
+        const bool mine = p.w && lane < k && (unsigned)id < (unsigned)E;
+        if (p.w) {
+            const float mean = warp_sum(lane < k ? w * d : 0.f);
+            float v = w * (d - mean);
+            // (an expert named twice gets the sum, in the slots' order, at its first slot)
+            const uint32_t same = __match_any_sync(0xffffffffu, mine ? id : E + lane);
+            const bool first = mine && (same & ((1u << lane) - 1)) == 0;
+            if (__any_sync(0xffffffffu, mine && !first)) {
+                float total = 0.f;
+                for (int j = 0; j < k; j++) {
+                    const float o = __shfl_sync(0xffffffffu, v, j);
+                    if (same >> j & 1) total += o;
+                }
+                v = total;
+            }
+            if (first) row[id] = v;
+            __syncwarp();
+        }
+        T *o = out + (int64_t)t * E;
+        if (kVec) {
+#pragma unroll
+            for (int i = 0; i < NV; i += 4) {
+                const int c = column<kVec>(i, lane);
+                if (c < E) {
+                    if (p.w) {
+                        const float4 a = *reinterpret_cast<const float4 *>(row + c);
+                        cur[i] += a.x, cur[i + 1] += a.y, cur[i + 2] += a.z, cur[i + 3] += a.w;
+                    }
+                    A::store4(o + c, cur + i);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                const int c = column<kVec>(i, lane);
+                if (c < E) A::store(o + c, p.w ? cur[i] + row[c] : cur[i]);
+            }
+        }
+        __syncwarp();
+        if (mine) row[id] = 0.f;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < NV; i++) cur[i] = nxt[i];
+        lse = lsen, id = idn, w = wn, d = dn;
+    }
+}
+
+// CTAs of the large form: two an SM, or one where a row takes a lane's 32 registers.
+static int grid_of(int T, int E) { return std::min((T + WARPS - 1) / WARPS, sm_count() * (E <= 512 ? 2 : 1)); }
+
+static size_t loss_smem(int E) { return ((size_t)WARPS * E + 2 * E + 2 + 2 * THREADS) * 4; }
+static size_t grad_smem(int E) { return (size_t)WARPS * ((E + 3) & ~3) * 4; }
+
+// Calls f<NV, kVec>() for a row length and whether rows are aligned for four columns at once.
+template <class F>
+moe_status with_row(int E, bool vec, F f)
+{
+#define MOE_RL(nv) \
+    if (E <= 32 * nv) return vec ? f(std::integral_constant<int, nv>{}, std::true_type{}) : f(std::integral_constant<int, nv>{}, std::false_type{})
+    MOE_RL(4);
+    MOE_RL(8);
+    MOE_RL(16);
+    MOE_RL(32);
+#undef MOE_RL
+    return fail(MOE_ERR_INVALID_ARG, "E=%d", E);
+}
+
+static moe_status check(moe_dtype dtype, int T, int E, int k)
+{
+    MOE_REQUIRE(dtype_ok(dtype), "dtype must be MOE_F32, MOE_BF16 or MOE_F16 (got %d)", (int)dtype);
+    MOE_REQUIRE(E >= 1 && E <= MAX_E, "E must be in [1, %d] (got %d)", MAX_E, E);
+    MOE_REQUIRE(k >= 1 && k <= std::min(E, MAX_K), "k must be in [1, min(E, %d)] (got %d)", MAX_K, k);
+    MOE_REQUIRE(T >= 0 && (int64_t)T * k < (1ll << 31), "T must be in [0, 2^31 / k) (got %d)", T);
+    return MOE_OK;
+}
+
+static bool vec_rows(const void *p, moe_dtype t, int E) { return E % 4 == 0 && aligned_to(p, 4 * dtype_bytes(t)); }
+
+}  // namespace rl
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_router_loss_workspace_size(int T, int E, size_t *bytes)
+{
+    using namespace rl;
+    MOE_REQUIRE(bytes, "bytes must not be NULL");
+    moe_status st = check(MOE_F32, T, E, 1);
+    if (st != MOE_OK) return st;
+    *bytes = T <= CLUSTER_ROWS ? 0 : (size_t)grid_of(T, E) * (2 * E + 2) * 4;
+    return MOE_OK;
+}
+
+extern "C" moe_status moe_router_loss(const void *logits, moe_dtype dtype, int T, int E, const int32_t *ids, int k,
+                                      const uint8_t *keep, float *loss, int32_t *counts, float *mean_prob, float *lse,
+                                      void *ws, size_t ws_bytes, int32_t *dev_status, moe_stream_t stream)
+{
+    using namespace rl;
+    moe_status st = check(dtype, T, E, k);
+    if (st != MOE_OK) return st;
+    MOE_REQUIRE(loss && counts && mean_prob && (T == 0 || (logits && ids && lse)), "NULL pointer");
+    MOE_REQUIRE(aligned_to(logits, dtype_bytes(dtype)) && aligned_to(ids, 4) && aligned_to(loss, 4) && aligned_to(counts, 4) &&
+                    aligned_to(mean_prob, 4) && aligned_to(lse, 4) && aligned_to(dev_status, 4),
+                "tensors must be aligned to their types");
+    size_t need = 0;
+    st = moe_router_loss_workspace_size(T, E, &need);
+    if (st != MOE_OK) return st;
+    if (ws_bytes < need || (need && !ws))
+        return fail(MOE_ERR_WORKSPACE, "moe_router_loss needs %zu bytes of workspace (got %zu)", need, ws ? ws_bytes : (size_t)0);
+    MOE_REQUIRE(!need || aligned16(ws), "ws must be 16-byte aligned");
+    Params p = {logits, T, E, k, ids, keep, loss, mean_prob, lse, counts, need ? static_cast<float *>(ws) : nullptr, dev_status};
+    const cudaStream_t s = to_cuda(stream);
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(THREADS);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    int grid = grid_of(T, E);
+    if (!need) {  // one cluster: a row or more per warp
+        int c = 1;
+        while (c < MAX_CLUSTER && c * WARPS < T) c *= 2;
+        grid = c;
+        at[0].val.clusterDim.x = (unsigned)c;
+        cfg.numAttrs = 1;
+    }
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.dynamicSmemBytes = loss_smem(E);
+    st = with_dtype(dtype, [&](auto a) {
+        return with_row(E, vec_rows(logits, dtype, E), [&](auto nv, auto vec) {
+            auto fn = loss_kernel<decltype(a), decltype(nv)::value, decltype(vec)::value>;
+            MOE_CUDA_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)loss_smem(32 * decltype(nv)::value)));
+            MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, fn, p));
+            return check_launch("router_loss");
+        });
+    });
+    if (st != MOE_OK || !need) return st;
+    int c = 1;
+    while (c < MAX_CLUSTER && c * 64 < E) c *= 2;
+    at[0].val.clusterDim.x = (unsigned)c;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3((unsigned)c);
+    cfg.dynamicSmemBytes = 0;
+    MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, finish_kernel, p, grid));
+    return check_launch("router_loss_finish");
+}
+
+extern "C" moe_status moe_router_loss_backward(const void *logits, moe_dtype dtype, int T, int E, const int32_t *ids, int k,
+                                               const int32_t *counts, const float *lse, const float *dloss, const float *w,
+                                               const float *dw, void *dlogits, moe_stream_t stream)
+{
+    using namespace rl;
+    moe_status st = check(dtype, T, E, k);
+    if (st != MOE_OK) return st;
+    if (T == 0) return MOE_OK;
+    MOE_REQUIRE(dlogits && (!dloss || (logits && counts && lse)), "NULL pointer");
+    MOE_REQUIRE(!w == !dw && (!w || ids), "w and dw go together, and with ids");
+    MOE_REQUIRE(aligned_to(logits, dtype_bytes(dtype)) && aligned_to(dlogits, dtype_bytes(dtype)) && aligned_to(ids, 4) &&
+                    aligned_to(counts, 4) && aligned_to(lse, 4) && aligned_to(dloss, 4) && aligned_to(w, 4) && aligned_to(dw, 4),
+                "tensors must be aligned to their types");
+    GradParams p = {logits, dlogits, T, E, k, ids, counts, lse, dloss, w, dw};
+    return with_dtype(dtype, [&](auto a) {
+        return with_row(E, vec_rows(logits, dtype, E) && vec_rows(dlogits, dtype, E), [&](auto nv, auto vec) {
+            auto fn = grad_kernel<decltype(a), decltype(nv)::value, decltype(vec)::value>;
+            MOE_CUDA_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)grad_smem(32 * decltype(nv)::value)));
+            fn<<<grid_of(T, E), THREADS, grad_smem(E), to_cuda(stream)>>>(p);
+            return check_launch("router_loss_backward");
+        });
+    });
+}

@@ -84,7 +84,7 @@ typedef enum moe_status {
 typedef enum moe_dtype {
     MOE_F32 = 0,
     MOE_BF16 = 1,
-    MOE_F16 = 2 /* the row, 4-bit and norm calls only */
+    MOE_F16 = 2 /* the row, 4-bit and norm calls and the training calls after them only */
 } moe_dtype;
 
 typedef enum moe_path {
@@ -629,6 +629,150 @@ moe_status moe_block_norm_backward(const void *x, moe_dtype res_dtype, int64_t x
                                    float eps, const void *dy, const void *du, void *dx, void *db,
                                    float *dw_post, float *dw_pre, float *dgate, void *ws, size_t ws_bytes,
                                    moe_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* The router's losses                                                      */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * What a router is trained on beside the model's own loss.  With p the softmax
+ * of a token's E logits, n the tokens that count, count[e] their pairs of
+ * expert e, f_e = count[e] / (n k) and P_e the mean of p_e over them:
+ *   loss[0] = E sum_e f_e P_e                   (1 for an even load)
+ *   loss[1] = mean over the tokens of lse^2,    lse = log sum_e exp(logit_e)
+ *   counts  [E + 1] int32: count[0 .. E-1], then n
+ *   mean_prob [E]: P,   lse [T]: for the gradient
+ * A token counts unless keep (bytes [T], NULL: all) is 0 or all its logits are
+ * -inf; a single logit of -inf is an expert that cannot be chosen.  A logit of
+ * NaN or +inf sets *dev_status = MOE_ERR_NONFINITE and its token does not
+ * count.  lse of a token that does not count is -inf.  An id of
+ * MOE_ID_NOT_LOCAL counts for no expert, any other outside [0, E) sets
+ * MOE_ERR_BOUNDS too.  No token that counts (or T = 0): losses, counts and
+ * means are 0.  logits and dlogits are fp32, bf16 or fp16 [T][E], everything
+ * is summed in fp32 in a fixed order.  1 <= E <= 1024, 1 <= k <= min(E, 16).
+ *
+ * moe_router_loss_backward: the logits' gradient, from dloss [2] (device; the
+ * gradients of the two losses; NULL: none) and from the gradient dw [T][k] of
+ * the routing weights w [T][k], the softmax over the kept logits as
+ * moe_router_topk gives it (both NULL: none):
+ *   dlogits[t][e] = p_te (g_e - sum_e' p_te' g_e' + 2 dloss[1] lse_t / n)
+ *                   + sum over j with ids[t][j] = e of
+ *                     w_tj (dw_tj - sum_i w_ti dw_ti)
+ * with g_e = dloss[0] E count[e] / (n^2 k); the first part is 0 for a token
+ * that does not count, the second goes by w and dw alone.  counts and lse are
+ * moe_router_loss's.  dlogits may be logits.
+ */
+moe_status moe_router_loss_workspace_size(int T, int E, size_t *bytes);
+moe_status moe_router_loss(const void *logits, moe_dtype dtype, int T, int E, const int32_t *ids, int k,
+                           const uint8_t *keep, float *loss, int32_t *counts, float *mean_prob, float *lse,
+                           void *ws, size_t ws_bytes, int32_t *dev_status, moe_stream_t stream);
+moe_status moe_router_loss_backward(const void *logits, moe_dtype dtype, int T, int E, const int32_t *ids,
+                                    int k, const int32_t *counts, const float *lse, const float *dloss,
+                                    const float *w, const float *dw, void *dlogits, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Cross entropy over a vocabulary                                          */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * The loss at the end of a model, from the hidden states h [T][H] and the
+ * head's weights w [V][H] (both bf16 or both fp16), on the tensor cores,
+ * without the T x V logits ever being held:
+ *   z_t = w h_t,  lse[t] = log sum_v exp(z_tv),  loss[t] = lse[t] - z_t,labels[t]
+ * A negative label leaves its token out (loss 0; lse is given all the same);
+ * one of V or more does too and sets *dev_status = MOE_ERR_BOUNDS.  Products
+ * are exact, sums fp32.  A value that is not finite makes the losses of the
+ * tokens that it reaches so too.  H a multiple of 8, V >= 1; h and w 16-byte
+ * aligned.  T = 0 is a no-op.
+ *
+ * moe_cross_entropy_backward: with dloss [T] and dlse [T] (NULL: zero) the
+ * gradients of loss and lse, and d_tv = exp(z_tv - lse[t]) (dloss[t] + dlse[t])
+ * - [v = labels[t]] dloss[t] (a token that is left out has dloss = 0),
+ *   dh[t] = sum_v d_tv w_v      [T][H], of h's type
+ *   dw[v] (+)= sum_t d_tv h_t   [V][H], of h's type or MOE_F32
+ * either of which may be NULL.  accumulate adds to dw as it is (MOE_F32 only;
+ * one addition per value and call).  The products are computed again, in
+ * pieces of the vocabulary: d enters the two gradients rounded to h's type,
+ * relative to the largest |dloss| or |dlse| of the call, and is held for one
+ * piece at a time (at most 256 MiB of the workspace, at least 256 columns of
+ * the vocabulary); a product over the whole of T or V is summed in fp32 and
+ * rounded once.  dh and dw must not overlap h and w.  With T = 0 dw is set to
+ * zero unless it is accumulated.
+ * A wait that runs out (about 2 s) sets MOE_ERR_TIMEOUT.
+ */
+moe_status moe_cross_entropy_workspace_size(int T, int H, int V, size_t *bytes);
+moe_status moe_cross_entropy(const void *h, moe_dtype dtype, int T, int H, const void *w, int V,
+                             const int32_t *labels, float *loss, float *lse, void *ws, size_t ws_bytes,
+                             int32_t *dev_status, moe_stream_t stream);
+moe_status moe_cross_entropy_backward_workspace_size(int T, int H, int V, size_t *bytes);
+moe_status moe_cross_entropy_backward(const void *h, moe_dtype dtype, int T, int H, const void *w, int V,
+                                      const int32_t *labels, const float *lse, const float *dloss,
+                                      const float *dlse, void *dh, void *dw, moe_dtype dw_dtype, int accumulate,
+                                      void *ws, size_t ws_bytes, int32_t *dev_status, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* AdamW                                                                    */
+/* ------------------------------------------------------------------------ */
+
+/* One tensor of n values (device pointers, aligned to their types; n = 0: nothing is done). */
+typedef struct moe_adamw_tensor {
+    void *param;        /* in/out, of param_dtype */
+    const void *grad;   /* of grad_dtype */
+    float *master;      /* in/out: the value in fp32, of which param is the rounding; NULL: param is the value */
+    void *m, *v;        /* in/out: fp32 [n], or codes (uint8 [n]) when scales are given */
+    float *scales;      /* in/out: [ceil(n / 256)][2], of m and of v's root; NULL: m and v are fp32 */
+    int64_t n;
+    int32_t param_dtype, grad_dtype; /* moe_dtype: any of the three */
+    float lr_factor;    /* the tensor's learning rate is lr * lr_factor */
+    float weight_decay;
+} moe_adamw_tensor;
+
+typedef struct moe_adamw_options {
+    double lr, beta1, beta2, eps;
+    int64_t step;              /* 1 for the first step */
+    const float *lr_dev;       /* device: the learning rate instead of lr, or NULL */
+    const int64_t *step_dev;   /* device: the step instead of `step`, or NULL */
+    const float *grad_scale;   /* device: a factor of all gradients (clipping, loss scaling), or NULL: 1 */
+} moe_adamw_options;
+
+/*
+ * One step of AdamW (I. Loshchilov, F. Hutter, "Decoupled Weight Decay
+ * Regularization", 2019) over all tensors, few launches whatever their number:
+ *   g = grad * grad_scale
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   x = x (1 - lr weight_decay)
+ *       - lr / (1 - beta1^step) m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in fp32.  tensors is a host array, copied into the launches; lr_dev, step_dev
+ * and grad_scale are read on the device, so that a captured step can be
+ * replayed with others.  An element whose g or g^2 is not finite is left as it
+ * is, m and v too, and sets *dev_status = MOE_ERR_NONFINITE; a grad_scale of
+ * NaN or infinity so leaves every tensor as it is.  Tensors must not overlap;
+ * equal param, master, m or v pointers are refused.  beta1 and beta2 in [0, 1),
+ * eps > 0, step >= 1 (a step_dev below 1 counts as 1).
+ *
+ * States in 8 bits (scales given; all zeros to begin with): a block of 256
+ * values shares two fp32 scales.  m is held in e4m3 (to nearest, ties to even)
+ * of m * (448 / max|m|), the scale being max|m| / 448.  The root r of v is held
+ * in a float without a sign, with 4 exponent and 4 mantissa bits, of
+ * r * (1.9375 / max r): code c > 0 stands for (1 + c % 16 / 16) 2^(c / 16 - 15)
+ * times the scale, max r / 1.9375 (to nearest, ties to even; what is not zero
+ * gets code 1 at least, so that no small v is taken for none); code 0 is zero.
+ * A block whose largest m (or r) is below 2^-100 is held as zeros.  m and v are
+ * computed in fp32, every operation rounded to nearest in the order written
+ * above (no product is fused with a sum), so that the codes do not depend on a
+ * machine's or compiler's choices.  x is updated from m and v before they are
+ * rounded to 8 bits.  A v that changes by less than half a step of its code
+ * (some 3 to 6 percent) keeps it: with beta2 near 1, a small change of the
+ * gradients' size is followed late.
+ *
+ * moe_adamw_states: the values that the states stand for, in fp32, tensor i's
+ * to m_values[i] and v_values[i] (host arrays of device pointers, NULL entries
+ * or arrays are left out): of codes, or copies of fp32 states.
+ */
+moe_status moe_adamw_step(const moe_adamw_tensor *tensors, int n_tensors, const moe_adamw_options *options,
+                          int32_t *dev_status, moe_stream_t stream);
+moe_status moe_adamw_states(const moe_adamw_tensor *tensors, int n_tensors, float *const *m_values,
+                            float *const *v_values, moe_stream_t stream);
 
 #ifdef __cplusplus
 }
