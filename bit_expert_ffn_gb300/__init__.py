@@ -617,6 +617,7 @@ class AdamwTensors:
 
     def __init__(self, array, held):
         self.array, self.held = array, held  # (the torch tensors stay alive with their addresses)
+        self.sizes = [a.n for a in array]
 
     def __len__(self):
         return len(self.array)
@@ -703,7 +704,9 @@ def make_adamw_values(m_values, v_values) -> AdamwValues:
 def moe_adamw_states(tensors: AdamwTensors, values: AdamwValues, stream=None):
     """The values that the tensors' states stand for, in fp32."""
     for what, sizes in zip(("m_values", "v_values"), values.sizes):
-        if sizes is not None and any(s is not None and s != a.n for s, a in zip(sizes, tensors.array)) or                 sizes is not None and len(sizes) != len(tensors):
+        if sizes is None or sizes == tensors.sizes:  # (lists, compared in one go: a step has hundreds of tensors)
+            continue
+        if len(sizes) != len(tensors.sizes) or any(s is not None and s != n for s, n in zip(sizes, tensors.sizes)):
             raise MoeError(MOE_ERR_INVALID_ARG, f"{what} must have the tensors' sizes")
     _call((_lib or load()).moe_adamw_states, tensors.array, len(tensors.array), values.m, values.v, _stream(stream))
 

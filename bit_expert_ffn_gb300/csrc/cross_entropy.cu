@@ -43,7 +43,7 @@ constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2;
 constexpr int STAGES = 4;
 constexpr int EPI_WARP0 = 2, EPI_WARPS = 4;
 constexpr int THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
-constexpr int OUT_BYTES = 32 * 128;  // a warp's 32 rows of 128 bytes on their way out, two in turn
+constexpr int OUT_BYTES = 32 * 128;  // a warp's 32 rows of 32 values on their way out, two in turn
 constexpr size_t SMEM = STAGES * (A_BYTES + B_BYTES) + EPI_WARPS * 2 * OUT_BYTES + 1024;
 constexpr int BAND = 32;  // row tiles that pass over the columns together
 constexpr unsigned long long kWaitNs = 2000000000ull;
@@ -52,21 +52,26 @@ constexpr size_t PIECE_BYTES = 256u << 20;
 constexpr float F16_ROOM = 16384.f;  // |d| <= 1 after the division: as fp16, 2^14 times that
 
 struct Job {
-    int m_tiles, n_tiles, nk;
-    int mn_a, mn_b;   // operand with M (N) inner
-    int a_y0, b_y0;   // added to the operands' and the output's row coordinates
-    int out_y0, add, out_f32;
+    int m_tiles, n_tiles, bn;  // columns of a tile: a multiple of 32, at most BN
+    int K, parts;              // the sum's length, and into how many parts it is split
+    int mn_a;                  // A with M inner
+    int b_y0, out_y0;          // added to B's and the output's row coordinates
+    int part_rows;             // rows of the output from one part to the next
+    int add, out_f32;
 };
 
+// Which items a CTA takes: of the first job every G-th (G the grid), then of the
+// second what evens the CTAs out: `long_items` each for those with one more of the first,
+// `short_items` for the others.
 struct Params {
     Job job[2];
-    int items0, items;  // of the first job, of both
-    uint32_t idesc;
+    int items0, items1, longer, long_items, short_items;
+    uint32_t idesc;     // but for N and the operands' order
     int T, V;           // rows, columns that there are (LOSS: of the vocabulary; GRAD: of the piece)
     int v0, all;        // the piece's first column, columns of the whole vocabulary
     int f16;
     const int32_t *labels;
-    float2 *stats;      // [n tiles][T]
+    float2 *stats;      // [T][n tiles]
     float *label_z;
     const float *lse, *dloss, *dlse, *top;
     int32_t *status;
@@ -85,21 +90,39 @@ struct Shared {
 };
 
 struct Item {
-    int j, m, n;  // job, tiles
+    int j, m, n, part;  // job, tiles, part of K
+    int kb0, kb1;       // steps
 };
 
-// Row tiles first, within bands of BAND: the tiles at work share the columns' operand, and a band's rows stay in L2.
-__device__ __forceinline__ Item item_of(const Params &p, int i)
+// The CTA's i-th item; false when there are no more.  Row tiles first, within bands of BAND: the tiles at work
+// share the columns' operand, and a band's rows stay in L2.
+__device__ __forceinline__ bool item_of(const Params &p, int i, Item &it)
 {
-    Item it;
-    it.j = i >= p.items0;
-    if (it.j) i -= p.items0;
+    const int c = blockIdx.x, G = gridDim.x;
+    int t = c + i * G;
+    it.j = 0;
+    if (t >= p.items0) {
+        i -= (p.items0 - c + G - 1) / G;
+        const bool more = c < p.longer;  // of the first job
+        const int even = min(p.long_items, p.short_items);
+        it.j = 1;
+        if (i < even) t = i * G + c;
+        else if (i < (more ? p.long_items : p.short_items)) t = even * G + (more ? (i - even) * p.longer + c : (i - even) * (G - p.longer) + c - p.longer);
+        else return false;
+        if (t >= p.items1) return false;
+    }
     const Job &g = p.job[it.j];
-    const int band = i / (BAND * g.n_tiles), m0 = band * BAND, rows = min(BAND, g.m_tiles - m0);
-    i -= band * BAND * g.n_tiles;
-    it.n = i / rows;
-    it.m = m0 + i - it.n * rows;
-    return it;
+    const int whole = g.m_tiles * g.n_tiles;
+    it.part = t / whole;
+    t -= it.part * whole;
+    const int band = t / (BAND * g.n_tiles), m0 = band * BAND, rows = min(BAND, g.m_tiles - m0);
+    t -= band * BAND * g.n_tiles;
+    it.n = t / rows;
+    it.m = m0 + t - it.n * rows;
+    const int nk = (g.K + BK - 1) / BK;
+    it.kb0 = (int)((int64_t)nk * it.part / g.parts);
+    it.kb1 = (int)((int64_t)nk * (it.part + 1) / g.parts);
+    return true;
 }
 
 __device__ __forceinline__ bool warp_wait(Shared &S, uint64_t *bar, uint32_t parity)
@@ -140,12 +163,18 @@ __device__ __forceinline__ void tma_add_2d(const CUtensorMap *map, int x, int y,
                  : "memory");
 }
 
-// A lane's row of 128 bytes into the warp's block, swizzled as TMA expects it, and the block on its way.
-__device__ __forceinline__ void put_row(char *buf, int lane, const uint32_t (&w)[32])
+// A lane's row of 32 fp32 (128 bytes) or 16-bit (64 bytes) values into the warp's block, swizzled as TMA expects it.
+__device__ __forceinline__ void put_row(char *buf, int lane, const uint32_t (&w)[32], bool f32)
 {
+    if (f32) {
 #pragma unroll
-    for (int j = 0; j < 8; j++)
-        *reinterpret_cast<uint4 *>(buf + lane * 128 + ((j ^ (lane & 7)) * 16)) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        for (int j = 0; j < 8; j++)
+            *reinterpret_cast<uint4 *>(buf + lane * 128 + ((j ^ (lane & 7)) * 16)) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            *reinterpret_cast<uint4 *>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16)) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    }
 }
 
 template <Kind K>
@@ -171,6 +200,9 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
         tc::fence_mbar_init();
     }
     if (warp == EPI_WARP0) tc::tmem_alloc(&S.tmem, 512);
+    // (launched while the kernel before it may still run, and lets the next one come as soon: nothing above reads what that one writes)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
@@ -181,28 +213,29 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
         int it = 0, s = 0;
         uint32_t phase = 1;
         bool ok = true;
-        for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
-            const Item m = item_of(p, item);
+        Item m;
+        for (int i = 0; ok && item_of(p, i, m); i++) {
             const Job &g = p.job[m.j];
-            for (int kb = 0; kb < g.nk; kb++, it++) {
+            const int boxes = (g.bn + 63) / 64;
+            const uint32_t bytes = A_BYTES + (K == PROD ? boxes * (BK * 128) : g.bn * 128);
+            for (int kb = m.kb0; kb < m.kb1; kb++, it++) {
                 if (it >= STAGES) ok = warp_wait(S, &S.empty[s], phase);
                 if (!ok) break;
                 if (elect_one()) {
-                    tc::mbar_arrive_expect_tx(&S.full[s], A_BYTES + B_BYTES);
+                    tc::mbar_arrive_expect_tx(&S.full[s], bytes);
                     char *a = sA + s * A_BYTES, *b = sB + s * B_BYTES;
                     if (K == PROD && g.mn_a) {
 #pragma unroll
-                        for (int i = 0; i < BM / 64; i++)
-                            tc::tma_load_2d(a + i * BK * 128, &maps.a[m.j], m.m * BM + i * 64, g.a_y0 + kb * BK, &S.full[s]);
+                        for (int h = 0; h < BM / 64; h++)
+                            tc::tma_load_2d(a + h * BK * 128, &maps.a[m.j], m.m * BM + h * 64, kb * BK, &S.full[s]);
                     } else {
-                        tc::tma_load_2d(a, &maps.a[m.j], kb * BK, g.a_y0 + m.m * BM, &S.full[s]);
+                        tc::tma_load_2d(a, &maps.a[m.j], kb * BK, m.m * BM, &S.full[s]);
                     }
                     if (K == PROD) {
-#pragma unroll
-                        for (int i = 0; i < BN / 64; i++)
-                            tc::tma_load_2d(b + i * BK * 128, &maps.b[m.j], m.n * BN + i * 64, g.b_y0 + kb * BK, &S.full[s]);
+                        for (int h = 0; h < boxes; h++)
+                            tc::tma_load_2d(b + h * BK * 128, &maps.b[m.j], m.n * g.bn + h * 64, g.b_y0 + kb * BK, &S.full[s]);
                     } else {
-                        tc::tma_load_2d(b, &maps.b[m.j], kb * BK, g.b_y0 + m.n * BN, &S.full[s]);
+                        tc::tma_load_2d(b, &maps.b[m.j], kb * BK, g.b_y0 + m.n * g.bn, &S.full[s]);
                     }
                 }
                 if (++s == STAGES) s = 0, phase ^= 1;
@@ -224,17 +257,19 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
         int j = 0, s = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x, j++) {
-            const Item m = item_of(p, item);
+        Item m;
+        for (int i = 0; ok && item_of(p, i, m); i++) {
             const Job &g = p.job[m.j];
+            if (m.kb0 == m.kb1) continue;  // a part of nothing
             const int acc = j & 1, v = j >> 1;
+            j++;
             if (v > 0) ok = warp_wait(S, &S.acc_empty[acc], (v - 1) & 1);
             if (!ok) break;
             tc::tc_fence_after();
             const uint32_t d = tmem + (uint32_t)(acc * BN);
-            const uint32_t idesc = p.idesc | (K == PROD ? (uint32_t)g.mn_a << 15 | 1u << 16 : 0u);
+            const uint32_t idesc = p.idesc | (uint32_t)(g.bn >> 3) << 17 | (K == PROD ? (uint32_t)g.mn_a << 15 | 1u << 16 : 0u);
             bool ready = mbar_test(&S.full[s], phase);
-            for (int kb = 0; kb < g.nk; kb++) {
+            for (int kb = m.kb0; kb < m.kb1; kb++) {
                 if (!__all_sync(0xffffffffu, ready)) ok = warp_wait(S, &S.full[s], phase);
                 if (!ok) break;
                 tc::tc_fence_after();
@@ -248,11 +283,12 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                     const uint64_t db = K == PROD ? desc_mnmajor_sw128(b) : tc::desc_kmajor_sw128(b);
                     // K = 16 an instruction: 32 bytes of a row, or 16 rows of 128 bytes
                     const uint64_t ka = ma ? 128 : 2, kbs = K == PROD ? 128 : 2;
+                    const int left = g.K - kb * BK;  // (d's columns past K's last sixteen may never have been written)
 #pragma unroll
-                    for (int i = 0; i < BK / 16; i++)
-                        tc::mma_f16_ss(d, da + i * ka, db + i * kbs, idesc, (kb > 0 || i > 0) ? 1u : 0u);
+                    for (int k = 0; k < BK / 16; k++)
+                        if (k * 16 < left) tc::mma_f16_ss(d, da + k * ka, db + k * kbs, idesc, (kb > m.kb0 || k > 0) ? 1u : 0u);
                     tc::mma_commit(&S.empty[s]);
-                    if (kb + 1 == g.nk) tc::mma_commit(&S.acc_full[acc]);
+                    if (kb + 1 == m.kb1) tc::mma_commit(&S.acc_full[acc]);
                 }
                 s = sn;
                 phase = phase_n;
@@ -272,11 +308,13 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
         const float top = K == LOSS ? 0.f : *p.top;
         const float up = K == PROD ? (p.f16 ? top / F16_ROOM : top) : 0.f;
         const float down = K == GRAD && top > 0.f ? (p.f16 ? F16_ROOM : 1.f) : 0.f;
-        for (int item = blockIdx.x; item < p.items; item += gridDim.x, j++) {
-            const Item m = item_of(p, item);
+        Item m;
+        for (int i = 0; item_of(p, i, m); i++) {
             const Job &g = p.job[m.j];
+            if (m.kb0 == m.kb1) continue;
             const int acc = j & 1, v = j >> 1;
-            const int row = m.m * BM + q * 32 + lane, n0 = m.n * BN;
+            j++;
+            const int row = m.m * BM + q * 32 + lane, n0 = m.n * g.bn;
             int label = -1;
             float nl = 0.f, a = 0.f, b = 0.f;
             if (K != PROD && row < p.T) label = p.labels[row];
@@ -304,7 +342,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                 float mx = -INFINITY, base = 0.f, sum = 0.f, zl = 0.f;
                 bool mine = false;
 #pragma unroll 1
-                for (int c = 0; c < BN; c += 32) {
+                for (int c = 0; c < g.bn; c += 32) {
                     const int left = p.V - n0 - c;
                     if (left <= 0) break;
                     uint32_t r[32];
@@ -335,60 +373,43 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                     base = off;
                 }
                 if (row < p.T) {
-                    p.stats[(int64_t)m.n * p.T + row] = make_float2(mx, mx == -INFINITY ? 0.f : sum * ex2(-fmaf(mx, LOG2E, -base)));
+                    p.stats[(int64_t)row * g.n_tiles + m.n] = make_float2(mx, mx == -INFINITY ? 0.f : sum * ex2(-fmaf(mx, LOG2E, -base)));
                     if (mine) p.label_z[row] = zl;
                 }
             } else {
-                const int width = K == GRAD || !g.out_f32 ? 64 : 32;  // columns of a box
 #pragma unroll 1
-                for (int c = 0; c < BN; c += width) {
-                    uint32_t w[32];
+                for (int c = 0; c < g.bn; c += 32) {
+                    uint32_t r[32];
                     __syncwarp();
+                    tc::tmem_ld_32x32b_x32(tbase + c, r);
+                    tc::tmem_ld_wait();
+                    const bool f32 = K == PROD && g.out_f32;
                     if (K == GRAD) {
+                        const int left = p.V - n0 - c, at = label - n0 - c;
 #pragma unroll
-                        for (int h = 0; h < 2; h++) {
-                            uint32_t r[32];
-                            tc::tmem_ld_32x32b_x32(tbase + c + h * 32, r);
-                            tc::tmem_ld_wait();
-                            const int left = p.V - n0 - c - h * 32, at = label - n0 - c - h * 32;
-#pragma unroll
-                            for (int i = 0; i < 32; i++) {
-                                float e = ex2(fmaf(__uint_as_float(r[i]), LOG2E, nl)) * a;
-                                if (i == at) e -= b;
-                                if (i >= left || (a == 0.f && b == 0.f)) e = 0.f;
-                                r[i] = __float_as_uint(e);
-                            }
-#pragma unroll
-                            for (int i = 0; i < 16; i++)
-                                w[h * 16 + i] = pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), p.f16);
+                        for (int i = 0; i < 32; i++) {
+                            float e = ex2(fmaf(__uint_as_float(r[i]), LOG2E, nl)) * a;
+                            if (i == at) e -= b;
+                            if (i >= left || (a == 0.f && b == 0.f)) e = 0.f;
+                            r[i] = __float_as_uint(e);
                         }
                     } else {
-                        uint32_t r[32];
-                        tc::tmem_ld_32x32b_x32(tbase + c, r);
-                        tc::tmem_ld_wait();
-                        if (g.out_f32) {
 #pragma unroll
-                            for (int i = 0; i < 32; i++) w[i] = __float_as_uint(__uint_as_float(r[i]) * up);
-                        } else {
+                        for (int i = 0; i < 32; i++) r[i] = __float_as_uint(__uint_as_float(r[i]) * up);
+                    }
+                    if (!f32) {
 #pragma unroll
-                            for (int i = 0; i < 16; i++)
-                                w[i] = pack2(__uint_as_float(r[2 * i]) * up, __uint_as_float(r[2 * i + 1]) * up, p.f16);
-                            tc::tmem_ld_32x32b_x32(tbase + c + 32, r);
-                            tc::tmem_ld_wait();
-#pragma unroll
-                            for (int i = 0; i < 16; i++)
-                                w[16 + i] = pack2(__uint_as_float(r[2 * i]) * up, __uint_as_float(r[2 * i + 1]) * up, p.f16);
-                        }
+                        for (int i = 0; i < 16; i++) r[i] = pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), p.f16);
                     }
                     char *buf = out + (turn & 1) * OUT_BYTES;
                     turn++;
                     if (lane == 0) tc::bulk_wait_read<1>();
                     __syncwarp();
-                    put_row(buf, lane, w);
+                    put_row(buf, lane, r, f32);
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        const int x = n0 + c, y = g.out_y0 + m.m * BM + q * 32;
+                        const int x = n0 + c, y = g.out_y0 + m.part * g.part_rows + m.m * BM + q * 32;
                         if (K == PROD && g.add) tma_add_2d(&maps.out[m.j], x, y, buf);
                         else tc::tma_store_2d(&maps.out[m.j], x, y, buf);
                         tc::bulk_commit();
@@ -409,27 +430,42 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
     }
 }
 
-// lse and loss from the tiles' maxima and sums: groups of threads take every G-th tile of a token.
-constexpr int COMBINE = 256;
+// lse and loss from the tiles' maxima and sums: a warp per token.
+constexpr int COMBINE_WARPS = 8;
 
-__global__ void __launch_bounds__(COMBINE) combine_kernel(const float2 *stats, const float *label_z, const int32_t *labels, int T,
-                                                          int V, int tiles, int per, float *loss, float *lse, int32_t *status)
+__global__ void __launch_bounds__(COMBINE_WARPS * 32) combine_kernel(const float2 *stats, const float *label_z, const int32_t *labels,
+                                                                     int T, int V, int tiles, float *loss, float *lse, int32_t *status)
 {
-    __shared__ float2 part[COMBINE];
-    const int c = threadIdx.x % per, g = threadIdx.x / per, groups = COMBINE / per, t = blockIdx.x * per + c;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int t = blockIdx.x * COMBINE_WARPS + warp_id(), lane = lane_id();
+    if (t >= T) return;
+    const float2 *row = stats + (int64_t)t * tiles;
     float m = -INFINITY, s = 0.f;
-    auto add = [&](float2 v) {
-        const float top = fmaxf(m, v.x), off = top == -INFINITY ? 0.f : top;
-        s = s * ex2((m - off) * LOG2E) + v.y * ex2((v.x - off) * LOG2E);
+    for (int i = lane; i < tiles; i += 256) {  // eight a lane at once
+        float2 v[8];
+        float top = m;
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            v[j] = i + 32 * j < tiles ? row[i + 32 * j] : make_float2(-INFINITY, 0.f);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++) top = fmaxf(top, v[j].x);
+        const float off = top == -INFINITY ? 0.f : top;
+        s *= ex2((m - off) * LOG2E);
+#pragma unroll
+        for (int j = 0; j < 8; j++) s = fmaf(v[j].y, ex2((v[j].x - off) * LOG2E), s);
         m = top;
-    };
-    if (t < T)
-#pragma unroll 4
-        for (int i = g; i < tiles; i += groups) add(stats[(int64_t)i * T + t]);
-    part[threadIdx.x] = make_float2(m, s);
-    __syncthreads();
-    if (g != 0 || t >= T) return;
-    for (int i = 1; i < groups; i++) add(part[threadIdx.x + i * per]);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+        const float top = fmaxf(m, m2), off = top == -INFINITY ? 0.f : top;
+        // (the smaller lane's term first, so that both lanes have the same sum)
+        const float a = s * ex2((m - off) * LOG2E), b = s2 * ex2((m2 - off) * LOG2E);
+        s = lane & o ? b + a : a + b;
+        m = top;
+    }
+    if (lane != 0) return;
     const int label = labels[t];
     const float l = logf(s);
     lse[t] = m + l;
@@ -443,6 +479,8 @@ __global__ void __launch_bounds__(COMBINE) combine_kernel(const float2 *stats, c
 __global__ void __launch_bounds__(1024) top_kernel(const float *dloss, const float *dlse, const int32_t *labels, int T, int V, float *top)
 {
     __shared__ float part[32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     float m = 0.f;
     for (int t = threadIdx.x; t < T; t += 1024) {
         const int label = labels[t];
@@ -458,14 +496,23 @@ __global__ void __launch_bounds__(1024) top_kernel(const float *dloss, const flo
     }
 }
 
-// fp32 sums to 16 bits, eight at a time (the count is a multiple of eight).
+// The parts' fp32 sums, in order, to 16 bits, eight values at a time (a part's n values are a multiple of eight).
 template <class A>
-__global__ void __launch_bounds__(256) round_kernel(const float *in, typename A::T *out, int64_t n)
+__global__ void __launch_bounds__(256) round_kernel(const float *in, int parts, int64_t part, typename A::T *out, int64_t n)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (int64_t)gridDim.x * 2048) {
         float v[8];
         F32::load4(in + i, v);
         F32::load4(in + i + 4, v + 4);
+#pragma unroll 4
+        for (int s = 1; s < parts; s++) {
+            float u[8];
+            F32::load4(in + s * part + i, u);
+            F32::load4(in + s * part + i + 4, u + 4);
+#pragma unroll
+            for (int j = 0; j < 8; j++) v[j] += u[j];
+        }
         A::store8(out + i, v);
     }
 }
@@ -480,19 +527,77 @@ static int piece_columns(int T, int V)
     return (int)((V + pieces - 1) / pieces + BN - 1) / BN * BN;
 }
 
-struct Layout {
-    int columns, pieces;
-    size_t d, sums, total;  // bytes: d after the top value, fp32 sums of dh when there are several pieces
+static int round_up(int n, int b) { return tiles(n, b) * b; }
+
+// Columns of a tile: equal ones over all n.
+static int tile_columns(int n) { return round_up(tiles(n, tiles(n, BN)), 32); }
+
+// The vocabulary's tiles for the logits: as wide as they go, unless narrower ones fill the last round of CTAs better
+// (100,003 columns for one row tile on 152 SMs: three rounds of 224 instead of 256).
+static int vocabulary_columns(int rows, int V, int sms)
+{
+    int best = BN;
+    int64_t least = INT64_MAX;
+    for (int bn = BN; bn >= 128; bn -= 32) {
+        const int64_t rounds = ((int64_t)tiles(rows, BM) * tiles(V, bn) + sms - 1) / sms, cost = rounds * (bn + 16);
+        if (cost < least) least = cost, best = bn;
+    }
+    return best;
+}
+
+// What a CTA of the gradients takes, in steps of BK: dh's items (nk0 each) dealt out first, dW's (nk1 each) so that the
+// longest CTA is as short as it gets.
+struct Deal {
+    int longer, long_items, short_items;
+    int64_t steps;
 };
 
+static Deal deal(int64_t items0, int64_t nk0, int64_t items1, int64_t nk1, int64_t G)
+{
+    Deal best = {0, 0, 0, INT64_MAX};
+    const int64_t q = items0 / G, r = items0 % G;
+    auto with = [&](int64_t s) {  // s items of the second job for a CTA without an extra one of the first
+        const int64_t rest = std::max<int64_t>(0, items1 - (G - r) * s);
+        if (s < 0 || (r == 0 && rest > 0)) return;
+        const int64_t l = r ? (rest + r - 1) / r : s;
+        const int64_t steps = std::max(r ? (q + 1) * nk0 + l * nk1 : 0, q * nk0 + s * nk1);
+        if (steps < best.steps) best = {(int)r, (int)l, (int)s, steps};
+    };
+    with((items1 + G - r - 1) / (G - r));
+    if (nk1 > 0) {  // about where all have the same
+        const int64_t s = ((items0 * nk0 + items1 * nk1) / G - q * nk0) / nk1;
+        for (int64_t i = s - 1; i <= s + 2; i++) with(i);
+    }
+    return best;
+}
+
+struct Layout {
+    int columns, pieces, parts;  // dh's sums over a piece are split into parts
+    int64_t part_rows;
+    size_t d, sums, total;  // bytes: d after the top value, fp32 sums of dh when there are several pieces or parts
+};
+
+// Splitting dh's sums pays where its few, long items would leave the other CTAs waiting: steps of 0.27 us are weighed
+// against a part's sums, written and read (8 bytes a value at 6 TB/s), and a launch for them.
 static Layout layout(int T, int H, int V)
 {
     Layout l;
+    const int sms = sm_count();
     l.columns = piece_columns(T, V);
     l.pieces = tiles(V, l.columns);
+    const int n = std::min(V, l.columns), nk0 = tiles(n, BK), nk1 = tiles(T, BK), nt = tiles(H, BN);
+    const int64_t items0 = (int64_t)tiles(T, BM) * nt, items1 = (int64_t)tiles(n, BM) * nt;
+    l.part_rows = round_up(T, BM);
+    l.parts = 1;
+    double least = 0;
+    for (int s = 1; s <= 32 && s <= nk0; s++) {
+        const Deal d = deal(items0 * s, tiles(nk0, s), items1, nk1, std::min<int64_t>(items0 * s + items1, sms));
+        const double us = 0.27 * d.steps + (s > 1 || l.pieces > 1 ? 3.0 / l.pieces + 1.3e-6 * s * T * H * (l.pieces > 1 ? 2 : 1) : 0);
+        if (s == 1 || us < least) least = us, l.parts = s;
+    }
     l.d = 256;
     l.sums = l.d + align256((size_t)T * l.columns * 2);
-    l.total = l.sums + (l.pieces > 1 ? align256((size_t)T * H * 4) : 0);
+    l.total = l.sums + (l.pieces > 1 || l.parts > 1 ? align256((size_t)l.parts * l.part_rows * H * 4) : 0);
     return l;
 }
 
@@ -501,7 +606,8 @@ static moe_status check(int T, int H, int V)
     MOE_REQUIRE(T >= 0 && T <= (1 << 24), "T must be in [0, 2^24] (got %d)", T);
     MOE_REQUIRE(H >= 8 && H % 8 == 0 && H <= (1 << 20), "H must be a multiple of 8 in [8, 2^20] (got %d)", H);
     MOE_REQUIRE(V >= 1 && V <= (1 << 24), "V must be in [1, 2^24] (got %d)", V);
-    MOE_REQUIRE((int64_t)tiles(T, BM) * tiles(V, BN) < (1 << 30), "too many tiles (T=%d V=%d)", T, V);
+    MOE_REQUIRE((int64_t)tiles(T, BM) * tiles(V, BN / 2) < (1 << 30) && (int64_t)std::max(T, V) * H < (1ll << 40),
+                "too many tiles (T=%d H=%d V=%d)", T, H, V);
     return MOE_OK;
 }
 
@@ -516,12 +622,34 @@ static moe_status check_types(const void *h, moe_dtype dtype, int T, int H, cons
     return MOE_OK;
 }
 
-template <Kind K>
-moe_status launch(const Params &p, const Maps &maps, cudaStream_t s)
+template <class F, class... A>
+moe_status launch(const char *what, F kernel, int grid, int threads, size_t smem, cudaStream_t s, const A &...args)
 {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];  // the set-up overlaps the end of the kernel before
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, args...));
+    return check_launch(what);
+}
+
+template <Kind K>
+moe_status product(Params &p, const Maps &maps, cudaStream_t s)
+{
+    auto items = [](const Job &g) { return g.m_tiles * g.n_tiles * g.parts; };
+    p.items0 = items(p.job[0]);
+    p.items1 = items(p.job[1]);
+    const int grid = (int)std::min<int64_t>((int64_t)p.items0 + p.items1, sm_count());
+    const Deal d = deal(p.items0, tiles(tiles(p.job[0].K, BK), p.job[0].parts), p.items1, tiles(p.job[1].K, BK), grid);
+    p.longer = d.longer, p.long_items = d.long_items, p.short_items = d.short_items;
     MOE_CUDA_TRY(cudaFuncSetAttribute(product_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM));
-    product_kernel<K><<<std::min(p.items, sm_count()), THREADS, SMEM, s>>>(p, maps);
-    return check_launch("cross_entropy");
+    return launch("cross_entropy", product_kernel<K>, grid, THREADS, SMEM, s, p, maps);
 }
 
 static CUtensorMapDataType map_type(moe_dtype t)
@@ -541,7 +669,7 @@ extern "C" moe_status moe_cross_entropy_workspace_size(int T, int H, int V, size
     MOE_REQUIRE(bytes, "bytes must not be NULL");
     moe_status st = check(T, H, V);
     if (st != MOE_OK) return st;
-    *bytes = align256((size_t)T * 4) + align256((size_t)tiles(V, BN) * T * 8);
+    *bytes = align256((size_t)T * 4) + align256((size_t)tiles(V, vocabulary_columns(T, V, sm_count())) * T * 8);
     return MOE_OK;
 }
 
@@ -563,22 +691,20 @@ extern "C" moe_status moe_cross_entropy(const void *h, moe_dtype dtype, int T, i
     MOE_REQUIRE(aligned16(ws), "ws must be 16-byte aligned");
     Params p = {};
     Maps maps = {};
-    p.job[0] = {tiles(T, BM), tiles(V, BN), tiles(H, BK), 0, 0, 0, 0, 0, 0, 0};
-    p.items0 = p.items = p.job[0].m_tiles * p.job[0].n_tiles;
-    p.idesc = tc::idesc_f16_f32(BM, BN, dtype == MOE_BF16);
+    const int bn = vocabulary_columns(T, V, sm_count()), n_tiles = tiles(V, bn);
+    p.job[0] = {tiles(T, BM), n_tiles, bn, H, 1, 0, 0, 0, 0, 0, 0};
+    p.idesc = tc::idesc_f16_f32(BM, 0, dtype == MOE_BF16);
     p.T = T, p.V = V, p.labels = labels, p.status = dev_status;
     p.label_z = static_cast<float *>(ws);
     p.stats = reinterpret_cast<float2 *>(static_cast<char *>(ws) + align256((size_t)T * 4));
     st = make_tmap_2d(&maps.a[0], h, map_type(dtype), 2, T, H, BK, BM);
-    if (st == MOE_OK) st = make_tmap_2d(&maps.b[0], w, map_type(dtype), 2, V, H, BK, BN);
+    if (st == MOE_OK) st = make_tmap_2d(&maps.b[0], w, map_type(dtype), 2, V, H, BK, bn);
     if (st != MOE_OK) return st;
     const cudaStream_t s = to_cuda(stream);
-    st = launch<LOSS>(p, maps, s);
+    st = product<LOSS>(p, maps, s);
     if (st != MOE_OK) return st;
-    int per = COMBINE;  // tokens of a CTA: fewer while the others' threads have tiles to take
-    while (per > 1 && (per / 2 >= T || (COMBINE / per * 2 <= p.job[0].n_tiles && tiles(T, per) < sm_count()))) per /= 2;
-    combine_kernel<<<tiles(T, per), COMBINE, 0, s>>>(p.stats, p.label_z, labels, T, V, p.job[0].n_tiles, per, loss, lse, dev_status);
-    return check_launch("cross_entropy_combine");
+    return launch("cross_entropy_combine", combine_kernel, tiles(T, COMBINE_WARPS), COMBINE_WARPS * 32, 0, s, p.stats, p.label_z, labels, T,
+                  V, n_tiles, loss, lse, dev_status);
 }
 
 extern "C" moe_status moe_cross_entropy_backward_workspace_size(int T, int H, int V, size_t *bytes)
@@ -619,60 +745,59 @@ extern "C" moe_status moe_cross_entropy_backward(const void *h, moe_dtype dtype,
     float *top = reinterpret_cast<float *>(base), *sums = reinterpret_cast<float *>(base + l.sums);
     void *d = base + l.d;
 
-    top_kernel<<<1, 1024, 0, s>>>(dloss, dlse, labels, T, V, top);
-    st = check_launch("cross_entropy_top");
+    st = launch("cross_entropy_top", top_kernel, 1, 1024, 0, s, dloss, dlse, labels, T, V, top);
     if (st != MOE_OK) return st;
     Params gp = {}, pp = {};
     Maps gm = {}, pm = {};
     const int f16 = dtype == MOE_F16;
-    gp.idesc = pp.idesc = tc::idesc_f16_f32(BM, BN, !f16);
+    gp.idesc = pp.idesc = tc::idesc_f16_f32(BM, 0, !f16);
     gp.T = T, gp.all = V, gp.labels = labels, gp.lse = lse, gp.dloss = dloss, gp.dlse = dlse, gp.top = pp.top = top;
     gp.status = pp.status = dev_status;
     gp.f16 = pp.f16 = f16;
-    const bool direct = l.pieces == 1;  // dh in one piece: no sums of pieces
+    const bool direct = l.pieces == 1 && l.parts == 1;  // dh leaves as it is: no sums of pieces or parts
+    const auto half = CU_TENSOR_MAP_SWIZZLE_64B;        // boxes of 32 16-bit columns
     st = make_tmap_2d(&gm.a[0], h, map_type(dtype), 2, T, H, BK, BM);
     if (st == MOE_OK) st = make_tmap_2d(&gm.b[0], w, map_type(dtype), 2, V, H, BK, BN);
-    if (st == MOE_OK) st = make_tmap_2d(&gm.out[0], d, map_type(dtype), 2, T, l.columns, 64, 32);
+    if (st == MOE_OK) st = make_tmap_2d(&gm.out[0], d, map_type(dtype), 2, T, l.columns, 32, 32, half);
     CUtensorMap d_k, d_m, w_n, h_n, out_h, out_w;
     if (st == MOE_OK) st = make_tmap_2d(&d_k, d, map_type(dtype), 2, T, l.columns, BK, BM);
     if (st == MOE_OK) st = make_tmap_2d(&d_m, d, map_type(dtype), 2, T, l.columns, 64, BK);
     if (st == MOE_OK) st = make_tmap_2d(&w_n, w, map_type(dtype), 2, V, H, 64, BK);
     if (st == MOE_OK) st = make_tmap_2d(&h_n, h, map_type(dtype), 2, T, H, 64, BK);
     if (st == MOE_OK && dh)
-        st = direct ? make_tmap_2d(&out_h, dh, map_type(dtype), 2, T, H, 64, 32) : make_tmap_2d(&out_h, sums, map_type(MOE_F32), 4, T, H, 32, 32);
+        st = direct ? make_tmap_2d(&out_h, dh, map_type(dtype), 2, T, H, 32, 32, half)
+                    : make_tmap_2d(&out_h, sums, map_type(MOE_F32), 4, l.parts * l.part_rows, H, 32, 32);
     if (st == MOE_OK && dw)
-        st = make_tmap_2d(&out_w, dw, map_type(dw_dtype), dtype_bytes(dw_dtype), V, H, dw_dtype == MOE_F32 ? 32 : 64, 32);
+        st = dw_dtype == MOE_F32 ? make_tmap_2d(&out_w, dw, map_type(MOE_F32), 4, V, H, 32, 32)
+                                 : make_tmap_2d(&out_w, dw, map_type(dtype), 2, V, H, 32, 32, half);
     if (st != MOE_OK) return st;
+    const int nt = tiles(H, BN), bn = tile_columns(H);
     for (int i = 0; i < l.pieces; i++) {
         const int v0 = i * l.columns, n = std::min(l.columns, V - v0);
         gp.v0 = v0;
         gp.V = n;
-        gp.job[0] = {tiles(T, BM), tiles(n, BN), tiles(H, BK), 0, 0, 0, v0, 0, 0, 0};
-        gp.items0 = gp.items = gp.job[0].m_tiles * gp.job[0].n_tiles;
-        st = launch<GRAD>(gp, gm, s);
+        gp.job[0] = {tiles(T, BM), tiles(n, BN), BN, H, 1, 0, v0, 0, 0, 0, 0};
+        st = product<GRAD>(gp, gm, s);
         if (st != MOE_OK) return st;
         int j = 0;
         if (dh) {
-            pp.job[j] = {tiles(T, BM), tiles(H, BN), tiles(n, BK), 0, 1, 0, v0, 0, !direct && i > 0, !direct};
+            pp.job[j] = {tiles(T, BM), nt, bn, n, l.parts, 0, v0, 0, (int)l.part_rows, !direct && i > 0, !direct};
             pm.a[j] = d_k, pm.b[j] = w_n, pm.out[j] = out_h;
             j++;
         }
         if (dw) {
-            pp.job[j] = {tiles(n, BM), tiles(H, BN), tiles(T, BK), 1, 1, 0, 0, v0, accumulate != 0, dw_dtype == MOE_F32};
+            pp.job[j] = {tiles(n, BM), nt, bn, T, 1, 1, 0, v0, 0, accumulate != 0, dw_dtype == MOE_F32};
             pm.a[j] = d_m, pm.b[j] = h_n, pm.out[j] = out_w;
             j++;
         }
-        pp.items0 = pp.job[0].m_tiles * pp.job[0].n_tiles;
-        pp.items = pp.items0 + (j > 1 ? pp.job[1].m_tiles * pp.job[1].n_tiles : 0);
-        st = launch<PROD>(pp, pm, s);
+        st = product<PROD>(pp, pm, s);
         if (st != MOE_OK) return st;
     }
     if (dh && !direct) {
         const int64_t n = (int64_t)T * H;
         const int grid = (int)std::min<int64_t>((n + 2047) / 2048, (int64_t)sm_count() * 8);
-        if (f16) round_kernel<Fp16><<<grid, 256, 0, s>>>(sums, static_cast<uint16_t *>(dh), n);
-        else round_kernel<Bf16><<<grid, 256, 0, s>>>(sums, static_cast<uint16_t *>(dh), n);
-        return check_launch("cross_entropy_round");
+        return f16 ? launch("cross_entropy_round", round_kernel<Fp16>, grid, 256, 0, s, sums, l.parts, l.part_rows * H, static_cast<uint16_t *>(dh), n)
+                   : launch("cross_entropy_round", round_kernel<Bf16>, grid, 256, 0, s, sums, l.parts, l.part_rows * H, static_cast<uint16_t *>(dh), n);
     }
     return MOE_OK;
 }

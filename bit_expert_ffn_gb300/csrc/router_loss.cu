@@ -33,11 +33,11 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// The largest of the warp's values (not NaN), by one integer reduction: the bits of negative values are turned over.
 __device__ __forceinline__ float warp_max(float v)
 {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
+    const int b = __float_as_int(v), m = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
+    return __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
 }
 
 __device__ __forceinline__ float warp_sum(float v)
@@ -74,6 +74,9 @@ __device__ __forceinline__ void load_row(const typename A::T *row, int E, int la
     }
 }
 
+// Words of a CTA's part: E sums of p, E counts, sum of lse^2, tokens; whole 16 bytes where the experts are.
+__host__ __device__ constexpr int pitch_of(int E) { return 2 * E + 4; }
+
 struct Params {
     const void *logits;
     int T, E, k;
@@ -81,72 +84,88 @@ struct Params {
     const uint8_t *keep;
     float *loss, *mean, *lse;
     int32_t *counts;
-    float *part;  // [CTAs][E] sums of p, [CTAs][E] counts, [CTAs][2] sum of lse^2 and tokens; NULL: one cluster
+    float *part;  // the CTAs' parts; NULL: one cluster
     int32_t *status;
 };
 
 // Sums over `parts` parts in order, a slice of the experts per CTA of the
-// cluster.  get(part, i): word i of the part's E sums, E counts, lse^2, tokens.
-template <class G>
+// cluster.  get<V>(part, i): words i .. i+V-1 of the part's E sums, E counts,
+// sum of lse^2 and tokens.  Groups of threads take every G-th part of V columns.
+template <int kThreads, int V, class G>
 __device__ __forceinline__ void finish(const Params &p, int parts, G get, float *red, float *slot)
 {
     const int C = gridDim.x, r = C > 1 ? (int)cluster_rank() : 0, tid = threadIdx.x;
-    const int E = p.E, e0 = (int)((int64_t)E * r / C), e1 = (int)((int64_t)E * (r + 1) / C), w = e1 - e0;
-    __shared__ float s_n, s_z;
+    const int E = p.E, units = (E + V - 1) / V;
+    const int e0 = (int)((int64_t)units * r / C) * V, w = (int)((int64_t)units * (r + 1) / C) - e0 / V;
+    const int per = min((w + 31) & ~31, kThreads), groups = max(1, min(kThreads / max(per, 32), parts));
+    const int g = per ? tid / per : groups, c0 = per ? tid % per : 0;
+    __shared__ float s_n, s_z, s_dot[kThreads / 32];
     __shared__ int s_tok;
-    if (tid < 32) {  // tokens and the squares, by every CTA
-        int n = 0;
-        float z = 0.f;
-        for (int i = tid; i < parts; i += 32) {
-            z += get(i, 2 * E);
-            n += __float_as_int(get(i, 2 * E + 1));
-        }
-        z = warp_sum(z);
-        n = __reduce_add_sync(0xffffffffu, n);
-        if (tid == 0) s_tok = n, s_n = n > 0 ? (float)n : 1.f, s_z = z;
-    }
-    // groups of threads take every G-th part of a column
-    const int wide = (w + 31) & ~31, groups = max(1, min(THREADS / max(wide, 32), parts));
-    float *sum = red;
-    int *cnt = reinterpret_cast<int *>(red + THREADS);
-    __syncthreads();
     float dot = 0.f;
-    for (int c0 = 0; c0 < w; c0 += THREADS / groups) {  // (one round, unless a slice is wider than the CTA)
-        const int per = THREADS / groups, g = tid / per, c = c0 + tid % per;
-        float a = 0.f;
-        int b = 0;
+    for (int c = c0;; c += per) {  // (one round, unless a slice is wider than the CTA)
+        float a[V];
+        int b[V];
+#pragma unroll
+        for (int i = 0; i < V; i++) a[i] = 0.f, b[i] = 0;
         if (g < groups && c < w) {
-#pragma unroll 4
+#pragma unroll 8
             for (int i = g; i < parts; i += groups) {
-                a += get(i, e0 + c);
-                b += __float_as_int(get(i, E + e0 + c));
+                float x[V], y[V];
+                get(i, e0 + c * V, x);
+                get(i, E + e0 + c * V, y);
+#pragma unroll
+                for (int j = 0; j < V; j++) a[j] += x[j], b[j] += __float_as_int(y[j]);
             }
         }
-        sum[tid] = a;
-        cnt[tid] = b;
+        if (groups > 1) {
+#pragma unroll
+            for (int j = 0; j < V; j++) {
+                red[j * kThreads + tid] = a[j];
+                red[(V + j) * kThreads + tid] = __int_as_float(b[j]);
+            }
+        }
+        if (c == c0 && tid >= kThreads - 32) {  // tokens and the squares, by the last warp of every CTA
+            int n = 0;
+            float z = 0.f;
+            for (int i = tid & 31; i < parts; i += 32) {
+                float x[1], y[1];
+                get(i, 2 * E, x);
+                get(i, 2 * E + 1, y);
+                z += x[0];
+                n += __float_as_int(y[0]);
+            }
+            z = warp_sum(z);
+            n = __reduce_add_sync(0xffffffffu, n);
+            if ((tid & 31) == 0) s_tok = n, s_n = n > 0 ? (float)n : 1.f, s_z = z;
+        }
         __syncthreads();
         if (g == 0 && c < w) {
             for (int i = 1; i < groups; i++) {
-                a += sum[tid + i * per];
-                b += cnt[tid + i * per];
+#pragma unroll
+                for (int j = 0; j < V; j++) {
+                    a[j] += red[j * kThreads + tid + i * per];
+                    b[j] += __float_as_int(red[(V + j) * kThreads + tid + i * per]);
+                }
             }
-            const float m = a / s_n;
-            p.mean[e0 + c] = m;
-            p.counts[e0 + c] = b;
-            dot += (float)b * m;
+#pragma unroll
+            for (int j = 0; j < V; j++) {
+                const float m = a[j] / s_n;
+                p.mean[e0 + c * V + j] = m;
+                p.counts[e0 + c * V + j] = b[j];
+                dot += (float)b[j] * m;
+            }
         }
+        if (per == 0 || c - c0 + per >= w) break;
         __syncthreads();
     }
     dot = warp_sum(dot);
-    if ((tid & 31) == 0) sum[tid >> 5] = dot;
+    if ((tid & 31) == 0) s_dot[tid >> 5] = dot;
     __syncthreads();
-    if (tid == 0) {
-        dot = 0.f;
-        for (int i = 0; i < WARPS; i++) dot += sum[i];
-        *slot = dot;
+    if (tid < 32) {
+        dot = warp_sum(tid < kThreads / 32 ? s_dot[tid] : 0.f);
+        if (tid == 0) *slot = dot;
     }
     if (C > 1) cluster_sync();
-    else __syncthreads();
     if (r == 0 && tid == 0) {
         dot = 0.f;
         for (int i = 0; i < C; i++) dot += C > 1 ? __uint_as_float(ld_cluster((uint32_t)__cvta_generic_to_shared(slot), i)) : *slot;
@@ -242,20 +261,33 @@ __global__ void __launch_bounds__(THREADS, NV <= 16 ? 2 : 1) loss_kernel(const _
     }
     __syncthreads();
     if (p.part) {
-        for (int c = threadIdx.x; c < 2 * E + 2; c += THREADS) p.part[(int64_t)blockIdx.x * (2 * E + 2) + c] = cta[c];
+        for (int c = threadIdx.x; c < 2 * E + 2; c += THREADS) p.part[(int64_t)blockIdx.x * pitch_of(E) + c] = cta[c];
         return;
     }
     const int C = gridDim.x;
     if (C > 1) cluster_sync();
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(cta);
-    finish(p, C, [&](int i, int w) { return C > 1 ? __uint_as_float(ld_cluster(base + w * 4, i)) : cta[w]; },
-           cta + 2 * E + 2, &s_slot);
+    finish<THREADS, 1>(p, C, [&](int i, int w, float (&v)[1]) { v[0] = C > 1 ? __uint_as_float(ld_cluster(base + w * 4, i)) : cta[w]; },
+                       cta + 2 * E + 2, &s_slot);
 }
 
-__global__ void __launch_bounds__(THREADS, 1) finish_kernel(const __grid_constant__ Params p, int parts)
+constexpr int FINISH = 1024;
+
+template <int V>
+__global__ void __launch_bounds__(FINISH, 1) finish_kernel(const __grid_constant__ Params p, int parts)
 {
-    __shared__ float red[2 * THREADS], slot;
-    finish(p, parts, [&](int i, int w) { return p.part[(int64_t)i * (2 * p.E + 2) + w]; }, red, &slot);
+    __shared__ float red[2 * V * FINISH], slot;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const float *part = p.part;
+    const int pitch = pitch_of(p.E);
+    finish<FINISH, V>(
+        p, parts,
+        [&](int i, int w, auto &v) {
+            const float *q = part + (int64_t)i * pitch + w;
+            if constexpr (sizeof(v) == 16) F32::load4(q, v);
+            else v[0] = *q;
+        },
+        red, &slot);
 }
 
 struct GradParams {
@@ -413,7 +445,7 @@ extern "C" moe_status moe_router_loss_workspace_size(int T, int E, size_t *bytes
     MOE_REQUIRE(bytes, "bytes must not be NULL");
     moe_status st = check(MOE_F32, T, E, 1);
     if (st != MOE_OK) return st;
-    *bytes = T <= CLUSTER_ROWS ? 0 : (size_t)grid_of(T, E) * (2 * E + 2) * 4;
+    *bytes = T <= CLUSTER_ROWS ? 0 : (size_t)grid_of(T, E) * pitch_of(E) * 4;
     return MOE_OK;
 }
 
@@ -464,11 +496,17 @@ extern "C" moe_status moe_router_loss(const void *logits, moe_dtype dtype, int T
     if (st != MOE_OK || !need) return st;
     int c = 1;
     while (c < MAX_CLUSTER && c * 64 < E) c *= 2;
-    at[0].val.clusterDim.x = (unsigned)c;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute fin[2];
+    fin[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    fin[0].val.programmaticStreamSerializationAllowed = 1;
+    fin[1] = at[0];
+    fin[1].val.clusterDim.x = (unsigned)c;
+    cfg.attrs = fin;
+    cfg.numAttrs = 2;
     cfg.gridDim = dim3((unsigned)c);
+    cfg.blockDim = dim3(FINISH);
     cfg.dynamicSmemBytes = 0;
-    MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, finish_kernel, p, grid));
+    MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, E % 4 == 0 ? finish_kernel<4> : finish_kernel<1>, p, grid));
     return check_launch("router_loss_finish");
 }
 
