@@ -26,7 +26,7 @@ namespace aw {
 constexpr int WARPS = 8, THREADS = WARPS * 32;
 constexpr int BLOCK = 256;                   // values that share scales, and of a warp's turn
 constexpr int MIN_CHUNK = WARPS * BLOCK;     // values of a CTA
-constexpr int FEW = 16, MANY = 384;          // tensors of a launch: its parameters hold 32,764 bytes
+constexpr int FEW = 16, MANY = 428;          // tensors of a launch: its parameters hold 32,764 bytes
 constexpr float SMALLEST = 7.888609052210118e-31f;  // 2^-100
 
 struct Tensor {
@@ -36,9 +36,8 @@ struct Tensor {
     void *m, *v;
     float *scales;
     int64_t n;
-    int32_t first;  // chunks before it
-    int8_t pt, gt, vec, pad;
     float lr_factor, decay;
+    int8_t pt, gt, vec, pad[5];
 };
 
 struct Common {
@@ -53,6 +52,7 @@ struct Common {
 template <int N>
 struct Params {
     Common c;
+    int32_t first[N];  // chunks before a tensor
     Tensor t[N];
 };
 
@@ -84,11 +84,11 @@ __device__ __forceinline__ void store4(void *p, int64_t i, int type, const float
     else Fp16::store4(static_cast<uint16_t *>(p) + i, v);
 }
 
-__device__ __forceinline__ float load1(const void *p, int64_t i, int type)
+constexpr int BYTES = 3;  // a type beside moe_dtype's: 8-bit codes
+
+__device__ __forceinline__ float value(uint32_t raw, int type)
 {
-    if (type == MOE_F32) return static_cast<const float *>(p)[i];
-    const uint16_t q = static_cast<const uint16_t *>(p)[i];
-    return type == MOE_BF16 ? bf16_to_f32(q) : fp16_to_f32(q);
+    return type == MOE_F32 ? __uint_as_float(raw) : type == MOE_BF16 ? __uint_as_float(raw << 16) : fp16_to_f32((uint16_t)raw);
 }
 
 __device__ __forceinline__ void store1(void *p, int64_t i, int type, float v)
@@ -139,7 +139,7 @@ __device__ __forceinline__ int find(const Params<N> &p, int chunk)
     int lo = 0, hi = p.c.n;  // the last tensor whose first chunk is at most `chunk`
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (p.t[mid].first <= chunk) lo = mid;
+        if (p.first[mid] <= chunk) lo = mid;
         else hi = mid;
     }
     return lo;
@@ -152,6 +152,23 @@ __device__ __forceinline__ int64_t place(int64_t base, int i, int lane)
     return kVec ? base + (i >> 2) * 128 + lane * 4 + (i & 3) : base + i * 32 + lane;
 }
 
+// A lane's eight values of 256 from `base`, as they lie, zero past the `left` that there are.
+template <bool kVec>
+__device__ __forceinline__ void load8(const void *p, int64_t base, int64_t left, int lane, int type, uint32_t (&r)[8])
+{
+    auto each = [&](auto unit) {
+        const decltype(unit) *q = static_cast<const decltype(unit) *>(p) + base;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const int e = (int)place<kVec>(0, i, lane);
+            r[i] = e < left ? q[e] : 0;
+        }
+    };
+    if (type == MOE_F32) each(uint32_t{});
+    else if (type == BYTES) each(uint8_t{});
+    else each(uint16_t{});
+}
+
 struct Scalars {
     float scale, shrink, rate, root2;
 };
@@ -162,7 +179,7 @@ __device__ __forceinline__ void block(const Common &c, const Tensor &t, const Sc
     float x[8], g[8], m[8], v[8];
     const void *xp = t.master ? t.master : t.param;
     const int xt = t.master ? (int)MOE_F32 : t.pt;
-    const bool whole = kVec && base + BLOCK <= t.n;  // (a last, short block goes value by value)
+    const bool whole = kVec && base + BLOCK <= t.n;  // (a last, short block goes value by value; k8: block8 takes whole ones)
     float um = 0.f, ur = 0.f;
     if (k8) {
         const float2 u = *reinterpret_cast<const float2 *>(t.scales + base / BLOCK * 2);
@@ -196,23 +213,25 @@ __device__ __forceinline__ void block(const Common &c, const Tensor &t, const Sc
                 unpack4(rv[j], MOE_F32, v + 4 * j);
             }
         }
-    } else {
+    } else {  // (all loads before the first use)
+        uint32_t rg[8], rx[8], rm[8], rv[8];
+        const int64_t left = t.n - base;
+        load8<kVec>(t.grad, base, left, lane, t.gt, rg);
+        load8<kVec>(xp, base, left, lane, xt, rx);
+        load8<kVec>(t.m, base, left, lane, k8 ? BYTES : (int)MOE_F32, rm);
+        load8<kVec>(t.v, base, left, lane, k8 ? BYTES : (int)MOE_F32, rv);
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            const int64_t e = place<kVec>(base, i, lane);
-            x[i] = g[i] = m[i] = v[i] = 0.f;
-            if (e < t.n) {
-                g[i] = load1(t.grad, e, t.gt);
-                x[i] = load1(xp, e, xt);
-                if (k8) {
-                    float q[4];
-                    e4m3_values(static_cast<const uint8_t *>(t.m)[e], q);
-                    m[i] = q[0];
-                    v[i] = root_value(static_cast<const uint8_t *>(t.v)[e]);
-                } else {
-                    m[i] = static_cast<const float *>(t.m)[e];
-                    v[i] = static_cast<const float *>(t.v)[e];
-                }
+            g[i] = value(rg[i], t.gt);
+            x[i] = value(rx[i], xt);
+            if (k8) {
+                float q[4];
+                e4m3_values(rm[i], q);
+                m[i] = q[0];
+                v[i] = root_value(rv[i]);
+            } else {
+                m[i] = __uint_as_float(rm[i]);
+                v[i] = __uint_as_float(rv[i]);
             }
         }
     }
@@ -304,11 +323,160 @@ __device__ __forceinline__ void block(const Common &c, const Tensor &t, const Sc
     }
 }
 
-template <int N>
-__global__ void __launch_bounds__(THREADS) step_kernel(const __grid_constant__ Params<N> p)
+// 256 values with 8-bit states, whole and aligned, as a rule: false, and nothing done, when the block wants block()'s
+// exact steps: a gradient that is not finite, roots so small that the fast root of a subnormal v, 0, would not get the same
+// code (below 2^-46 of the largest all do: code 1), or a root next to a border between two codes.  The fast root is within 2^-23 of the correctly rounded one, its product with the block's
+// factor within 3 last places: eight of 2^19 to either side of a border are left to the exact steps, so
+// that the codes are theirs in every case (8 blocks of 1,000).  The largest root is the rounded root of the
+// largest v, since rounding keeps the order.
+// Four values of a type as they lie, and in fp32.
+template <class A>
+struct Four {
+    using Raw = std::conditional_t<A::kBytes == 4, uint4, uint2>;
+    __device__ static Raw raw(const void *p, int64_t i) { return *reinterpret_cast<const Raw *>(static_cast<const typename A::T *>(p) + i); }
+    __device__ static void unpack(const Raw &q, float *v) { A::load4(reinterpret_cast<const typename A::T *>(&q), v); }
+};
+
+// A lane's places in a chunk's tensors; blocks are `o` values further on.
+template <class G, class X>
+struct At {
+    const typename G::T *g;
+    typename X::T *x;  // the fp32 copy, or the parameter
+    void *p;           // the parameter beside a copy, or NULL
+    uint8_t *m, *v;
+    float2 *scales;
+    int pt;
+
+    __device__ At(const Tensor &t, int64_t i, int lane)
+        : g(static_cast<const typename G::T *>(t.grad) + i + lane * 4), m(static_cast<uint8_t *>(t.m) + i + lane * 4),
+          v(static_cast<uint8_t *>(t.v) + i + lane * 4), scales(reinterpret_cast<float2 *>(t.scales) + i / BLOCK), pt(t.pt)
+    {
+        x = static_cast<typename X::T *>(t.master ? static_cast<void *>(t.master) : t.param) + i + lane * 4;
+        p = t.master ? static_cast<char *>(t.param) + (i + lane * 4) * (pt == MOE_F32 ? 4 : 2) : nullptr;
+    }
+};
+
+// What a lane loads of a block.
+template <class G, class X>
+struct Held8 {
+    typename Four<G>::Raw g[2];
+    typename Four<X>::Raw x[2];
+    uint32_t m[2], v[2];
+    float2 u;
+
+    __device__ void load(const At<G, X> &at, int o)
+    {
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            g[j] = Four<G>::raw(at.g + o, 128 * j);
+            x[j] = Four<X>::raw(at.x + o, 128 * j);
+            m[j] = *reinterpret_cast<const uint32_t *>(at.m + o + 128 * j);
+            v[j] = *reinterpret_cast<const uint32_t *>(at.v + o + 128 * j);
+        }
+        u = at.scales[o / BLOCK];
+    }
+};
+
+template <class G, class X>
+__device__ __forceinline__ bool block8(const Common &c, const At<G, X> &at, const Scalars &s, int o, int lane, const Held8<G, X> &raw)
+{
+    float x[8], m[8], v[8], r[8];
+    const float2 u = raw.u;
+    float odd = 0.f, top_m = 0.f, top_v = 0.f;
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+        float g[4];
+        Four<G>::unpack(raw.g[j], g);
+        Four<X>::unpack(raw.x[j], x + 4 * j);
+        e4m3_values(raw.m[j], m + 4 * j);
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const int i = 4 * j + e;
+            const float gi = g[e] * s.scale, g2 = __fmul_rn(gi, gi), root = __fmul_rn(root_value(raw.v[j] >> (8 * e) & 255u), u.y);
+            odd = fmaf(g2, 0.f, odd);  // NaN when a square is not finite
+            m[i] = __fadd_rn(__fmul_rn(__fmul_rn(m[i], u.x), c.b1), __fmul_rn(gi, c.o1));
+            v[i] = __fadd_rn(__fmul_rn(__fmul_rn(root, root), c.b2), __fmul_rn(g2, c.o2));
+            top_m = fmaxf(top_m, fabsf(m[i]));
+            top_v = fmaxf(top_v, v[i]);
+        }
+    }
+    top_m = warp_top(top_m);
+    top_v = warp_top(top_v);
+    if (top_m < SMALLEST) top_m = 0.f;
+    const float top_r = __fsqrt_rn(top_v);
+    if (__any_sync(0xffffffffu, odd != 0.f) || (top_v > 0.f && top_r < 1.4210855e-14f)) return false;  // (2^-46)
+    // the four quotients in four lanes at once: 448 / top, top / 448 and the root's
+    const float top = lane & 1 ? top_r : top_m, full = lane & 1 ? 1.9375f : 448.f;
+    const float q = top > 0.f ? __fdiv_rn(lane & 2 ? top : full, lane & 2 ? full : top) : 0.f;
+    const float im = __shfl_sync(0xffffffffu, q, 0), ir = __shfl_sync(0xffffffffu, q, 1);
+    const float2 held = make_float2(__shfl_sync(0xffffffffu, q, 2), __shfl_sync(0xffffffffu, q, 3));
+    uint32_t close = ~0u, codes[2];
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+        codes[j] = 0;
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const int i = 4 * j + e;
+            asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r[i]) : "f"(v[i]));
+            const uint32_t b = __float_as_uint(fmaxf(__fmul_rn(r[i], ir), 17.f / 524288.f));  // code 1 at least
+            close = min(close, (b + (8u - 0x40000u)) & 0x7FFFFu);
+            const uint32_t near = (b + (0x40000u - (112u << 23))) >> 19;  // (no ties here: they are close)
+            codes[j] |= (v[i] > 0.f ? near : 0u) << (8 * e);
+        }
+    }
+    if (__any_sync(0xffffffffu, close <= 16u)) return false;
+    if (lane == 0) at.scales[o / BLOCK] = held;
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const int i = 4 * j + e;
+            float inv;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(r[i], s.root2, c.eps)));
+            x[i] = fmaf(x[i], s.shrink, -(m[i] * s.rate * inv));
+            m[i] = __fmul_rn(m[i], im);
+        }
+        X::store4(at.x + o + 128 * j, x + 4 * j);
+        if (X::kBytes == 4 && at.p) store4(at.p, o + 128 * j, at.pt, x + 4 * j);
+        *reinterpret_cast<uint32_t *>(at.m + o + 128 * j) = e4m3_codes(m + 4 * j);
+        *reinterpret_cast<uint32_t *>(at.v + o + 128 * j) = codes[j];
+    }
+    return true;
+}
+
+template <class F>
+__device__ __forceinline__ void on_type(int type, F f)
+{
+    if (type == MOE_F32) f(F32{});
+    else if (type == MOE_BF16) f(Bf16{});
+    else f(Fp16{});
+}
+
+// A warp's blocks of a chunk, the next one's values on their way.  Returns which of them are left to the exact steps: a
+// last short block, values next to a border.
+template <class G, class X>
+__device__ __forceinline__ uint32_t blocks8(const Common &c, const Tensor &t, const Scalars &s, int64_t base, int n, int lane)
+{
+    const At<G, X> at(t, base, lane);
+    Held8<G, X> cur, nxt;
+    uint32_t left = 0;
+    if (BLOCK <= n) cur.load(at, 0);
+#pragma unroll 1
+    for (int o = 0; o < n; o += MIN_CHUNK) {
+        if (o + MIN_CHUNK + BLOCK <= n) nxt.load(at, o + MIN_CHUNK);
+        if (o + BLOCK > n || !block8<G, X>(c, at, s, o, lane, cur)) left |= 1u << (o / MIN_CHUNK);
+        cur = nxt;
+    }
+    return left;
+}
+
+// k8: the launch's tensors have 8-bit states.
+template <int N, bool k8>
+__global__ void __launch_bounds__(THREADS, 3) step_kernel(const __grid_constant__ Params<N> p)
 {
     const Common &c = p.c;
-    const Tensor &t = p.t[find(p, blockIdx.x)];
+    const int which = find(p, blockIdx.x);
+    const Tensor &t = p.t[which];
     float lr = c.lr, rate1 = c.rate1;
     Scalars s;
     s.scale = c.grad_scale ? *c.grad_scale : 1.f;
@@ -323,12 +491,19 @@ __global__ void __launch_bounds__(THREADS) step_kernel(const __grid_constant__ P
     s.rate = lr * rate1;
     s.shrink = 1.f - lr * t.decay;
     const int lane = lane_id();
-    const int64_t begin = (int64_t)(blockIdx.x - t.first) * c.chunk, end = min(begin + c.chunk, t.n);
-    for (int64_t base = begin + warp_id() * BLOCK; base < end; base += MIN_CHUNK) {
-        if (t.scales) {
-            if (t.vec) block<true, true>(c, t, s, base, lane);
-            else block<true, false>(c, t, s, base, lane);
-        } else {
+    const int64_t begin = (int64_t)(blockIdx.x - p.first[which]) * c.chunk, end = min(begin + c.chunk, t.n);
+    const int64_t first = begin + warp_id() * BLOCK;
+    if (k8) {
+        uint32_t left = ~0u;
+        if (t.vec && first < end)
+            on_type(t.gt, [&](auto g) {
+                on_type(t.master ? (int)MOE_F32 : t.pt,
+                        [&](auto x) { left = blocks8<decltype(g), decltype(x)>(c, t, s, first, (int)(end - first), lane); });
+            });
+        for (int64_t base = first; base < end; base += MIN_CHUNK, left >>= 1)
+            if (left & 1) block<true, false>(c, t, s, base, lane);
+    } else {
+        for (int64_t base = first; base < end; base += MIN_CHUNK) {
             if (t.vec) block<false, true>(c, t, s, base, lane);
             else block<false, false>(c, t, s, base, lane);
         }
@@ -337,12 +512,13 @@ __global__ void __launch_bounds__(THREADS) step_kernel(const __grid_constant__ P
 
 // The states' values: t.master takes m's, t.param v's (fp32, either may be NULL).
 template <int N>
-__global__ void __launch_bounds__(THREADS) states_kernel(const __grid_constant__ Params<N> p)
+__global__ void __launch_bounds__(THREADS, 8) states_kernel(const __grid_constant__ Params<N> p)
 {
-    const Tensor &t = p.t[find(p, blockIdx.x)];
+    const int which = find(p, blockIdx.x);
+    const Tensor &t = p.t[which];
     float *mo = t.master, *vo = static_cast<float *>(t.param);
     const int lane = lane_id();
-    const int64_t begin = (int64_t)(blockIdx.x - t.first) * p.c.chunk, end = min(begin + p.c.chunk, t.n);
+    const int64_t begin = (int64_t)(blockIdx.x - p.first[which]) * p.c.chunk, end = min(begin + p.c.chunk, t.n);
     for (int64_t base = begin + warp_id() * BLOCK; base < end; base += MIN_CHUNK) {
         float2 u = make_float2(0.f, 0.f);
         if (t.scales) u = *reinterpret_cast<const float2 *>(t.scales + base / BLOCK * 2);
@@ -369,18 +545,19 @@ __global__ void __launch_bounds__(THREADS) states_kernel(const __grid_constant__
             }
             continue;
         }
+        uint32_t rm[8], rv[8];
+        load8<false>(t.m, base, t.n - base, lane, t.scales ? BYTES : (int)MOE_F32, rm);
+        load8<false>(t.v, base, t.n - base, lane, t.scales ? BYTES : (int)MOE_F32, rv);
+#pragma unroll
         for (int i = 0; i < 8; i++) {
             const int64_t e = place<false>(base, i, lane);
             if (e >= t.n) continue;
-            float q[4], v;
+            float q[4] = {__uint_as_float(rm[i])}, v = __uint_as_float(rv[i]);
             if (t.scales) {
-                e4m3_values(static_cast<const uint8_t *>(t.m)[e], q);
+                e4m3_values(rm[i], q);
                 q[0] = __fmul_rn(q[0], u.x);
-                v = __fmul_rn(root_value(static_cast<const uint8_t *>(t.v)[e]), u.y);
+                v = __fmul_rn(root_value(rv[i]), u.y);
                 v = __fmul_rn(v, v);
-            } else {
-                q[0] = static_cast<const float *>(t.m)[e];
-                v = static_cast<const float *>(t.v)[e];
             }
             if (mo) mo[e] = q[0];
             if (vo) vo[e] = v;
@@ -403,9 +580,9 @@ static moe_status check(const moe_adamw_tensor *t, int n)
     return MOE_OK;
 }
 
-// Fills launches of up to MANY tensors; `one` sets a tensor's outputs and says whether its pointers are aligned for fours.
+// Fills launches of up to MANY tensors (kind 0 or 1: those without or with scales; -1: all); `one` sets a tensor's outputs and says whether its pointers are aligned for fours.
 template <class K, class F>
-moe_status launch(const moe_adamw_tensor *tensors, int n, const Common &c, cudaStream_t s, const char *what, K kernel, F one)
+moe_status launch(const moe_adamw_tensor *tensors, int n, int kind, const Common &c, const char *what, K kernel, F one)
 {
     int64_t total = 0;
     for (int i = 0; i < n; i++) total += tensors[i].n;
@@ -422,13 +599,14 @@ moe_status launch(const moe_adamw_tensor *tensors, int n, const Common &c, cudaS
         int64_t chunks = 0;
         for (; i < n && p.c.n < kN; i++) {
             const moe_adamw_tensor &a = tensors[i];
-            if (a.n == 0) continue;
+            if (a.n == 0 || (kind >= 0 && kind != (a.scales != nullptr))) continue;
             const int64_t more = (a.n + chunk - 1) / chunk;
             if (more > INT32_MAX) return fail(MOE_ERR_UNSUPPORTED, "tensor %d is too large (n=%lld)", i, (long long)a.n);
             if (chunks + more > INT32_MAX) break;
+            p.first[p.c.n] = (int32_t)chunks;
             Tensor &t = p.t[p.c.n++];
-            t = {a.param, a.grad, a.master, a.m, a.v, a.scales, a.n, (int32_t)chunks, (int8_t)a.param_dtype, (int8_t)a.grad_dtype,
-                 0, 0, a.lr_factor, a.weight_decay};
+            t = {a.param, a.grad, a.master, a.m, a.v, a.scales, a.n, a.lr_factor, a.weight_decay, (int8_t)a.param_dtype,
+                 (int8_t)a.grad_dtype, 0, {}};
             const int states = a.scales ? 4 : 16;
             t.vec = aligned_to(a.m, states) && aligned_to(a.v, states);
             one(i, t);
@@ -449,7 +627,6 @@ moe_status launch(const moe_adamw_tensor *tensors, int n, const Common &c, cudaS
         }
         if (st != MOE_OK) return st;
     }
-    (void)s;
     return MOE_OK;
 }
 
@@ -499,7 +676,7 @@ extern "C" moe_status moe_adamw_step(const moe_adamw_tensor *tensors, int n_tens
     MOE_REQUIRE(o, "options must not be NULL");
     MOE_REQUIRE(o->beta1 >= 0 && o->beta1 < 1 && o->beta2 >= 0 && o->beta2 < 1, "beta1 and beta2 must be in [0, 1) (got %g, %g)",
                 o->beta1, o->beta2);
-    MOE_REQUIRE((float)o->eps > 0 && (float)o->eps < INFINITY, "eps must be positive and finite (got %g)", o->eps);
+    MOE_REQUIRE((float)o->eps >= 1.17549435e-38f && (float)o->eps < INFINITY, "eps must be a normal fp32 number above zero (got %g)", o->eps);
     MOE_REQUIRE(o->step_dev || o->step >= 1, "step must be 1 or more (got %lld)", (long long)o->step);
     MOE_REQUIRE(o->lr_dev || (o->lr - o->lr == 0), "lr must be finite (got %g)", o->lr);
     MOE_REQUIRE(aligned_to(o->lr_dev, 4) && aligned_to(o->grad_scale, 4) && aligned_to(o->step_dev, 8) && aligned_to(dev_status, 4),
@@ -528,14 +705,21 @@ extern "C" moe_status moe_adamw_step(const moe_adamw_tensor *tensors, int n_tens
     c.log_b1 = (float)l1, c.log_b2 = (float)l2;
     c.lr_dev = o->lr_dev, c.grad_scale = o->grad_scale, c.step_dev = o->step_dev, c.status = dev_status;
     const cudaStream_t s = to_cuda(stream);
-    return launch(
-        tensors, n_tensors, c, s, "adamw_step",
-        [&](auto &p, unsigned grid) { step_kernel<<<grid, THREADS, 0, s>>>(p); },
-        [&](int i, Tensor &t) {
-            const moe_adamw_tensor &a = tensors[i];
-            t.vec = t.vec && aligned_to(a.param, 4 * dtype_bytes((moe_dtype)a.param_dtype)) &&
-                    aligned_to(a.grad, 4 * dtype_bytes((moe_dtype)a.grad_dtype)) && aligned16(a.master);
-        });
+    auto one = [&](int i, Tensor &t) {
+        const moe_adamw_tensor &a = tensors[i];
+        t.vec = t.vec && aligned_to(a.param, 4 * dtype_bytes((moe_dtype)a.param_dtype)) &&
+                aligned_to(a.grad, 4 * dtype_bytes((moe_dtype)a.grad_dtype)) && aligned16(a.master);
+    };
+    bool kinds[2] = {false, false};
+    for (int i = 0; i < n_tensors; i++)
+        if (tensors[i].n) kinds[tensors[i].scales != nullptr] = true;
+    if (kinds[0])
+        st = launch(
+            tensors, n_tensors, 0, c, "adamw_step", [&](auto &p, unsigned grid) { step_kernel<sizeof(p.t) / sizeof(Tensor), false><<<grid, THREADS, 0, s>>>(p); }, one);
+    if (kinds[1] && st == MOE_OK)
+        st = launch(
+            tensors, n_tensors, 1, c, "adamw_step", [&](auto &p, unsigned grid) { step_kernel<sizeof(p.t) / sizeof(Tensor), true><<<grid, THREADS, 0, s>>>(p); }, one);
+    return st;
 }
 
 extern "C" moe_status moe_adamw_states(const moe_adamw_tensor *tensors, int n_tensors, float *const *m_values,
@@ -549,7 +733,7 @@ extern "C" moe_status moe_adamw_states(const moe_adamw_tensor *tensors, int n_te
         MOE_REQUIRE(aligned_to(out(m_values, i), 4) && aligned_to(out(v_values, i), 4), "tensor %d: values must be 4-byte aligned", i);
     const cudaStream_t s = to_cuda(stream);
     return launch(
-        tensors, n_tensors, Common{}, s, "adamw_states",
+        tensors, n_tensors, -1, Common{}, "adamw_states",
         [&](auto &p, unsigned grid) { states_kernel<<<grid, THREADS, 0, s>>>(p); },
         [&](int i, Tensor &t) {
             t.master = out(m_values, i);

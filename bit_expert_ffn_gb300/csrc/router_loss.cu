@@ -97,7 +97,7 @@ __device__ __forceinline__ void finish(const Params &p, int parts, G get, float 
     const int C = gridDim.x, r = C > 1 ? (int)cluster_rank() : 0, tid = threadIdx.x;
     const int E = p.E, units = (E + V - 1) / V;
     const int e0 = (int)((int64_t)units * r / C) * V, w = (int)((int64_t)units * (r + 1) / C) - e0 / V;
-    const int per = min((w + 31) & ~31, kThreads), groups = max(1, min(kThreads / max(per, 32), parts));
+    const int per = min(w, kThreads), groups = max(1, min(kThreads / max(per, 1), parts));
     const int g = per ? tid / per : groups, c0 = per ? tid % per : 0;
     __shared__ float s_n, s_z, s_dot[kThreads / 32];
     __shared__ int s_tok;
@@ -488,7 +488,8 @@ extern "C" moe_status moe_router_loss(const void *logits, moe_dtype dtype, int T
     st = with_dtype(dtype, [&](auto a) {
         return with_row(E, vec_rows(logits, dtype, E), [&](auto nv, auto vec) {
             auto fn = loss_kernel<decltype(a), decltype(nv)::value, decltype(vec)::value>;
-            MOE_CUDA_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)loss_smem(32 * decltype(nv)::value)));
+            if (cfg.dynamicSmemBytes > 40 * 1024)  // (with the static part more than the 48 KB of any kernel)
+                MOE_CUDA_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)loss_smem(32 * decltype(nv)::value)));
             MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, fn, p));
             return check_launch("router_loss");
         });
@@ -527,7 +528,8 @@ extern "C" moe_status moe_router_loss_backward(const void *logits, moe_dtype dty
     return with_dtype(dtype, [&](auto a) {
         return with_row(E, vec_rows(logits, dtype, E) && vec_rows(dlogits, dtype, E), [&](auto nv, auto vec) {
             auto fn = grad_kernel<decltype(a), decltype(nv)::value, decltype(vec)::value>;
-            MOE_CUDA_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)grad_smem(32 * decltype(nv)::value)));
+            if (grad_smem(E) > 40 * 1024)
+                MOE_CUDA_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)grad_smem(32 * decltype(nv)::value)));
             fn<<<grid_of(T, E), THREADS, grad_smem(E), to_cuda(stream)>>>(p);
             return check_launch("router_loss_backward");
         });

@@ -748,7 +748,7 @@ typedef struct moe_adamw_options {
  * is, m and v too, and sets *dev_status = MOE_ERR_NONFINITE; a grad_scale of
  * NaN or infinity so leaves every tensor as it is.  Tensors must not overlap;
  * equal param, master, m or v pointers are refused.  beta1 and beta2 in [0, 1),
- * eps > 0, step >= 1 (a step_dev below 1 counts as 1).
+ * eps a normal fp32 number above 0, step >= 1 (a step_dev below 1 counts as 1).
  *
  * States in 8 bits (scales given; all zeros to begin with): a block of 256
  * values shares two fp32 scales.  m is held in e4m3 (to nearest, ties to even)

@@ -103,7 +103,7 @@ def test_adamw():
                      (dict(master=A + 2), "aligned"), (dict(m=A + 1), "aligned"), (dict(scales=A + 4), "scales"),
                      (dict(lr_factor=float("nan")), "finite"), (dict(weight_decay=float("inf")), "finite")):
         refused(BAD, word, f, raw(**kw), o())
-    for kw, word in ((dict(beta1=1.0), "beta1"), (dict(beta2=-0.1), "beta2"), (dict(eps=0.0), "eps"), (dict(eps=1e-60), "eps"),
+    for kw, word in ((dict(beta1=1.0), "beta1"), (dict(beta2=-0.1), "beta2"), (dict(eps=0.0), "eps"), (dict(eps=1e-60), "eps"), (dict(eps=1e-40), "eps"),
                      (dict(step=0), "step"), (dict(lr=float("nan")), "lr"), (dict(lr_dev=A + 2), "aligned"), (dict(step_dev=A + 4), "aligned")):
         refused(BAD, word, f, raw(), o(**kw))
     two = (m.moe_adamw_tensor * 2)(raw().array[0], raw().array[0])
