@@ -40,6 +40,14 @@ __device__ __forceinline__ float warp_max(float v)
     return __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
 }
 
+// The kernels of a call, and of the calls after it, are launched while the one before may still run: nothing before this
+// reads what that one writes.
+__device__ __forceinline__ void next_launch()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
@@ -187,6 +195,7 @@ __global__ void __launch_bounds__(THREADS, NV <= 16 ? 2 : 1) loss_kernel(const _
     __shared__ int s_tok[WARPS];
     for (int i = threadIdx.x; i < E; i += THREADS) hist[i] = 0;
     __syncthreads();
+    next_launch();
 
     using T = typename A::T;
     const T *logits = static_cast<const T *>(p.logits);
@@ -277,7 +286,7 @@ template <int V>
 __global__ void __launch_bounds__(FINISH, 1) finish_kernel(const __grid_constant__ Params p, int parts)
 {
     __shared__ float red[2 * V * FINISH], slot;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    next_launch();
     const float *part = p.part;
     const int pitch = pitch_of(p.E);
     finish<FINISH, V>(
@@ -307,20 +316,10 @@ __global__ void __launch_bounds__(THREADS, NV <= 16 ? 2 : 1) grad_kernel(const _
     const T *logits = static_cast<const T *>(p.logits);
     T *out = static_cast<T *>(p.dlogits);
     float *row = dyn + warp * ((E + 3) & ~3);
-    float g[NV], cur[NV], nxt[NV], zc = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; i++) g[i] = 0.f;
-    if (p.dloss) {
-        const float n = (float)max(p.counts[E], 1), c = p.dloss[0] * (float)E / n / (n * (float)k);
-        zc = 2.f * p.dloss[1] / n;
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-            const int e = column<kVec>(i, lane);
-            if (e < E) g[i] = c * (float)p.counts[e];
-        }
-    }
     for (int i = lane; i < E; i += 32) row[i] = 0.f;
     __syncwarp();
+    next_launch();
+    float g[NV], cur[NV], nxt[NV], zc = 0.f;
     const int step = gridDim.x * WARPS;
     int t = blockIdx.x * WARPS + warp, id = -1, idn = -1;
     float lse = 0.f, lsen = 0.f, w = 0.f, wn = 0.f, d = 0.f, dn = 0.f;
@@ -336,6 +335,17 @@ __global__ void __launch_bounds__(THREADS, NV <= 16 ? 2 : 1) grad_kernel(const _
         }
     };
     if (t < p.T) fetch(t, cur, lse, id, w, d);
+#pragma unroll
+    for (int i = 0; i < NV; i++) g[i] = 0.f;
+    if (p.dloss) {
+        const float n = (float)max(p.counts[E], 1), c = p.dloss[0] * (float)E / n / (n * (float)k);
+        zc = 2.f * p.dloss[1] / n;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int e = column<kVec>(i, lane);
+            if (e < E) g[i] = c * (float)p.counts[e];
+        }
+    }
     for (; t < p.T; t += step) {
         if (p.T - t > step) fetch(t + step, nxt, lsen, idn, wn, dn);
         const bool counts = p.dloss && lse - lse == 0.f;
@@ -471,17 +481,20 @@ extern "C" moe_status moe_router_loss(const void *logits, moe_dtype dtype, int T
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(THREADS);
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
+    cfg.numAttrs = 1;
     int grid = grid_of(T, E);
     if (!need) {  // one cluster: a row or more per warp
         int c = 1;
         while (c < MAX_CLUSTER && c * WARPS < T) c *= 2;
         grid = c;
-        at[0].val.clusterDim.x = (unsigned)c;
-        cfg.numAttrs = 1;
+        at[1].val.clusterDim.x = (unsigned)c;
+        cfg.numAttrs = 2;
     }
     cfg.gridDim = dim3((unsigned)grid);
     cfg.dynamicSmemBytes = loss_smem(E);
@@ -497,12 +510,7 @@ extern "C" moe_status moe_router_loss(const void *logits, moe_dtype dtype, int T
     if (st != MOE_OK || !need) return st;
     int c = 1;
     while (c < MAX_CLUSTER && c * 64 < E) c *= 2;
-    cudaLaunchAttribute fin[2];
-    fin[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    fin[0].val.programmaticStreamSerializationAllowed = 1;
-    fin[1] = at[0];
-    fin[1].val.clusterDim.x = (unsigned)c;
-    cfg.attrs = fin;
+    at[1].val.clusterDim.x = (unsigned)c;
     cfg.numAttrs = 2;
     cfg.gridDim = dim3((unsigned)c);
     cfg.blockDim = dim3(FINISH);
@@ -530,7 +538,17 @@ extern "C" moe_status moe_router_loss_backward(const void *logits, moe_dtype dty
             auto fn = grad_kernel<decltype(a), decltype(nv)::value, decltype(vec)::value>;
             if (grad_smem(E) > 40 * 1024)
                 MOE_CUDA_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)grad_smem(32 * decltype(nv)::value)));
-            fn<<<grid_of(T, E), THREADS, grad_smem(E), to_cuda(stream)>>>(p);
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)grid_of(T, E));
+            cfg.blockDim = dim3(THREADS);
+            cfg.dynamicSmemBytes = grad_smem(E);
+            cfg.stream = to_cuda(stream);
+            cudaLaunchAttribute at[1];
+            at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            at[0].val.programmaticStreamSerializationAllowed = 1;
+            cfg.attrs = at;
+            cfg.numAttrs = 1;
+            MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, fn, p));
             return check_launch("router_loss_backward");
         });
     });
