@@ -48,6 +48,7 @@ constexpr size_t SMEM = STAGES * (A_BYTES + B_BYTES) + EPI_WARPS * 2 * OUT_BYTES
 constexpr int BAND = 32;  // row tiles that pass over the columns together
 constexpr unsigned long long kWaitNs = 2000000000ull;
 constexpr float LOG2E = 1.4426950408889634f;
+constexpr float FUSED = 1e6f;  // below it x log2 e is rounded by at most 1/16
 constexpr size_t PIECE_BYTES = 256u << 20;
 constexpr float F16_ROOM = 16384.f;  // |d| <= 1 after the division: as fp16, 2^14 times that
 
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
             j++;
             const int row = m.m * BM + q * 32 + lane, n0 = m.n * g.bn;
             int label = -1;
-            float nl = 0.f, a = 0.f, b = 0.f;
+            float lse = 0.f, nl = 0.f, a = 0.f, b = 0.f;
             if (K != PROD && row < p.T) label = p.labels[row];
             if (K == GRAD && row < p.T) {
                 const bool there = label >= 0 && label < p.all;
@@ -328,9 +329,9 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                 a = b + (p.dlse ? p.dlse[row] : 0.f);
                 a = down > 0.f ? a / top * down : 0.f;
                 b = down > 0.f ? b / top * down : 0.f;
-                const float lse = p.lse[row];
+                lse = p.lse[row];
                 nl = -lse * LOG2E;
-                a *= ex2(-fmaf(lse, LOG2E, nl));  // (what the product's rounding left out)
+                if (fabsf(lse) < FUSED) a *= ex2(-fmaf(lse, LOG2E, nl));  // (what the product's rounding left out)
                 label -= p.v0;
             }
             if (!warp_wait(S, &S.acc_full[acc], v & 1)) {
@@ -341,9 +342,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
             tc::tc_fence_after();
             const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
             if (K == LOSS) {
-                // sums of 2^(z log2 e - base), base the running maximum's product, rounded: what its rounding left out
-                // is put right once at the end (with logits of 10^5 it is a percent)
-                float mx = -INFINITY, base = 0.f, sum = 0.f, zl = 0.f;
+                float mx = -INFINITY, sum = 0.f, zl = 0.f;
                 bool mine = false;
 #pragma unroll 1
                 for (int c = 0; c < g.bn; c += 32) {
@@ -368,16 +367,22 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                     float cm = mx;
 #pragma unroll
                     for (int i = 0; i < 32; i++) cm = fmaxf(cm, __uint_as_float(r[i]));
-                    const float off = cm == -INFINITY ? 0.f : cm * LOG2E;
-                    float t[4] = {0.f, 0.f, 0.f, 0.f};
+                    const float ref = cm == -INFINITY ? 0.f : cm;
+                    float t[4] = {0.f, 0.f, 0.f, 0.f}, right = 1.f;
+                    if (fabsf(ref) < FUSED) {  // exponents as products and sums in one; the maximum's rounding put right after
+                        const float off = ref * LOG2E;
+                        right = ex2(-fmaf(ref, LOG2E, -off));
 #pragma unroll
-                    for (int i = 0; i < 32; i++) t[i & 3] += ex2(fmaf(__uint_as_float(r[i]), LOG2E, -off));
-                    sum = sum * ex2(base - off) + ((t[0] + t[1]) + (t[2] + t[3]));
+                        for (int i = 0; i < 32; i++) t[i & 3] += ex2(fmaf(__uint_as_float(r[i]), LOG2E, -off));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; i++) t[i & 3] += ex2((__uint_as_float(r[i]) - ref) * LOG2E);
+                    }
+                    sum = fmaf((t[0] + t[1]) + (t[2] + t[3]), right, sum * ex2((mx - ref) * LOG2E));
                     mx = cm;
-                    base = off;
                 }
                 if (row < p.T) {
-                    p.stats[(int64_t)row * g.n_tiles + m.n] = make_float2(mx, mx == -INFINITY ? 0.f : sum * ex2(-fmaf(mx, LOG2E, -base)));
+                    p.stats[(int64_t)row * g.n_tiles + m.n] = make_float2(mx, sum);
                     if (mine) p.label_z[row] = zl;
                 }
             } else {
@@ -390,12 +395,22 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                     const bool f32 = K == PROD && g.out_f32;
                     if (K == GRAD) {
                         const int left = p.V - n0 - c, at = label - n0 - c;
+                        if (!(fabsf(lse) < FUSED)) {
 #pragma unroll
-                        for (int i = 0; i < 32; i++) {
-                            float e = ex2(fmaf(__uint_as_float(r[i]), LOG2E, nl)) * a;
-                            if (i == at) e -= b;
-                            if (i >= left || (a == 0.f && b == 0.f)) e = 0.f;
-                            r[i] = __float_as_uint(e);
+                            for (int i = 0; i < 32; i++) r[i] = __float_as_uint(ex2((__uint_as_float(r[i]) - lse) * LOG2E) * a);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; i++) r[i] = __float_as_uint(ex2(fmaf(__uint_as_float(r[i]), LOG2E, nl)) * a);
+                        }
+                        if ((unsigned)at < 32u) {
+#pragma unroll
+                            for (int i = 0; i < 32; i++)
+                                if (i == at) r[i] = __float_as_uint(__uint_as_float(r[i]) - b);
+                        }
+                        if (left < 32 || (a == 0.f && b == 0.f)) {  // past the vocabulary; a token that takes no part, whatever its logits
+#pragma unroll
+                            for (int i = 0; i < 32; i++)
+                                if (i >= left || (a == 0.f && b == 0.f)) r[i] = 0;
                         }
                     } else {
 #pragma unroll

@@ -21,10 +21,11 @@ namespace moe {
 namespace rl {
 
 constexpr int MAX_E = 1024, MAX_K = 16;
-constexpr int WARPS = 16, THREADS = WARPS * 32;
+constexpr int WARPS = 12, THREADS = WARPS * 32;
 constexpr int MAX_CLUSTER = 8;
 constexpr int CLUSTER_ROWS = 1024;  // up to this many tokens are one cluster's
-constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float FUSED = 1e6f;  // below it x log2 e is rounded by at most 1/16
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -55,28 +56,31 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// A row's columns of a lane: 4 (lane + 32 j) + 0..3 (kVec), or lane + 32 i.
-template <bool kVec>
+// How a lane takes a row: single columns, fours of them (aligned rows), fours of a row that fills the lanes' registers.
+enum Mode { ONES, FOURS, FULL };
+
+// A row's columns of a lane: 4 (lane + 32 j) + 0..3, or lane + 32 i.
+template <Mode M>
 __device__ __forceinline__ int column(int i, int lane)
 {
-    return kVec ? 4 * (lane + 32 * (i >> 2)) + (i & 3) : lane + 32 * i;
+    return M != ONES ? 4 * (lane + 32 * (i >> 2)) + (i & 3) : lane + 32 * i;
 }
 
 // The lane's columns of a row; those past E as `fill`.
-template <class A, int NV, bool kVec>
+template <class A, int NV, Mode M>
 __device__ __forceinline__ void load_row(const typename A::T *row, int E, int lane, float fill, float (&v)[NV])
 {
-    if (kVec) {
+    if (M != ONES) {
 #pragma unroll
         for (int i = 0; i < NV; i += 4) {
-            const int c = column<kVec>(i, lane);
-            v[i] = v[i + 1] = v[i + 2] = v[i + 3] = fill;
-            if (c < E) A::load4(row + c, v + i);
+            const int c = column<M>(i, lane);
+            if (M != FULL) v[i] = v[i + 1] = v[i + 2] = v[i + 3] = fill;
+            if (M == FULL || c < E) A::load4(row + c, v + i);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const int c = column<kVec>(i, lane);
+            const int c = column<M>(i, lane);
             v[i] = c < E ? A::load(row + c) : fill;
         }
     }
@@ -184,7 +188,7 @@ __device__ __forceinline__ void finish(const Params &p, int parts, G get, float 
     if (C > 1) cluster_sync();  // no CTA leaves while another reads its slot
 }
 
-template <class A, int NV, bool kVec>
+template <class A, int NV, Mode M>
 __global__ void __launch_bounds__(THREADS, NV <= 16 ? 2 : 1) loss_kernel(const __grid_constant__ Params p)
 {
     extern __shared__ float dyn[];  // [WARPS][E] sums of p, [E] sums of the CTA, [E] counts, 2; 2 THREADS words for finish
@@ -198,60 +202,72 @@ __global__ void __launch_bounds__(THREADS, NV <= 16 ? 2 : 1) loss_kernel(const _
     next_launch();
 
     using T = typename A::T;
-    const T *logits = static_cast<const T *>(p.logits);
     const int step = gridDim.x * WARPS;
-    float acc[NV], cur[NV], nxt[NV], z = 0.f;
-    int tokens = 0;
+    int t = blockIdx.x * WARPS + warp, tokens = 0;
+    const T *src = static_cast<const T *>(p.logits) + (int64_t)t * E;
+    const int64_t src_step = (int64_t)step * E;
+    const int32_t *ids = p.ids + (int64_t)t * k + lane;
+    float acc[NV], one[NV], two[NV], z = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; i++) acc[i] = 0.f;
-    int t = blockIdx.x * WARPS + warp, id = -1, idn = -1;
-    bool in = true, inn = true;
+    int id1 = 0, id2 = 0;
+    bool in1 = true, in2 = true;
     auto fetch = [&](int t, float (&v)[NV], int &id, bool &in) {
-        load_row<A, NV, kVec>(logits + (int64_t)t * E, E, lane, -INFINITY, v);
-        id = lane < k ? p.ids[(int64_t)t * k + lane] : MOE_ID_NOT_LOCAL;
-        in = !p.keep || p.keep[t] != 0;
+        load_row<A, NV, M>(src, E, lane, -INFINITY, v);
+        if (lane < k) id = *ids;
+        if (p.keep) in = p.keep[t] != 0;
+        src += src_step;
+        ids += step * k;
     };
-    if (t < p.T) fetch(t, cur, id, in);
-    for (; t < p.T; t += step) {
-        if (p.T - t > step) fetch(t + step, nxt, idn, inn);
-        if ((unsigned)id >= (unsigned)E) {
-            if (id != MOE_ID_NOT_LOCAL) set_status(p.status, MOE_ERR_BOUNDS);
-            id = -1;
-        }
-        float top = cur[0];
+    auto row = [&](int t, float (&v)[NV], int id, bool in) {
+        float top = v[0];
 #pragma unroll
-        for (int i = 1; i < NV; i++) top = fmaxf(top, cur[i]);
+        for (int i = 1; i < NV; i++) top = fmaxf(top, v[i]);
         top = warp_max(top);
-        const float off = top == -INFINITY ? 0.f : top;
-        float s = 0.f;
+        // exponents as products and sums in one; where the product's rounding is no small matter, the difference comes first
+        float off = top * LOG2E, s = 0.f;
+        if (fabsf(top) < FUSED) {
 #pragma unroll
-        for (int i = 0; i < NV; i++) {
-            cur[i] = ex2((cur[i] - off) * LOG2E);
-            s += cur[i];
+            for (int i = 0; i < NV; i++) v[i] = ex2(fmaf(v[i], LOG2E, -off));
+        } else {
+            off = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; i++) v[i] = ex2((v[i] - (top == -INFINITY ? 0.f : top)) * LOG2E);
         }
+#pragma unroll
+        for (int i = 0; i < NV; i++) s += v[i];
         s = warp_sum(s);
         // (s is NaN when a logit is NaN or +inf, 0 when all are -inf)
         if (in && s != s && lane == 0) set_status(p.status, MOE_ERR_NONFINITE);
         const bool counts = in && s > 0.f;
-        const float lse = counts ? top + logf(s) : -INFINITY;
+        // (what the product's rounding left out of the exponents; nothing in the other form)
+        const float lse = counts ? top + (logf(s) - (off != 0.f ? fmaf(top, LOG2E, -off) * LN2 : 0.f)) : -INFINITY;
         if (lane == 0) p.lse[t] = lse;
+        if (lane < k && (unsigned)id >= (unsigned)E && id != MOE_ID_NOT_LOCAL) set_status(p.status, MOE_ERR_BOUNDS);
         if (counts) {
-            const float inv = 1.f / s;
+            const float inv = __fdividef(1.f, s);
 #pragma unroll
-            for (int i = 0; i < NV; i++) acc[i] = fmaf(cur[i], inv, acc[i]);
+            for (int i = 0; i < NV; i++) acc[i] = fmaf(v[i], inv, acc[i]);
             z = fmaf(lse, lse, z);
             tokens++;
-            if (id >= 0) atomicAdd(&hist[id], 1);
+            if (lane < k && (unsigned)id < (unsigned)E) atomicAdd(&hist[id], 1);
         }
-#pragma unroll
-        for (int i = 0; i < NV; i++) cur[i] = nxt[i];
-        id = idn;
-        in = inn;
+    };
+    if (t < p.T) fetch(t, one, id1, in1);
+    while (t < p.T) {  // two rows in turn, the other one on its way
+        if (p.T - t > step) fetch(t + step, two, id2, in2);
+        row(t, one, id1, in1);
+        if (p.T - t <= step) break;
+        t += step;
+        if (p.T - t > step) fetch(t + step, one, id1, in1);
+        row(t, two, id2, in2);
+        if (p.T - t <= step) break;
+        t += step;
     }
 #pragma unroll
     for (int i = 0; i < NV; i++) {
-        const int c = column<kVec>(i, lane);
-        if (c < E) rows[warp * E + c] = acc[i];
+        const int c = column<M>(i, lane);
+        if (M == FULL || c < E) rows[warp * E + c] = acc[i];
     }
     if (lane == 0) s_z[warp] = z, s_tok[warp] = tokens;
     __syncthreads();
@@ -307,109 +323,119 @@ struct GradParams {
     const float *lse, *dloss, *w, *dw;
 };
 
-template <class A, int NV, bool kVec>
+template <class A, int NV, Mode M>
 __global__ void __launch_bounds__(THREADS, NV <= 16 ? 2 : 1) grad_kernel(const __grid_constant__ GradParams p)
 {
-    extern __shared__ float dyn[];  // [WARPS][E rounded up to 4]: the weights' part of a warp's row
+    extern __shared__ float dyn[];  // [WARPS][E rounded up to 4]: the weights' part of a warp's row; then g
     const int lane = lane_id(), warp = warp_id(), E = p.E, k = p.k;
     using T = typename A::T;
-    const T *logits = static_cast<const T *>(p.logits);
-    T *out = static_cast<T *>(p.dlogits);
-    float *row = dyn + warp * ((E + 3) & ~3);
-    for (int i = lane; i < E; i += 32) row[i] = 0.f;
+    float *extra = dyn + warp * ((E + 3) & ~3), *g = dyn + WARPS * ((E + 3) & ~3);
+    for (int i = lane; i < E; i += 32) extra[i] = 0.f;
     __syncwarp();
     next_launch();
-    float g[NV], cur[NV], nxt[NV], zc = 0.f;
     const int step = gridDim.x * WARPS;
-    int t = blockIdx.x * WARPS + warp, id = -1, idn = -1;
-    float lse = 0.f, lsen = 0.f, w = 0.f, wn = 0.f, d = 0.f, dn = 0.f;
+    int t = blockIdx.x * WARPS + warp;
+    const T *src = static_cast<const T *>(p.logits) + (int64_t)t * E;
+    T *out = static_cast<T *>(p.dlogits) + (int64_t)t * E;
+    const int64_t row_step = (int64_t)step * E;
+    int64_t pair = (int64_t)t * k + lane;
+    float one[NV], two[NV], zc = 0.f, lse1 = 0.f, lse2 = 0.f, w1 = 0.f, w2 = 0.f, d1 = 0.f, d2 = 0.f;
+    int id1 = -1, id2 = -1;
+    const bool slot = p.w && lane < k, base = p.dloss != nullptr;
     auto fetch = [&](int t, float (&v)[NV], float &lse, int &id, float &w, float &d) {
-        if (p.dloss) {
-            load_row<A, NV, kVec>(logits + (int64_t)t * E, E, lane, -INFINITY, v);
+        if (base) {
+            load_row<A, NV, M>(src, E, lane, -INFINITY, v);
             lse = p.lse[t];
         }
-        if (p.w && lane < k) {
-            id = p.ids[(int64_t)t * k + lane];
-            w = p.w[(int64_t)t * k + lane];
-            d = p.dw[(int64_t)t * k + lane];
+        if (slot) id = p.ids[pair], w = p.w[pair], d = p.dw[pair];
+        src += row_step;
+        pair += step * k;
+    };
+    auto each_g = [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < NV; i += M == ONES ? 1 : 4) {
+            const int c = column<M>(i, lane);
+            if (M != FULL && c >= E) continue;
+            if (M != ONES) {
+                const float4 a = *reinterpret_cast<const float4 *>(g + c);
+                f(i, a.x), f(i + 1, a.y), f(i + 2, a.z), f(i + 3, a.w);
+            } else {
+                f(i, g[c]);
+            }
         }
     };
-    if (t < p.T) fetch(t, cur, lse, id, w, d);
+    auto row = [&](float (&v)[NV], float lse, int id, float w, float d) {
+        if (base && lse - lse == 0.f) {
+            // p = 2^(l log2 e - lse log2 e), the last product's rounding put right by a factor of the whole row (where it
+            // is no small matter, the difference comes first)
+            float nl = -lse * LOG2E, right = 1.f, dot = 0.f;
+            if (fabsf(lse) < FUSED) {
+                right = ex2(-fmaf(lse, LOG2E, nl));
 #pragma unroll
-    for (int i = 0; i < NV; i++) g[i] = 0.f;
-    if (p.dloss) {
-        const float n = (float)max(p.counts[E], 1), c = p.dloss[0] * (float)E / n / (n * (float)k);
-        zc = 2.f * p.dloss[1] / n;
+                for (int i = 0; i < NV; i++) v[i] = ex2(fmaf(v[i], LOG2E, nl));
+            } else {
 #pragma unroll
-        for (int i = 0; i < NV; i++) {
-            const int e = column<kVec>(i, lane);
-            if (e < E) g[i] = c * (float)p.counts[e];
-        }
-    }
-    for (; t < p.T; t += step) {
-        if (p.T - t > step) fetch(t + step, nxt, lsen, idn, wn, dn);
-        const bool counts = p.dloss && lse - lse == 0.f;
-        float dot = 0.f;
-        if (counts) {
-#pragma unroll
-            for (int i = 0; i < NV; i++) {
-                cur[i] = ex2((cur[i] - lse) * LOG2E);
-                dot = fmaf(cur[i], g[i], dot);
+                for (int i = 0; i < NV; i++) v[i] = ex2((v[i] - lse) * LOG2E);
             }
+            each_g([&](int i, float gi) { dot = fmaf(v[i], gi, dot); });
+            const float add = right * (zc * lse - right * warp_sum(dot));
+            each_g([&](int i, float gi) { v[i] *= fmaf(gi, right, add); });
         } else {
 #pragma unroll
-            for (int i = 0; i < NV; i++) cur[i] = 0.f;
+            for (int i = 0; i < NV; i++) v[i] = 0.f;
         }
-        dot = warp_sum(dot);
-        const float add = zc * lse - dot;
-        if (counts) {
-#pragma unroll
-            for (int i = 0; i < NV; i++) cur[i] *= g[i] + add;
-        }
-        const bool mine = p.w && lane < k && (unsigned)id < (unsigned)E;
+        const bool mine = slot && (unsigned)id < (unsigned)E;
         if (p.w) {
-            const float mean = warp_sum(lane < k ? w * d : 0.f);
-            float v = w * (d - mean);
+            float u = w * (d - warp_sum(w * d));  // (w = d = 0 in the lanes without a slot)
             // (an expert named twice gets the sum, in the slots' order, at its first slot)
             const uint32_t same = __match_any_sync(0xffffffffu, mine ? id : E + lane);
             const bool first = mine && (same & ((1u << lane) - 1)) == 0;
             if (__any_sync(0xffffffffu, mine && !first)) {
                 float total = 0.f;
                 for (int j = 0; j < k; j++) {
-                    const float o = __shfl_sync(0xffffffffu, v, j);
+                    const float o = __shfl_sync(0xffffffffu, u, j);
                     if (same >> j & 1) total += o;
                 }
-                v = total;
+                u = total;
             }
-            if (first) row[id] = v;
+            if (first) extra[id] = u;
             __syncwarp();
         }
-        T *o = out + (int64_t)t * E;
-        if (kVec) {
 #pragma unroll
-            for (int i = 0; i < NV; i += 4) {
-                const int c = column<kVec>(i, lane);
-                if (c < E) {
-                    if (p.w) {
-                        const float4 a = *reinterpret_cast<const float4 *>(row + c);
-                        cur[i] += a.x, cur[i + 1] += a.y, cur[i + 2] += a.z, cur[i + 3] += a.w;
-                    }
-                    A::store4(o + c, cur + i);
+        for (int i = 0; i < NV; i += M == ONES ? 1 : 4) {
+            const int c = column<M>(i, lane);
+            if (M != FULL && c >= E) continue;
+            if (M != ONES) {
+                if (p.w) {
+                    const float4 a = *reinterpret_cast<const float4 *>(extra + c);
+                    v[i] += a.x, v[i + 1] += a.y, v[i + 2] += a.z, v[i + 3] += a.w;
                 }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < NV; i++) {
-                const int c = column<kVec>(i, lane);
-                if (c < E) A::store(o + c, p.w ? cur[i] + row[c] : cur[i]);
+                A::store4(out + c, v + i);
+            } else {
+                A::store(out + c, p.w ? v[i] + extra[c] : v[i]);
             }
         }
+        out += row_step;
         __syncwarp();
-        if (mine) row[id] = 0.f;
+        if (mine) extra[id] = 0.f;
         __syncwarp();
-#pragma unroll
-        for (int i = 0; i < NV; i++) cur[i] = nxt[i];
-        lse = lsen, id = idn, w = wn, d = dn;
+    };
+    if (t < p.T) fetch(t, one, lse1, id1, w1, d1);
+    if (base) {
+        const float n = (float)max(p.counts[E], 1), c = p.dloss[0] * (float)E / n / (n * (float)k);
+        zc = 2.f * p.dloss[1] / n;
+        for (int i = threadIdx.x; i < E; i += THREADS) g[i] = c * (float)p.counts[i];
+    }
+    __syncthreads();
+    while (t < p.T) {  // two rows in turn, the other one on its way
+        if (p.T - t > step) fetch(t + step, two, lse2, id2, w2, d2);
+        row(one, lse1, id1, w1, d1);
+        if (p.T - t <= step) break;
+        t += step;
+        if (p.T - t > step) fetch(t + step, one, lse1, id1, w1, d1);
+        row(two, lse2, id2, w2, d2);
+        if (p.T - t <= step) break;
+        t += step;
     }
 }
 
@@ -417,20 +443,21 @@ __global__ void __launch_bounds__(THREADS, NV <= 16 ? 2 : 1) grad_kernel(const _
 static int grid_of(int T, int E) { return std::min((T + WARPS - 1) / WARPS, sm_count() * (E <= 512 ? 2 : 1)); }
 
 static size_t loss_smem(int E) { return ((size_t)WARPS * E + 2 * E + 2 + 2 * THREADS) * 4; }
-static size_t grad_smem(int E) { return (size_t)WARPS * ((E + 3) & ~3) * 4; }
+static size_t grad_smem(int E) { return (size_t)(WARPS + 1) * ((E + 3) & ~3) * 4; }
 
-// Calls f<NV, kVec>() for a row length and whether rows are aligned for four columns at once.
+// Calls f with the registers of a row and how they are filled (`fours`: rows are aligned for four columns at once).
 template <class F>
-moe_status with_row(int E, bool vec, F f)
+moe_status with_row(int E, bool fours, F f)
 {
-#define MOE_RL(nv) \
-    if (E <= 32 * nv) return vec ? f(std::integral_constant<int, nv>{}, std::true_type{}) : f(std::integral_constant<int, nv>{}, std::false_type{})
-    MOE_RL(4);
-    MOE_RL(8);
-    MOE_RL(16);
-    MOE_RL(32);
-#undef MOE_RL
-    return fail(MOE_ERR_INVALID_ARG, "E=%d", E);
+    auto mode = [&](auto nv) {
+        if (fours && E == 32 * decltype(nv)::value) return f(nv, std::integral_constant<Mode, FULL>{});
+        if (fours) return f(nv, std::integral_constant<Mode, FOURS>{});
+        return f(nv, std::integral_constant<Mode, ONES>{});
+    };
+    if (E <= 128) return mode(std::integral_constant<int, 4>{});
+    if (E <= 256) return mode(std::integral_constant<int, 8>{});
+    if (E <= 512) return mode(std::integral_constant<int, 16>{});
+    return mode(std::integral_constant<int, 32>{});
 }
 
 static moe_status check(moe_dtype dtype, int T, int E, int k)
@@ -499,8 +526,8 @@ extern "C" moe_status moe_router_loss(const void *logits, moe_dtype dtype, int T
     cfg.gridDim = dim3((unsigned)grid);
     cfg.dynamicSmemBytes = loss_smem(E);
     st = with_dtype(dtype, [&](auto a) {
-        return with_row(E, vec_rows(logits, dtype, E), [&](auto nv, auto vec) {
-            auto fn = loss_kernel<decltype(a), decltype(nv)::value, decltype(vec)::value>;
+        return with_row(E, vec_rows(logits, dtype, E), [&](auto nv, auto mode) {
+            auto fn = loss_kernel<decltype(a), decltype(nv)::value, decltype(mode)::value>;
             if (cfg.dynamicSmemBytes > 40 * 1024)  // (with the static part more than the 48 KB of any kernel)
                 MOE_CUDA_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)loss_smem(32 * decltype(nv)::value)));
             MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, fn, p));
@@ -534,8 +561,8 @@ extern "C" moe_status moe_router_loss_backward(const void *logits, moe_dtype dty
                 "tensors must be aligned to their types");
     GradParams p = {logits, dlogits, T, E, k, ids, counts, lse, dloss, w, dw};
     return with_dtype(dtype, [&](auto a) {
-        return with_row(E, vec_rows(logits, dtype, E) && vec_rows(dlogits, dtype, E), [&](auto nv, auto vec) {
-            auto fn = grad_kernel<decltype(a), decltype(nv)::value, decltype(vec)::value>;
+        return with_row(E, vec_rows(logits, dtype, E) && vec_rows(dlogits, dtype, E), [&](auto nv, auto mode) {
+            auto fn = grad_kernel<decltype(a), decltype(nv)::value, decltype(mode)::value>;
             if (grad_smem(E) > 40 * 1024)
                 MOE_CUDA_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)grad_smem(32 * decltype(nv)::value)));
             cudaLaunchConfig_t cfg = {};

@@ -132,6 +132,26 @@ def test_extreme_logits(moe):
     assert (loss[:50] >= 0).all()
 
 
+def test_huge_logits(moe):
+    """Logits of 10^30 beside ordinary rows: the largest takes all."""
+    T, H, V = 40, 64, 300
+    h, w, labels, dloss = inputs(T, H, V, m.MOE_BF16, 9)
+    labels.clamp_(min=0)
+    h[5] *= 1e30
+    h[6] *= 1e6
+    loss, lse, _ = forward(h, w, labels, m.MOE_BF16)
+    want = cross_entropy(h, w, labels, dloss)
+    check(loss, want["loss"], want["loss_tol"])
+    check(lse, want["lse"], want["lse_tol"])
+    best = (h[5].double() @ w.double().T).argmax()
+    labels[5] = int(best)
+    loss, lse, _ = forward(h, w, labels, m.MOE_BF16)
+    assert loss[5] == 0
+    dloss[6] = 0
+    dh, dw = backward(h, w, labels, m.MOE_BF16, lse, dloss)
+    assert (dh[5] == 0).all() and torch.isfinite(dw).all()
+
+
 def test_several_pieces_of_the_vocabulary(moe):
     T, H, V = 2048, 64, 70001
     h, w, labels, dloss = inputs(T, H, V, m.MOE_BF16, 5)
