@@ -219,11 +219,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
             const Job &g = p.job[m.j];
             const int boxes = (g.bn + 63) / 64;
             const uint32_t bytes = A_BYTES + (K == PROD ? boxes * (BK * 128) : g.bn * 128);
-            // column tiles begin at steps of their own: rows of w lie at one stride, and tiles that all read the same
-            // columns of theirs at once meet in the same memory channels (four tokens, 100,003 x 2,048: 86 -> 80 us)
-            const int turn = K == PROD ? 0 : m.n * 5 % (m.kb1 - m.kb0);
-            for (int k = m.kb0; k < m.kb1; k++, it++) {
-                const int kb = k + turn < m.kb1 ? k + turn : k + turn - (m.kb1 - m.kb0);
+            for (int kb = m.kb0; kb < m.kb1; kb++, it++) {
                 if (it >= STAGES) ok = warp_wait(S, &S.empty[s], phase);
                 if (!ok) break;
                 if (elect_one()) {

@@ -139,20 +139,46 @@ __device__ __forceinline__ void finish(const Params &p, int parts, G get, float 
         if (c == c0 && tid >= kThreads - 32) {  // tokens and the squares, by the last warp of every CTA
             int n = 0;
             float z = 0.f;
-            for (int i = tid & 31; i < parts; i += 32) {
-                float x[1], y[1];
-                get(i, 2 * E, x);
-                get(i, 2 * E + 1, y);
-                z += x[0];
-                n += __float_as_int(y[0]);
+            for (int i = tid & 31; i < parts; i += 256) {  // eight a lane at once
+                float x[8][1], y[8][1];
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    x[j][0] = y[j][0] = 0.f;
+                    if (i + 32 * j < parts) get(i + 32 * j, 2 * E, x[j]), get(i + 32 * j, 2 * E + 1, y[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; j++) z += x[j][0], n += __float_as_int(y[j][0]);
             }
             z = warp_sum(z);
             n = __reduce_add_sync(0xffffffffu, n);
             if ((tid & 31) == 0) s_tok = n, s_n = n > 0 ? (float)n : 1.f, s_z = z;
         }
         __syncthreads();
+        const int values = 2 * V * per, turns = kThreads / values;
+        const bool twice = groups >= 16 && turns >= 2;  // many groups: their sums by all threads, then the threads'
+        if (twice) {
+            float f = 0.f;
+            int k = 0;
+            const int o = tid % values, j = o / per, first = tid / values;
+            if (first < turns) {
+                const float *src = red + j * kThreads + o % per;
+#pragma unroll 4
+                for (int i = first; i < groups; i += turns) {
+                    if (j < V) f += src[i * per];
+                    else k += __float_as_int(src[i * per]);
+                }
+            }
+            __syncthreads();
+            if (first < turns) red[j * kThreads + first * per + o % per] = j < V ? f : __int_as_float(k);
+            __syncthreads();
+        }
         if (g == 0 && c < w) {
-            for (int i = 1; i < groups; i++) {
+            if (twice) {
+#pragma unroll
+                for (int j = 0; j < V; j++) a[j] = red[j * kThreads + tid], b[j] = __float_as_int(red[(V + j) * kThreads + tid]);
+            }
+            const int sums = twice ? turns : groups;
+            for (int i = 1; i < sums; i++) {
 #pragma unroll
                 for (int j = 0; j < V; j++) {
                     a[j] += red[j * kThreads + tid + i * per];

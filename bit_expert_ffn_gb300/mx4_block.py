@@ -11,8 +11,10 @@ runs one block as the sequence of library calls
 from the residual stream x (fp32) and its normalised input u (bf16) to the next
 block's: y = x + alpha gate w_post rmsnorm(experts(u)), u' = w_pre rmsnorm(y).
 :meth:`Mx4Block.backward` gives the gradients of what is trained around frozen
-quantised experts: the norms' weights, the gate and the routing weights, and
-the residual stream's own.  Nothing here computes any part of the block itself.
+quantised experts: the norms' weights, the gate, the routing weights and the
+router's logits (with the router's own losses, :meth:`Mx4Block.router_loss`),
+and the residual stream's own.  Nothing here computes any part of the block
+itself.
 """
 from __future__ import annotations
 
@@ -23,7 +25,8 @@ import torch
 from . import (MOE_BF16, MOE_ERR_INVALID_ARG, MOE_F32, MOE_GATE_CHANNEL, MOE_MX4_PLAIN, MOE_MX4_SWIGLU, RMS_EPS, MoeError,
                load, moe_block_norm, moe_block_norm_backward, moe_block_norm_backward_workspace_size, moe_check_status,
                moe_combine, moe_combine_backward, moe_dispatch, moe_dispatch_backward, moe_mx4_matmul, moe_mx4_quantise,
-               moe_mx4_size, moe_permute, moe_permute_workspace_size, moe_router_topk, moe_router_workspace_size)
+               moe_mx4_size, moe_permute, moe_permute_workspace_size, moe_router_loss, moe_router_loss_backward, moe_router_loss_workspace_size,
+               moe_router_topk, moe_router_workspace_size)
 from .model import LayerShape, Workspace
 
 
@@ -52,6 +55,10 @@ class Mx4BlockBuffers:
         self.logits = torch.empty(n, s.E, dtype=f32, device=d)
         self.ids = torch.empty(n, s.k, dtype=i32, device=d)
         self.w = torch.empty(n, s.k, dtype=f32, device=d)
+        self.loss = torch.empty(2, dtype=f32, device=d)  # the router's losses: balance, squared log-sum
+        self.counts = torch.empty(s.E + 1, dtype=i32, device=d)
+        self.mean_prob = torch.empty(s.E, dtype=f32, device=d)
+        self.lse = torch.empty(n, dtype=f32, device=d)
         self.offsets = torch.empty(s.E + 1, dtype=i32, device=d)
         self.perm = torch.empty(max(P, 1), dtype=i32, device=d)
         self.inv = torch.empty(max(P, 1), dtype=i32, device=d)
@@ -118,16 +125,29 @@ class Mx4Block:
         moe_block_norm(x, MOE_F32, B.b, MOE_BF16, T, s.H, self.w_post, self.w_pre, self.gate, MOE_GATE_CHANNEL, self.alpha,
                        RMS_EPS, y, u_next)
 
-    def backward(self, x, T, bufs: Mx4BlockBuffers, dy, du_next, drows=None):
-        """Gradients of a forward pass on x (as it was) that filled bufs, for dy [T][H] fp32 and du_next [T][H] bf16: a dict of
-        x, w_post, w_pre, gate, w (routing weights) and rows (the experts' outputs); with drows, the gradient of the
-        dispatched rows as the caller's own experts give it, also u."""
+    def router_loss(self, T, bufs: Mx4BlockBuffers, keep=None):
+        """The router's losses of a forward pass that filled bufs, over its T tokens or those that keep [T] (bytes or truth
+        values) marks: bufs.loss [2], counts [E + 1], mean_prob [E]; returns bufs.loss."""
+        s, B = self.s, bufs
+        self._check(T, B)
+        nb = moe_router_loss_workspace_size(T, s.E)
+        moe_router_loss(B.logits, MOE_F32, T, s.E, B.ids, s.k, keep, B.loss, B.counts, B.mean_prob, B.lse, self.ws.get(nb), nb,
+                        self.status)
+        return B.loss
+
+    def backward(self, x, T, bufs: Mx4BlockBuffers, dy, du_next, drows=None, dloss=None, into=None):
+        """Gradients of a forward pass on x (as it was) that filled bufs, for dy [T][H] fp32 and du_next [T][H] bf16 (either may
+        be None): a dict of x, w_post, w_pre, gate, w (routing weights) and rows (the experts' outputs); with drows, the
+        gradient of the dispatched rows as the caller's own experts give it, also u; with dloss [2], the gradient of what
+        router_loss gave, also logits, from the losses and the routing weights.  into: tensors to write w_post, w_pre and
+        gate to."""
         s, B, d = self.s, bufs, self.dev
         self._check(T, B)
         f32 = torch.float32
         g = {"x": torch.empty_like(x), "w_post": torch.empty(s.H, dtype=f32, device=d),
              "w_pre": torch.empty(s.H, dtype=f32, device=d), "gate": torch.empty(s.H, dtype=f32, device=d),
              "rows": torch.empty_like(B.rows[:T * s.k]), "w": torch.empty_like(B.w[:T])}
+        g.update(into or {})
         db = torch.empty_like(B.b[:T])
         nb = moe_block_norm_backward_workspace_size(T, s.H, MOE_GATE_CHANNEL)
         moe_block_norm_backward(x, MOE_F32, B.b, MOE_BF16, T, s.H, self.w_post, self.w_pre, self.gate, MOE_GATE_CHANNEL,
@@ -137,6 +157,9 @@ class Mx4Block:
         if drows is not None:
             g["u"] = torch.empty(T, s.H, dtype=torch.bfloat16, device=d)
             moe_dispatch_backward(drows, MOE_BF16, T, s.H, s.k, B.inv, g["u"])
+        if dloss is not None:
+            g["logits"] = torch.empty_like(B.logits[:T])
+            moe_router_loss_backward(B.logits, MOE_F32, T, s.E, B.ids, s.k, B.counts, B.lse, dloss, B.w, g["w"], g["logits"])
         return g
 
 
