@@ -6,9 +6,9 @@
 //   d = exp(z - lse) (dloss + dlse) - onehot dloss
 //   dh = d W, dW = d^T h
 //
-// Three kinds of product share one kernel (128 x 256 tiles, K in steps of 64):
+// Three kinds of product share one kernel:
 //   LOSS   z's tiles; each row's maximum and sum of exponentials over the
-//          tile's 256 columns leave (8 bytes instead of 1 KB), and its label's z
+//          tile's columns leave (8 bytes a warp's half of them), and its label's z
 //   GRAD   z's tiles again, for a piece of the vocabulary; d leaves in 16 bits
 //   PROD   both gradients of a piece in one launch: dh (K over the piece's
 //          columns) and dW (K over the tokens)
@@ -18,13 +18,27 @@
 //
 // d is row-major [T][piece]: for dh it is the A operand as it lies (K inner), for
 // dW it is A with M inner, and W and h are B with N inner: the tensor cores take
-// both, so nothing is transposed.  Operands come by TMA (128-byte swizzle), sums
-// lie in two accumulators of 256 columns of tensor memory in turn, so that a
-// tile's epilogue runs under the next tile's products; results leave through
-// shared memory by TMA.
+// both, so nothing is transposed.  A tile is 128 x 256 of one CTA, or 256 x 256 of
+// a pair of CTAs whose tensor cores work as one (each loads its 128 rows of A and
+// its half of B's columns: two thirds of the shared-memory traffic per product,
+// and six steps of K = 64 on their way instead of four).  Operands come by TMA
+// (128-byte swizzle), sums lie in two accumulators of 256 columns of tensor memory
+// in turn, so that a tile's way out runs under the next tile's products; results
+// leave through shared memory by TMA.  Tiles of both jobs of PROD are dealt out so
+// that all CTAs end together; dh's long sums are split into parts where they are
+// too few for that.
+//
+// Measured on one GB300 (bf16, H = 2,048): 4,096 tokens against 65,536 words 519
+// us (2.1 PFLOP/s; by single CTAs 563), with both gradients 2.44 ms (1.8 PFLOP/s,
+// power-bound; by single CTAs 2.69); four tokens against 100,003 words 80 us (410
+// MB of W, 5.1 TB/s); 1,111 tokens, H = 1,056, 8,191 words with gradients 70 us.
+// Tried without gain: W on its way to L2 in boxes of 512 bytes a row (four tokens
+// 79 -> 89 us), results straight from the registers, the next columns loaded from
+// tensor memory ahead, four blocks of results on their way instead of two.
 //
 // Every wait is bounded: after about 2 s the CTA records MOE_ERR_TIMEOUT and
 // stops.
+#include "cluster.cuh"
 #include "dense_tc.cuh"
 #include "rows.cuh"
 #include "tc.cuh"
@@ -38,14 +52,20 @@ using tc::uniform;
 
 enum Kind { LOSS, GRAD, PROD };
 
-constexpr int BM = 128, BN = 256, BK = 64;
-constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2;
-constexpr int STAGES = 4;
-constexpr int EPI_WARP0 = 2, EPI_WARPS = 4;
+constexpr int ROWS = 128, BN = 256, BK = 64;  // a CTA's rows of a tile, its most columns, K of a step
+constexpr int A_BYTES = ROWS * BK * 2;
+
+// A tile is one CTA's (C = 1: 128 rows) or a pair's (C = 2: 256 rows), each with its rows of A and its half of B's columns.
+template <int C>
+struct Tile {
+    static constexpr int BM = ROWS * C, B_BYTES = BN / C * BK * 2, STAGES = C == 1 ? 4 : 6;
+};
+constexpr int MAX_STAGES = 6;
+constexpr int EPI_WARP0 = 2, EPI_WARPS = 8;  // two per quarter of the lanes: every other 32 columns each
 constexpr int THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
 constexpr int OUT_BYTES = 32 * 128;  // a warp's 32 rows of 32 values on their way out, two in turn
-constexpr size_t SMEM = STAGES * (A_BYTES + B_BYTES) + EPI_WARPS * 2 * OUT_BYTES + 1024;
-constexpr int BAND = 32;  // row tiles that pass over the columns together
+constexpr size_t SMEM = 192 * 1024 + EPI_WARPS * OUT_BYTES + 1024;
+constexpr int BAND_ROWS = 4096;  // rows that pass over the columns together
 constexpr unsigned long long kWaitNs = 2000000000ull;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float FUSED = 1e6f;  // below it x log2 e is rounded by at most 1/16
@@ -61,8 +81,8 @@ struct Job {
     int add, out_f32;
 };
 
-// Which items a CTA takes: of the first job every G-th (G the grid), then of the
-// second what evens the CTAs out: `long_items` each for those with one more of the first,
+// Which items a CTA or pair takes: of the first job every G-th (G of them in all), then of the
+// second what evens them out: `long_items` each for those with one more of the first,
 // `short_items` for the others.
 struct Params {
     Job job[2];
@@ -72,9 +92,10 @@ struct Params {
     int v0, all;        // the piece's first column, columns of the whole vocabulary
     int f16;
     const int32_t *labels;
-    float2 *stats;      // [T][n tiles]
+    float2 *stats;      // [T][n tiles][2]
     float *label_z;
-    const float *lse, *dloss, *dlse, *top;
+    const float *lse, *dloss, *dlse;
+    float *top;         // the largest |dloss| or |dlse|: written by GRAD, for PROD
     int32_t *status;
 };
 
@@ -83,10 +104,11 @@ struct Maps {
 };
 
 struct Shared {
-    uint64_t full[STAGES], empty[STAGES];
+    uint64_t full[MAX_STAGES], empty[MAX_STAGES];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t mma_done;
     uint32_t tmem;
+    float top[EPI_WARPS];
     volatile int abort;
 };
 
@@ -95,11 +117,13 @@ struct Item {
     int kb0, kb1;       // steps
 };
 
-// The CTA's i-th item; false when there are no more.  Row tiles first, within bands of BAND: the tiles at work
+// The CTA's or pair's i-th item; false when there are no more.  Row tiles first, within bands of BAND: the tiles at work
 // share the columns' operand, and a band's rows stay in L2.
+template <int C>
 __device__ __forceinline__ bool item_of(const Params &p, int i, Item &it)
 {
-    const int c = blockIdx.x, G = gridDim.x;
+    constexpr int BAND = BAND_ROWS / Tile<C>::BM;
+    const int c = blockIdx.x / C, G = gridDim.x / C;
     int t = c + i * G;
     it.j = 0;
     if (t >= p.items0) {
@@ -131,6 +155,77 @@ __device__ __forceinline__ bool warp_wait(Shared &S, uint64_t *bar, uint32_t par
     if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
     const bool ok = tc::mbar_wait(bar, parity, kWaitNs);
     return __all_sync(0xffffffffu, ok && !S.abort);
+}
+
+// The shared-memory address of the pair's first CTA that corresponds to this CTA's.
+__device__ __forceinline__ uint32_t leaders(const void *p)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(tc::smem_u32(p)));
+    return a;
+}
+
+// Arrive on the first CTA's barrier, and its wait for both CTAs' arrivals.
+template <int C>
+__device__ __forceinline__ void arrive_leader(uint64_t *bar)
+{
+    if (C == 1) return tc::mbar_arrive(bar);
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leaders(bar)) : "memory");
+}
+
+__device__ __forceinline__ bool cluster_try_wait(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ bool warp_wait_pair(Shared &S, uint64_t *bar, uint32_t parity)
+{
+    bool ok = cluster_try_wait(bar, parity);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    const unsigned long long t0 = tc::now_ns();
+    while (!ok && tc::now_ns() - t0 <= kWaitNs) ok = cluster_try_wait(bar, parity);
+    return __all_sync(0xffffffffu, ok && !S.abort);
+}
+
+// A box into this CTA's shared memory, its bytes counted by the first CTA's barrier.
+template <int C>
+__device__ __forceinline__ void load(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar, uint32_t leader_bar)
+{
+    if (C == 1) return tc::tma_load_2d(dst, map, x, y, bar);
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            tc::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(leader_bar)
+        : "memory");
+}
+
+// D[tmem] (+)= A B^T; a pair's, each CTA's part of the operands at the same places of its shared memory.
+template <int C>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    if (C == 1) return tc::mma_f16_ss(d, a, b, idesc, accumulate);
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrive on the CTA's or both CTAs' barriers once the MMAs issued so far are done.
+template <int C>
+__device__ __forceinline__ void commit(uint64_t *bar)
+{
+    if (C == 1) return tc::mma_commit(bar);
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     tc::smem_u32(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
 }
 
 // Descriptor of an operand with M or N inner, 128-byte swizzle: 64 elements (128 bytes) a row, eight K rows
@@ -178,9 +273,19 @@ __device__ __forceinline__ void put_row(char *buf, int lane, const uint32_t (&w)
     }
 }
 
-template <Kind K>
+// All threads of the CTA or pair.
+template <int C>
+__device__ __forceinline__ void tile_sync()
+{
+    if (C == 1) __syncthreads();
+    else cluster_sync();
+}
+
+template <Kind K, int C>
 __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps)
 {
+    using Z = Tile<C>;
+    constexpr int BM = Z::BM, STAGES = Z::STAGES, B_BYTES = Z::B_BYTES;
     extern __shared__ __align__(1024) char dyn_raw[];
     char *dyn = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~uintptr_t(1023));
     char *sA = dyn, *sB = sA + STAGES * A_BYTES, *sO = sB + STAGES * B_BYTES;
@@ -194,20 +299,25 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
         }
         for (int i = 0; i < 2; i++) {
             tc::mbar_init(&S.acc_full[i], 1);
-            tc::mbar_init(&S.acc_empty[i], EPI_WARPS);
+            tc::mbar_init(&S.acc_empty[i], C * EPI_WARPS);  // both CTAs'; the first one's barrier is the one waited for
         }
         tc::mbar_init(&S.mma_done, 1);
         S.abort = 0;
         tc::fence_mbar_init();
     }
-    if (warp == EPI_WARP0) tc::tmem_alloc(&S.tmem, 512);
+    if (warp == EPI_WARP0 && C == 1) tc::tmem_alloc(&S.tmem, 512);
+    if (warp == EPI_WARP0 && C == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::smem_u32(&S.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
     // (launched while the kernel before it may still run, and lets the next one come as soon: nothing above reads what that one writes)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc::tc_fence_before();
-    __syncthreads();
+    tile_sync<C>();  // both CTAs' barriers are there
     tc::tc_fence_after();
     const uint32_t tmem = (uint32_t)uniform((int)S.tmem);
+    const int rank = C == 1 ? 0 : uniform((int)cluster_rank());
 
     if (warp == 0) {
         // ---------------- operands
@@ -215,28 +325,30 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
         uint32_t phase = 1;
         bool ok = true;
         Item m;
-        for (int i = 0; ok && item_of(p, i, m); i++) {
+        for (int i = 0; ok && item_of<C>(p, i, m); i++) {
             const Job &g = p.job[m.j];
-            const int boxes = (g.bn + 63) / 64;
-            const uint32_t bytes = A_BYTES + (K == PROD ? boxes * (BK * 128) : g.bn * 128);
+            const int half = g.bn / C, boxes = (half + 63) / 64;
+            const uint32_t bytes = A_BYTES + (K == PROD ? boxes * (BK * 128) : half * 128);
             for (int kb = m.kb0; kb < m.kb1; kb++, it++) {
                 if (it >= STAGES) ok = warp_wait(S, &S.empty[s], phase);
                 if (!ok) break;
                 if (elect_one()) {
-                    tc::mbar_arrive_expect_tx(&S.full[s], bytes);
+                    if (rank == 0) tc::mbar_arrive_expect_tx(&S.full[s], C * bytes);
+                    uint64_t *own = &S.full[s];
+                    const uint32_t bar = C == 1 ? 0 : leaders(own);
                     char *a = sA + s * A_BYTES, *b = sB + s * B_BYTES;
                     if (K == PROD && g.mn_a) {
 #pragma unroll
-                        for (int h = 0; h < BM / 64; h++)
-                            tc::tma_load_2d(a + h * BK * 128, &maps.a[m.j], m.m * BM + h * 64, kb * BK, &S.full[s]);
+                        for (int h = 0; h < ROWS / 64; h++)
+                            load<C>(a + h * BK * 128, &maps.a[m.j], m.m * BM + rank * ROWS + h * 64, kb * BK, own, bar);
                     } else {
-                        tc::tma_load_2d(a, &maps.a[m.j], kb * BK, m.m * BM, &S.full[s]);
+                        load<C>(a, &maps.a[m.j], kb * BK, m.m * BM + rank * ROWS, own, bar);
                     }
                     if (K == PROD) {
                         for (int h = 0; h < boxes; h++)
-                            tc::tma_load_2d(b + h * BK * 128, &maps.b[m.j], m.n * g.bn + h * 64, g.b_y0 + kb * BK, &S.full[s]);
+                            load<C>(b + h * BK * 128, &maps.b[m.j], m.n * g.bn + rank * half + h * 64, g.b_y0 + kb * BK, own, bar);
                     } else {
-                        tc::tma_load_2d(b, &maps.b[m.j], kb * BK, g.b_y0 + m.n * g.bn, &S.full[s]);
+                        load<C>(b, &maps.b[m.j], kb * BK, g.b_y0 + m.n * g.bn + rank * half, own, bar);
                     }
                 }
                 if (++s == STAGES) s = 0, phase ^= 1;
@@ -247,24 +359,31 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                 set_status(p.status, MOE_ERR_TIMEOUT);
                 S.abort = 1;
             }
-            // no copy may still be in flight when the CTA leaves
+            // no copy, and no arrival from the products, may still be on its way when the pair leaves: every stage's last
+            // use is over (after a stop: every copy has landed, in the first CTA's count of both CTAs')
             for (int i = 0; i < STAGES && i < it; i++) {
-                const int u = (it - 1 - i) / STAGES;
-                if (!tc::mbar_wait(&S.full[(it - 1 - i) % STAGES], u & 1, kWaitNs)) set_status(p.status, MOE_ERR_TIMEOUT);
+                const int u = (it - 1 - i) / STAGES, at = (it - 1 - i) % STAGES;
+                bool over = true;
+                if (ok && !S.abort) over = tc::mbar_wait(&S.empty[at], u & 1, kWaitNs);
+                else if (rank == 0) over = tc::mbar_wait(&S.full[at], u & 1, kWaitNs / 100);
+                if (!over) {
+                    set_status(p.status, MOE_ERR_TIMEOUT);
+                    S.abort = 1;
+                }
             }
         }
     } else if (warp == 1) {
-        // ---------------- MMA
+        // ---------------- MMA, by the pair's first CTA
         int j = 0, s = 0;
         uint32_t phase = 0;
         bool ok = true;
         Item m;
-        for (int i = 0; ok && item_of(p, i, m); i++) {
+        for (int i = 0; rank == 0 && ok && item_of<C>(p, i, m); i++) {
             const Job &g = p.job[m.j];
             if (m.kb0 == m.kb1) continue;  // a part of nothing
             const int acc = j & 1, v = j >> 1;
             j++;
-            if (v > 0) ok = warp_wait(S, &S.acc_empty[acc], (v - 1) & 1);
+            if (v > 0) ok = (C == 1 ? warp_wait : warp_wait_pair)(S, &S.acc_empty[acc], (v - 1) & 1);
             if (!ok) break;
             tc::tc_fence_after();
             const uint32_t d = tmem + (uint32_t)(acc * BN);
@@ -287,9 +406,9 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                     const int left = K == PROD ? g.K - kb * BK : BK;  // (d's columns past K's last sixteen may never have been written)
 #pragma unroll
                     for (int k = 0; k < BK / 16; k++)
-                        if (k * 16 < left) tc::mma_f16_ss(d, da + k * ka, db + k * kbs, idesc, (kb > m.kb0 || k > 0) ? 1u : 0u);
-                    tc::mma_commit(&S.empty[s]);
-                    if (kb + 1 == m.kb1) tc::mma_commit(&S.acc_full[acc]);
+                        if (k * 16 < left) mma<C>(d, da + k * ka, db + k * kbs, idesc, (kb > m.kb0 || k > 0) ? 1u : 0u);
+                    commit<C>(&S.empty[s]);
+                    if (kb + 1 == m.kb1) commit<C>(&S.acc_full[acc]);
                 }
                 s = sn;
                 phase = phase_n;
@@ -299,23 +418,39 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
             set_status(p.status, MOE_ERR_TIMEOUT);
             S.abort = 1;
         }
-        if (elect_one()) tc::mma_commit(&S.mma_done);
+        if (rank == 0 && elect_one()) commit<C>(&S.mma_done);
         if (!tc::mbar_wait(&S.mma_done, 0, kWaitNs) && lane == 0) set_status(p.status, MOE_ERR_TIMEOUT);
     } else {
         // ---------------- sums out
-        const int q = warp & 3;
-        char *out = sO + (warp - EPI_WARP0) * 2 * OUT_BYTES;
+        const int q = warp & 3, side = (warp - EPI_WARP0) >> 2;
+        char *out = sO + (warp - EPI_WARP0) * OUT_BYTES;
         int j = 0, turn = 0;
-        const float top = K == LOSS ? 0.f : *p.top;
+        bool was32 = false;
+        // the largest |dloss| or |dlse| of the tokens that count, by every CTA for itself, under its first tile's products
+        float top = K == PROD ? *p.top : 0.f;
+        if (K == GRAD) {
+#pragma unroll 4
+            for (int t = threadIdx.x - EPI_WARP0 * 32; t < p.T; t += EPI_WARPS * 32) {
+                const int label = p.labels[t];
+                if (label >= 0 && label < p.all) top = fmaxf(top, fabsf(p.dloss[t]));
+                if (p.dlse) top = fmaxf(top, fabsf(p.dlse[t]));
+            }
+            top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+            if (lane == 0) S.top[warp - EPI_WARP0] = top;
+            tc::named_sync(1, EPI_WARPS * 32);
+#pragma unroll
+            for (int w = 0; w < EPI_WARPS; w++) top = fmaxf(top, S.top[w]);
+            if (blockIdx.x == 0 && threadIdx.x == EPI_WARP0 * 32) *p.top = top;
+        }
         const float up = K == PROD ? (p.f16 ? top / F16_ROOM : top) : 0.f;
         const float down = K == GRAD && top > 0.f ? (p.f16 ? F16_ROOM : 1.f) : 0.f;
         Item m;
-        for (int i = 0; item_of(p, i, m); i++) {
+        for (int i = 0; item_of<C>(p, i, m); i++) {
             const Job &g = p.job[m.j];
             if (m.kb0 == m.kb1) continue;
             const int acc = j & 1, v = j >> 1;
             j++;
-            const int row = m.m * BM + q * 32 + lane, n0 = m.n * g.bn;
+            const int row = m.m * BM + rank * ROWS + q * 32 + lane, n0 = m.n * g.bn;
             int label = -1;
             float lse = 0.f, nl = 0.f, a = 0.f, b = 0.f;
             if (K != PROD && row < p.T) label = p.labels[row];
@@ -341,7 +476,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                 float mx = -INFINITY, sum = 0.f, zl = 0.f;
                 bool mine = false;
 #pragma unroll 1
-                for (int c = 0; c < g.bn; c += 32) {
+                for (int c = side * 32; c < g.bn; c += 64) {
                     const int left = p.V - n0 - c;
                     if (left <= 0) break;
                     uint32_t r[32];
@@ -378,12 +513,12 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                     mx = cm;
                 }
                 if (row < p.T) {
-                    p.stats[(int64_t)row * g.n_tiles + m.n] = make_float2(mx, sum);
+                    p.stats[((int64_t)row * g.n_tiles + m.n) * 2 + side] = make_float2(mx, sum);
                     if (mine) p.label_z[row] = zl;
                 }
             } else {
 #pragma unroll 1
-                for (int c = 0; c < g.bn; c += 32) {
+                for (int c = side * 32; c < g.bn; c += 64) {
                     uint32_t r[32];
                     __syncwarp();
                     tc::tmem_ld_32x32b_x32(tbase + c, r);
@@ -416,15 +551,19 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
 #pragma unroll
                         for (int i = 0; i < 16; i++) r[i] = pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), p.f16);
                     }
-                    char *buf = out + (turn & 1) * OUT_BYTES;
+                    char *buf = out + (f32 ? 0 : (turn & 1) * (OUT_BYTES / 2));
                     turn++;
-                    if (lane == 0) tc::bulk_wait_read<1>();
+                    if (lane == 0) {
+                        if (K == PROD && (f32 || was32)) tc::bulk_wait_read<0>();
+                        else tc::bulk_wait_read<1>();
+                    }
+                    was32 = f32;
                     __syncwarp();
                     put_row(buf, lane, r, f32);
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        const int x = n0 + c, y = g.out_y0 + m.part * g.part_rows + m.m * BM + q * 32;
+                        const int x = n0 + c, y = g.out_y0 + m.part * g.part_rows + m.m * BM + rank * ROWS + q * 32;
                         if (K == PROD && g.add) tma_add_2d(&maps.out[m.j], x, y, buf);
                         else tc::tma_store_2d(&maps.out[m.j], x, y, buf);
                         tc::bulk_commit();
@@ -433,15 +572,16 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
             }
             tc::tc_fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&S.acc_empty[acc]);
+            if (lane == 0) arrive_leader<C>(&S.acc_empty[acc]);
         }
         if (K != LOSS && lane == 0) tc::bulk_wait_all();
     }
     tc::tc_fence_before();
-    __syncthreads();
+    tile_sync<C>();  // neither CTA leaves while the other's products read its operands or write its sums
     if (warp == EPI_WARP0) {
         tc::tc_fence_after();
-        tc::tmem_dealloc(tmem, 512);
+        if (C == 1) tc::tmem_dealloc(tmem, 512);
+        else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
 }
 
@@ -490,27 +630,6 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32) combine_kernel(const float
     loss[t] = v < 0.f ? 0.f : v;
 }
 
-// The largest |dloss| or |dlse| of the tokens that count; one CTA.
-__global__ void __launch_bounds__(1024) top_kernel(const float *dloss, const float *dlse, const int32_t *labels, int T, int V, float *top)
-{
-    __shared__ float part[32];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    float m = 0.f;
-    for (int t = threadIdx.x; t < T; t += 1024) {
-        const int label = labels[t];
-        if (label >= 0 && label < V) m = fmaxf(m, fabsf(dloss[t]));
-        if (dlse) m = fmaxf(m, fabsf(dlse[t]));
-    }
-    m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
-    if (lane_id() == 0) part[warp_id()] = m;
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(part[threadIdx.x])));
-        if (threadIdx.x == 0) *top = m;
-    }
-}
-
 // The parts' fp32 sums, in order, to 16 bits, eight values at a time (a part's n values are a multiple of eight).
 template <class A>
 __global__ void __launch_bounds__(256) round_kernel(const float *in, int parts, int64_t part, typename A::T *out, int64_t n)
@@ -547,16 +666,27 @@ static int round_up(int n, int b) { return tiles(n, b) * b; }
 // Columns of a tile: equal ones over all n.
 static int tile_columns(int n) { return round_up(tiles(n, tiles(n, BN)), 32); }
 
-// The vocabulary's tiles for the logits: as wide as they go, unless narrower ones fill the last round of CTAs better
-// (100,003 columns for one row tile on 152 SMs: three rounds of 224 instead of 256).
-static int vocabulary_columns(int rows, int V, int sms)
+// Measured time of a step (K = 64) of 256 columns in us: pairs read and store less through shared memory per product and
+// have two more steps on their way (4,096 x 2,048 against 65,536: 563 us by single CTAs, 516 by pairs).
+static double step_us(int C) { return C == 1 ? 0.325 : 0.298; }
+
+// Tiles of the logits: by single CTAs or pairs, as wide as they go unless narrower ones fill the last round better
+// (100,003 columns for one row tile on 152 SMs: three rounds of 224 instead of 256).  A tile costs its steps and some 16
+// columns' worth besides.
+struct Cut {
+    int C, bn;
+};
+
+static Cut cut_logits(int rows, int V, int sms)
 {
-    int best = BN;
-    int64_t least = INT64_MAX;
-    for (int bn = BN; bn >= 128; bn -= 32) {
-        const int64_t rounds = ((int64_t)tiles(rows, BM) * tiles(V, bn) + sms - 1) / sms, cost = rounds * (bn + 16);
-        if (cost < least) least = cost, best = bn;
-    }
+    Cut best = {1, BN};
+    double least = 1e300;
+    for (int C = 1; C <= 2; C++)
+        for (int bn = BN; bn >= 128; bn -= 32) {
+            const int64_t items = (int64_t)tiles(rows, ROWS * C) * tiles(V, bn), at_once = sms / C;
+            const double cost = (double)((items + at_once - 1) / at_once) * (bn + 16) * step_us(C);
+            if (cost < least) least = cost, best = {C, bn};
+        }
     return best;
 }
 
@@ -569,6 +699,9 @@ struct Deal {
 
 static Deal deal(int64_t items0, int64_t nk0, int64_t items1, int64_t nk1, int64_t G)
 {
+    // a tile's way out takes as long as some six steps, under the next tile's steps where those are more
+    nk0 = std::max<int64_t>(nk0, 6);
+    nk1 = std::max<int64_t>(nk1, 6);
     Deal best = {0, 0, 0, INT64_MAX};
     const int64_t q = items0 / G, r = items0 % G;
     auto with = [&](int64_t s) {  // s items of the second job for a CTA without an extra one of the first
@@ -579,7 +712,7 @@ static Deal deal(int64_t items0, int64_t nk0, int64_t items1, int64_t nk1, int64
         if (steps < best.steps) best = {(int)r, (int)l, (int)s, steps};
     };
     with((items1 + G - r - 1) / (G - r));
-    if (nk1 > 0) {  // about where all have the same
+    if (items1 > 0) {  // about where all have the same
         const int64_t s = ((items0 * nk0 + items1 * nk1) / G - q * nk0) / nk1;
         for (int64_t i = s - 1; i <= s + 2; i++) with(i);
     }
@@ -587,12 +720,12 @@ static Deal deal(int64_t items0, int64_t nk0, int64_t items1, int64_t nk1, int64
 }
 
 struct Layout {
-    int columns, pieces, parts;  // dh's sums over a piece are split into parts
+    int columns, pieces, parts, C;  // dh's sums over a piece are split into parts; by CTAs or pairs
     int64_t part_rows;
     size_t d, sums, total;  // bytes: d after the top value, fp32 sums of dh when there are several pieces or parts
 };
 
-// Splitting dh's sums pays where its few, long items would leave the other CTAs waiting: steps of 0.27 us are weighed
+// Splitting dh's sums pays where its few, long items would leave the other CTAs waiting: the steps' time is weighed
 // against a part's sums, written and read (8 bytes a value at 6 TB/s), and a launch for them.
 static Layout layout(int T, int H, int V)
 {
@@ -601,15 +734,17 @@ static Layout layout(int T, int H, int V)
     l.columns = piece_columns(T, V);
     l.pieces = tiles(V, l.columns);
     const int n = std::min(V, l.columns), nk0 = tiles(n, BK), nk1 = tiles(T, BK), nt = tiles(H, BN);
-    const int64_t items0 = (int64_t)tiles(T, BM) * nt, items1 = (int64_t)tiles(n, BM) * nt;
-    l.part_rows = round_up(T, BM);
-    l.parts = 1;
-    double least = 0;
-    for (int s = 1; s <= 32 && s <= nk0; s++) {
-        const Deal d = deal(items0 * s, tiles(nk0, s), items1, nk1, std::min<int64_t>(items0 * s + items1, sms));
-        const double us = 0.27 * d.steps + (s > 1 || l.pieces > 1 ? 3.0 / l.pieces + 1.3e-6 * s * T * H * (l.pieces > 1 ? 2 : 1) : 0);
-        if (s == 1 || us < least) least = us, l.parts = s;
+    double least = 1e300;
+    for (int C = 1; C <= 2; C++) {
+        const int64_t items0 = (int64_t)tiles(T, ROWS * C) * nt, items1 = (int64_t)tiles(n, ROWS * C) * nt;
+        for (int s = 1; s <= 32 && s <= nk0; s++) {
+            const Deal d = deal(items0 * s, tiles(nk0, s), items1, nk1, std::min<int64_t>(items0 * s + items1, sms / C));
+            const double us = step_us(C) * tile_columns(H) / BN * d.steps +
+                              (s > 1 || l.pieces > 1 ? 3.0 / l.pieces + 1.3e-6 * s * T * H * (l.pieces > 1 ? 2 : 1) : 0);
+            if (us < least) least = us, l.parts = s, l.C = C;
+        }
     }
+    l.part_rows = round_up(T, ROWS * l.C);
     l.d = 256;
     l.sums = l.d + align256((size_t)T * l.columns * 2);
     l.total = l.sums + (l.pieces > 1 || l.parts > 1 ? align256((size_t)l.parts * l.part_rows * H * 4) : 0);
@@ -621,7 +756,7 @@ static moe_status check(int T, int H, int V)
     MOE_REQUIRE(T >= 0 && T <= (1 << 24), "T must be in [0, 2^24] (got %d)", T);
     MOE_REQUIRE(H >= 8 && H % 8 == 0 && H <= (1 << 20), "H must be a multiple of 8 in [8, 2^20] (got %d)", H);
     MOE_REQUIRE(V >= 1 && V <= (1 << 24), "V must be in [1, 2^24] (got %d)", V);
-    MOE_REQUIRE((int64_t)tiles(T, BM) * tiles(V, BN / 2) < (1 << 30) && (int64_t)std::max(T, V) * H < (1ll << 40),
+    MOE_REQUIRE((int64_t)tiles(T, ROWS) * tiles(V, BN / 2) < (1 << 30) && (int64_t)std::max(T, V) * H < (1ll << 40),
                 "too many tiles (T=%d H=%d V=%d)", T, H, V);
     return MOE_OK;
 }
@@ -638,33 +773,42 @@ static moe_status check_types(const void *h, moe_dtype dtype, int T, int H, cons
 }
 
 template <class F, class... A>
-moe_status launch(const char *what, F kernel, int grid, int threads, size_t smem, cudaStream_t s, const A &...args)
+moe_status launch(const char *what, F kernel, int cluster, int grid, int threads, size_t smem, cudaStream_t s, const A &...args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute at[1];  // the set-up overlaps the end of the kernel before
+    cudaLaunchAttribute at[2];  // the set-up overlaps the end of the kernel before
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, args...));
     return check_launch(what);
 }
 
-template <Kind K>
+template <Kind K, int C>
 moe_status product(Params &p, const Maps &maps, cudaStream_t s)
 {
     auto items = [](const Job &g) { return g.m_tiles * g.n_tiles * g.parts; };
     p.items0 = items(p.job[0]);
     p.items1 = items(p.job[1]);
-    const int grid = (int)std::min<int64_t>((int64_t)p.items0 + p.items1, sm_count());
-    const Deal d = deal(p.items0, tiles(tiles(p.job[0].K, BK), p.job[0].parts), p.items1, tiles(p.job[1].K, BK), grid);
+    const int at_once = (int)std::min<int64_t>((int64_t)p.items0 + p.items1, sm_count() / C);
+    const Deal d = deal(p.items0, tiles(tiles(p.job[0].K, BK), p.job[0].parts), p.items1, tiles(p.job[1].K, BK), at_once);
     p.longer = d.longer, p.long_items = d.long_items, p.short_items = d.short_items;
-    MOE_CUDA_TRY(cudaFuncSetAttribute(product_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM));
-    return launch("cross_entropy", product_kernel<K>, grid, THREADS, SMEM, s, p, maps);
+    MOE_CUDA_TRY(cudaFuncSetAttribute(product_kernel<K, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM));
+    return launch("cross_entropy", product_kernel<K, C>, C, C * at_once, THREADS, SMEM, s, p, maps);
+}
+
+template <Kind K>
+moe_status product(int C, Params &p, const Maps &maps, cudaStream_t s)
+{
+    return C == 1 ? product<K, 1>(p, maps, s) : product<K, 2>(p, maps, s);
 }
 
 static CUtensorMapDataType map_type(moe_dtype t)
@@ -684,7 +828,7 @@ extern "C" moe_status moe_cross_entropy_workspace_size(int T, int H, int V, size
     MOE_REQUIRE(bytes, "bytes must not be NULL");
     moe_status st = check(T, H, V);
     if (st != MOE_OK) return st;
-    *bytes = align256((size_t)T * 4) + align256((size_t)tiles(V, vocabulary_columns(T, V, sm_count())) * T * 8);
+    *bytes = align256((size_t)T * 4) + align256((size_t)tiles(V, cut_logits(T, V, sm_count()).bn) * T * 16);
     return MOE_OK;
 }
 
@@ -706,20 +850,21 @@ extern "C" moe_status moe_cross_entropy(const void *h, moe_dtype dtype, int T, i
     MOE_REQUIRE(aligned16(ws), "ws must be 16-byte aligned");
     Params p = {};
     Maps maps = {};
-    const int bn = vocabulary_columns(T, V, sm_count()), n_tiles = tiles(V, bn);
-    p.job[0] = {tiles(T, BM), n_tiles, bn, H, 1, 0, 0, 0, 0, 0, 0};
-    p.idesc = tc::idesc_f16_f32(BM, 0, dtype == MOE_BF16);
+    const Cut cut = cut_logits(T, V, sm_count());
+    const int n_tiles = tiles(V, cut.bn);
+    p.job[0] = {tiles(T, ROWS * cut.C), n_tiles, cut.bn, H, 1, 0, 0, 0, 0, 0, 0};
+    p.idesc = tc::idesc_f16_f32(ROWS * cut.C, 0, dtype == MOE_BF16);
     p.T = T, p.V = V, p.labels = labels, p.status = dev_status;
     p.label_z = static_cast<float *>(ws);
     p.stats = reinterpret_cast<float2 *>(static_cast<char *>(ws) + align256((size_t)T * 4));
-    st = make_tmap_2d(&maps.a[0], h, map_type(dtype), 2, T, H, BK, BM);
-    if (st == MOE_OK) st = make_tmap_2d(&maps.b[0], w, map_type(dtype), 2, V, H, BK, bn);
+    st = make_tmap_2d(&maps.a[0], h, map_type(dtype), 2, T, H, BK, ROWS);
+    if (st == MOE_OK) st = make_tmap_2d(&maps.b[0], w, map_type(dtype), 2, V, H, BK, cut.bn / cut.C);
     if (st != MOE_OK) return st;
     const cudaStream_t s = to_cuda(stream);
-    st = product<LOSS>(p, maps, s);
+    st = product<LOSS>(cut.C, p, maps, s);
     if (st != MOE_OK) return st;
-    return launch("cross_entropy_combine", combine_kernel, tiles(T, COMBINE_WARPS), COMBINE_WARPS * 32, 0, s, p.stats, p.label_z, labels, T,
-                  V, n_tiles, loss, lse, dev_status);
+    return launch("cross_entropy_combine", combine_kernel, 1, tiles(T, COMBINE_WARPS), COMBINE_WARPS * 32, 0, s, p.stats, p.label_z, labels, T,
+                  V, 2 * n_tiles, loss, lse, dev_status);
 }
 
 extern "C" moe_status moe_cross_entropy_backward_workspace_size(int T, int H, int V, size_t *bytes)
@@ -760,22 +905,22 @@ extern "C" moe_status moe_cross_entropy_backward(const void *h, moe_dtype dtype,
     float *top = reinterpret_cast<float *>(base), *sums = reinterpret_cast<float *>(base + l.sums);
     void *d = base + l.d;
 
-    st = launch("cross_entropy_top", top_kernel, 1, 1024, 0, s, dloss, dlse, labels, T, V, top);
-    if (st != MOE_OK) return st;
     Params gp = {}, pp = {};
     Maps gm = {}, pm = {};
     const int f16 = dtype == MOE_F16;
-    gp.idesc = pp.idesc = tc::idesc_f16_f32(BM, 0, !f16);
+    const Cut cut = cut_logits(T, std::min(V, l.columns), sm_count());  // (of every piece)
+    gp.idesc = tc::idesc_f16_f32(ROWS * cut.C, 0, !f16);
+    pp.idesc = tc::idesc_f16_f32(ROWS * l.C, 0, !f16);
     gp.T = T, gp.all = V, gp.labels = labels, gp.lse = lse, gp.dloss = dloss, gp.dlse = dlse, gp.top = pp.top = top;
     gp.status = pp.status = dev_status;
     gp.f16 = pp.f16 = f16;
     const bool direct = l.pieces == 1 && l.parts == 1;  // dh leaves as it is: no sums of pieces or parts
     const auto half = CU_TENSOR_MAP_SWIZZLE_64B;        // boxes of 32 16-bit columns
-    st = make_tmap_2d(&gm.a[0], h, map_type(dtype), 2, T, H, BK, BM);
-    if (st == MOE_OK) st = make_tmap_2d(&gm.b[0], w, map_type(dtype), 2, V, H, BK, BN);
+    st = make_tmap_2d(&gm.a[0], h, map_type(dtype), 2, T, H, BK, ROWS);
+    if (st == MOE_OK) st = make_tmap_2d(&gm.b[0], w, map_type(dtype), 2, V, H, BK, cut.bn / cut.C);
     if (st == MOE_OK) st = make_tmap_2d(&gm.out[0], d, map_type(dtype), 2, T, l.columns, 32, 32, half);
     CUtensorMap d_k, d_m, w_n, h_n, out_h, out_w;
-    if (st == MOE_OK) st = make_tmap_2d(&d_k, d, map_type(dtype), 2, T, l.columns, BK, BM);
+    if (st == MOE_OK) st = make_tmap_2d(&d_k, d, map_type(dtype), 2, T, l.columns, BK, ROWS);
     if (st == MOE_OK) st = make_tmap_2d(&d_m, d, map_type(dtype), 2, T, l.columns, 64, BK);
     if (st == MOE_OK) st = make_tmap_2d(&w_n, w, map_type(dtype), 2, V, H, 64, BK);
     if (st == MOE_OK) st = make_tmap_2d(&h_n, h, map_type(dtype), 2, T, H, 64, BK);
@@ -791,28 +936,28 @@ extern "C" moe_status moe_cross_entropy_backward(const void *h, moe_dtype dtype,
         const int v0 = i * l.columns, n = std::min(l.columns, V - v0);
         gp.v0 = v0;
         gp.V = n;
-        gp.job[0] = {tiles(T, BM), tiles(n, BN), BN, H, 1, 0, v0, 0, 0, 0, 0};
-        st = product<GRAD>(gp, gm, s);
+        gp.job[0] = {tiles(T, ROWS * cut.C), tiles(n, cut.bn), cut.bn, H, 1, 0, v0, 0, 0, 0, 0};
+        st = product<GRAD>(cut.C, gp, gm, s);
         if (st != MOE_OK) return st;
         int j = 0;
         if (dh) {
-            pp.job[j] = {tiles(T, BM), nt, bn, n, l.parts, 0, v0, 0, (int)l.part_rows, !direct && i > 0, !direct};
+            pp.job[j] = {tiles(T, ROWS * l.C), nt, bn, n, l.parts, 0, v0, 0, (int)l.part_rows, !direct && i > 0, !direct};
             pm.a[j] = d_k, pm.b[j] = w_n, pm.out[j] = out_h;
             j++;
         }
         if (dw) {
-            pp.job[j] = {tiles(n, BM), nt, bn, T, 1, 1, 0, v0, 0, accumulate != 0, dw_dtype == MOE_F32};
+            pp.job[j] = {tiles(n, ROWS * l.C), nt, bn, T, 1, 1, 0, v0, 0, accumulate != 0, dw_dtype == MOE_F32};
             pm.a[j] = d_m, pm.b[j] = h_n, pm.out[j] = out_w;
             j++;
         }
-        st = product<PROD>(pp, pm, s);
+        st = product<PROD>(l.C, pp, pm, s);
         if (st != MOE_OK) return st;
     }
     if (dh && !direct) {
         const int64_t n = (int64_t)T * H;
         const int grid = (int)std::min<int64_t>((n + 2047) / 2048, (int64_t)sm_count() * 8);
-        return f16 ? launch("cross_entropy_round", round_kernel<Fp16>, grid, 256, 0, s, sums, l.parts, l.part_rows * H, static_cast<uint16_t *>(dh), n)
-                   : launch("cross_entropy_round", round_kernel<Bf16>, grid, 256, 0, s, sums, l.parts, l.part_rows * H, static_cast<uint16_t *>(dh), n);
+        return f16 ? launch("cross_entropy_round", round_kernel<Fp16>, 1, grid, 256, 0, s, sums, l.parts, l.part_rows * H, static_cast<uint16_t *>(dh), n)
+                   : launch("cross_entropy_round", round_kernel<Bf16>, 1, grid, 256, 0, s, sums, l.parts, l.part_rows * H, static_cast<uint16_t *>(dh), n);
     }
     return MOE_OK;
 }
