@@ -648,23 +648,25 @@ def make_adamw_tensors(tensors) -> AdamwTensors:
             if t is None:
                 continue
             want = (n + 255) // 256 * 2 if name == "scales" else n
-            p = _packed(t, f"tensor {i}: {name}", want, kind)
-            if t.numel() != want:
-                raise MoeError(MOE_ERR_INVALID_ARG, f"tensor {i}: {name} must have {want} elements (got {t.numel()})")
-            if p.__class__ is _Host:
+            if t.dtype in _KINDS[kind] and t.numel() == want and t.is_cuda and t.is_contiguous():
+                p = t.data_ptr()
+            else:  # (says what is wrong; a step has hundreds of tensors, and the messages' names take their time)
+                p = _packed(t, f"tensor {i}: {name}", want, kind)
+                if t.numel() != want:
+                    raise MoeError(MOE_ERR_INVALID_ARG, f"tensor {i}: {name} must have {want} elements (got {t.numel()})")
                 host = host or p
-            else:
-                setattr(a, name, p)
+                p = t.data_ptr()
             if want:
-                ranges.append((t.data_ptr(), t.data_ptr() + want * t.element_size(), name != "grad", f"tensor {i}: {name}"))
+                setattr(a, name, p)
+                ranges.append((p, p + want * t.element_size(), name != "grad", i, name))
         a.n, a.param_dtype, a.grad_dtype = n, kinds["param"], kinds["grad"]
         a.lr_factor, a.weight_decay = d.get("lr_factor", 1.0), d.get("weight_decay", 0.0)
-    end = {True: (0, ""), False: (0, "")}  # how far what is written, and what is read, has come
-    for lo, hi, written, name in sorted(ranges):
+    end = {True: (0, 0, ""), False: (0, 0, "")}  # how far what is written, and what is read, has come
+    for lo, hi, written, i, name in sorted(ranges):
         for other in ((True, False) if written else (True,)):
             if lo < end[other][0]:
-                raise MoeError(MOE_ERR_INVALID_ARG, f"{name} overlaps {end[other][1]}")
-        end[written] = max(end[written], (hi, name))
+                raise MoeError(MOE_ERR_INVALID_ARG, "tensor %d: %s overlaps tensor %d: %s" % (i, name, *end[other][1:]))
+        end[written] = max(end[written], (hi, i, name))
     if host:
         raise MoeError(MOE_ERR_INVALID_ARG, host.what)
     return AdamwTensors(array, [dict(d) for d in tensors])

@@ -630,8 +630,7 @@ moe_status launch(const moe_adamw_tensor *tensors, int n, int kind, const Common
     return MOE_OK;
 }
 
-// Whether two of the written ranges param overlap (equal master, m or v pointers come with equal owners or are caught
-// by the binding): sorted by address, unless they are so already.
+// Whether two tensors' params overlap (the same tensor named twice): sorted by address, unless they are so already.
 struct Range {
     uintptr_t a, b;
 };

@@ -746,8 +746,8 @@ typedef struct moe_adamw_options {
  * and grad_scale are read on the device, so that a captured step can be
  * replayed with others.  An element whose g or g^2 is not finite is left as it
  * is, m and v too, and sets *dev_status = MOE_ERR_NONFINITE; a grad_scale of
- * NaN or infinity so leaves every tensor as it is.  Tensors must not overlap;
- * equal param, master, m or v pointers are refused.  beta1 and beta2 in [0, 1),
+ * NaN or infinity so leaves every tensor as it is.  What a step writes must not
+ * overlap anything else of the call; overlapping params are refused.  beta1 and beta2 in [0, 1),
  * eps a normal fp32 number above 0, step >= 1 (a step_dev below 1 counts as 1).
  *
  * States in 8 bits (scales given; all zeros to begin with): a block of 256

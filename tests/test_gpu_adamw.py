@@ -224,3 +224,29 @@ def test_values_of_the_states(moe, off):
     only = torch.empty_like(mv[0])
     m.moe_adamw_states(m.make_adamw_tensors(ds[:1]), m.make_adamw_values([only], None))
     assert torch.equal(only, mv[0])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_one_large_tensor_as_its_pieces(moe, bits):
+    """One tensor of 90 million values, whose CTAs take 16,384 each, and the same in pieces whose CTAs take 2,048: the same bits."""
+    n, piece = 90_000_128, 1 << 24
+    g = torch.Generator(device=DEV).manual_seed(1)
+
+    def make():
+        g.manual_seed(1)
+        d = {"param": torch.randn(n, generator=g, device=DEV).bfloat16(), "grad": torch.randn(n, generator=g, device=DEV).bfloat16()}
+        if bits == 32:
+            d["m"], d["v"] = torch.randn(n, generator=g, device=DEV), torch.rand(n, generator=g, device=DEV)
+        else:
+            d["m"] = torch.randint(0, 126, (n,), generator=g, device=DEV).to(torch.uint8)
+            d["v"] = torch.randint(0, 256, (n,), generator=g, device=DEV).to(torch.uint8)
+            d["scales"] = torch.rand((n + 255) // 256, 2, generator=g, device=DEV)
+        return d
+
+    a, b = make(), make()
+    step([a])
+    for at in range(0, n, piece):
+        end = min(n, at + piece)
+        step([{k: (t[at // 256:(end + 255) // 256] if k == "scales" else t[at:end]) for k, t in b.items()}])
+    for k in a:
+        assert torch.equal(a[k], b[k]), k
