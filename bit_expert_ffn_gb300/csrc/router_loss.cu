@@ -341,6 +341,19 @@ __global__ void __launch_bounds__(FINISH, 1) finish_kernel(const __grid_constant
         red, &slot);
 }
 
+// Four values that this call does not read again.
+template <class A>
+__device__ __forceinline__ void store4_once(typename A::T *p, const float *v)
+{
+    if constexpr (A::kBytes == 4) {
+        __stcs(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
+    } else {
+        typename A::T q[4];
+        A::store4(q, v);
+        __stcs(reinterpret_cast<uint2 *>(p), *reinterpret_cast<const uint2 *>(q));
+    }
+}
+
 struct GradParams {
     const void *logits;
     void *dlogits;
@@ -436,7 +449,7 @@ __global__ void __launch_bounds__(THREADS, NV <= 16 ? 2 : 1) grad_kernel(const _
                     const float4 a = *reinterpret_cast<const float4 *>(extra + c);
                     v[i] += a.x, v[i + 1] += a.y, v[i + 2] += a.z, v[i + 3] += a.w;
                 }
-                A::store4(out + c, v + i);
+                store4_once<A>(out + c, v + i);
             } else {
                 A::store(out + c, p.w ? v[i] + extra[c] : v[i]);
             }
