@@ -9,13 +9,21 @@
 // launch's parameters (up to 32 KB of constant memory), so a step needs no
 // table in device memory; a CTA finds its tensor by bisection of the tensors'
 // first chunks.  A warp takes 256 values at a time, the block of the 8-bit
-// states, so that a block's largest values come from one warp's registers; a
-// lane has two groups of four (16-byte accesses of fp32), or eight single ones
-// where a tensor's pointers are not aligned for that.
+// states, so that a block's largest values come from one warp's registers.  With
+// fp32 states a lane has two groups of four (16-byte accesses), with 8-bit ones
+// eight side by side (32 bytes of fp32; in fours as well 3% more time) and the next
+// block on its way; or eight single ones where a tensor's pointers are not
+// aligned for that.
 //
 // The 8-bit codes are defined by 32-bit arithmetic, each operation rounded:
 // hence the explicit roundings below, where the compiler must not fuse a
-// product with a sum.
+// product with a sum.  (Pairs of fp32 operations in one instruction, mul and add
+// .f32x2, were fused all the same, and brought 1%.)
+//
+// Measured on one GB300: 50 M fp32 values with fp32 states in 192 tensors 207 us
+// (6.8 TB/s: memory); 189 M values, 8-bit states, 16-bit gradient and parameter
+// and an fp32 copy 512 us (5.9 TB/s; 74 instructions a value, two thirds of the
+// issue slots), their states' values in fp32 283 us (6.7 TB/s).
 #include <new>
 
 #include "rows.cuh"
@@ -173,13 +181,15 @@ struct Scalars {
     float scale, shrink, rate, root2;
 };
 
+// 256 values: with fp32 states (kVec: aligned for fours), or, k8, with 8-bit ones, value by value.
 template <bool k8, bool kVec>
 __device__ __forceinline__ void block(const Common &c, const Tensor &t, const Scalars &s, int64_t base, int lane)
 {
     float x[8], g[8], m[8], v[8];
     const void *xp = t.master ? t.master : t.param;
     const int xt = t.master ? (int)MOE_F32 : t.pt;
-    const bool whole = kVec && base + BLOCK <= t.n;  // (a last, short block goes value by value; k8: block8 takes whole ones)
+    static_assert(!(k8 && kVec), "whole, aligned blocks with 8-bit states are block8's");
+    const bool whole = kVec && base + BLOCK <= t.n;  // (a last, short block goes value by value)
     float um = 0.f, ur = 0.f;
     if (k8) {
         const float2 u = *reinterpret_cast<const float2 *>(t.scales + base / BLOCK * 2);
@@ -192,26 +202,15 @@ __device__ __forceinline__ void block(const Common &c, const Tensor &t, const Sc
             const int64_t i = place<true>(base, 4 * j, lane);
             rg[j] = raw4(t.grad, i, t.gt);
             rx[j] = raw4(xp, i, xt);
-            if (k8) {
-                rm[j].x = *reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(t.m) + i);
-                rv[j].x = *reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(t.v) + i);
-            } else {
-                rm[j] = raw4(t.m, i, MOE_F32);
-                rv[j] = raw4(t.v, i, MOE_F32);
-            }
+            rm[j] = raw4(t.m, i, MOE_F32);
+            rv[j] = raw4(t.v, i, MOE_F32);
         }
 #pragma unroll
         for (int j = 0; j < 2; j++) {
             unpack4(rg[j], t.gt, g + 4 * j);
             unpack4(rx[j], xt, x + 4 * j);
-            if (k8) {
-                e4m3_values(rm[j].x, m + 4 * j);
-#pragma unroll
-                for (int i = 0; i < 4; i++) v[4 * j + i] = root_value(rv[j].x >> (8 * i) & 255u);
-            } else {
-                unpack4(rm[j], MOE_F32, m + 4 * j);
-                unpack4(rv[j], MOE_F32, v + 4 * j);
-            }
+            unpack4(rm[j], MOE_F32, m + 4 * j);
+            unpack4(rv[j], MOE_F32, v + 4 * j);
         }
     } else {  // (all loads before the first use)
         uint32_t rg[8], rx[8], rm[8], rv[8];
@@ -293,16 +292,8 @@ __device__ __forceinline__ void block(const Common &c, const Tensor &t, const Sc
             const int64_t i = place<true>(base, 4 * j, lane);
             if (t.master) F32::store4(t.master + i, x + 4 * j);
             store4(t.param, i, t.pt, x + 4 * j);
-            if (k8) {
-                uint32_t q = 0;
-#pragma unroll
-                for (int e = 0; e < 4; e++) q |= (r[4 * j + e] > 0.f ? root_code(r[4 * j + e]) : 0u) << (8 * e);
-                *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(t.m) + i) = e4m3_codes(m + 4 * j);
-                *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(t.v) + i) = q;
-            } else {
-                F32::store4(static_cast<float *>(t.m) + i, m + 4 * j);
-                F32::store4(static_cast<float *>(t.v) + i, v + 4 * j);
-            }
+            F32::store4(static_cast<float *>(t.m) + i, m + 4 * j);
+            F32::store4(static_cast<float *>(t.v) + i, v + 4 * j);
         }
     } else {
 #pragma unroll
@@ -323,19 +314,42 @@ __device__ __forceinline__ void block(const Common &c, const Tensor &t, const Sc
     }
 }
 
-// 256 values with 8-bit states, whole and aligned, as a rule: false, and nothing done, when the block wants block()'s
-// exact steps: a gradient that is not finite, roots so small that the fast root of a subnormal v, 0, would not get the same
-// code (below 2^-46 of the largest all do: code 1), or a root next to a border between two codes.  The fast root is within 2^-23 of the correctly rounded one, its product with the block's
-// factor within 3 last places: eight of 2^19 to either side of a border are left to the exact steps, so
-// that the codes are theirs in every case (8 blocks of 1,000).  The largest root is the rounded root of the
-// largest v, since rounding keeps the order.
-// Four values of a type as they lie, and in fp32.
+// Eight values of a type side by side as they lie (32 or 16 bytes), and in fp32.
 template <class A>
-struct Four {
-    using Raw = std::conditional_t<A::kBytes == 4, uint4, uint2>;
-    __device__ static Raw raw(const void *p, int64_t i) { return *reinterpret_cast<const Raw *>(static_cast<const typename A::T *>(p) + i); }
-    __device__ static void unpack(const Raw &q, float *v) { A::load4(reinterpret_cast<const typename A::T *>(&q), v); }
+struct Eight {
+    uint32_t w[A::kBytes * 2];
+
+    __device__ void load(const typename A::T *p)
+    {
+        if constexpr (A::kBytes == 4) {
+            asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                         : "l"(p));
+        } else {
+            const uint4 q = *reinterpret_cast<const uint4 *>(p);
+            w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+        }
+    }
+    __device__ void unpack(float (&v)[8]) const
+    {
+        if constexpr (A::kBytes == 4) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i] = __uint_as_float(w[i]);
+        } else {
+            A::unpack8(make_uint4(w[0], w[1], w[2], w[3]), v);
+        }
+    }
 };
+
+template <class A>
+__device__ __forceinline__ void store_eight(typename A::T *p, const float (&v)[8])
+{
+    if constexpr (A::kBytes == 4)
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+                     "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                     : "memory");
+    else A::store8(p, v);
+}
 
 // A lane's places in a chunk's tensors; blocks are `o` values further on.
 template <class G, class X>
@@ -348,57 +362,57 @@ struct At {
     int pt;
 
     __device__ At(const Tensor &t, int64_t i, int lane)
-        : g(static_cast<const typename G::T *>(t.grad) + i + lane * 4), m(static_cast<uint8_t *>(t.m) + i + lane * 4),
-          v(static_cast<uint8_t *>(t.v) + i + lane * 4), scales(reinterpret_cast<float2 *>(t.scales) + i / BLOCK), pt(t.pt)
+        : g(static_cast<const typename G::T *>(t.grad) + i + lane * 8), m(static_cast<uint8_t *>(t.m) + i + lane * 8),
+          v(static_cast<uint8_t *>(t.v) + i + lane * 8), scales(reinterpret_cast<float2 *>(t.scales) + i / BLOCK), pt(t.pt)
     {
-        x = static_cast<typename X::T *>(t.master ? static_cast<void *>(t.master) : t.param) + i + lane * 4;
-        p = t.master ? static_cast<char *>(t.param) + (i + lane * 4) * (pt == MOE_F32 ? 4 : 2) : nullptr;
+        x = static_cast<typename X::T *>(t.master ? static_cast<void *>(t.master) : t.param) + i + lane * 8;
+        p = t.master ? static_cast<char *>(t.param) + (i + lane * 8) * (pt == MOE_F32 ? 4 : 2) : nullptr;
     }
 };
 
 // What a lane loads of a block.
 template <class G, class X>
 struct Held8 {
-    typename Four<G>::Raw g[2];
-    typename Four<X>::Raw x[2];
-    uint32_t m[2], v[2];
+    Eight<G> g;
+    Eight<X> x;
+    uint2 m, v;
     float2 u;
 
     __device__ void load(const At<G, X> &at, int o)
     {
-#pragma unroll
-        for (int j = 0; j < 2; j++) {
-            g[j] = Four<G>::raw(at.g + o, 128 * j);
-            x[j] = Four<X>::raw(at.x + o, 128 * j);
-            m[j] = *reinterpret_cast<const uint32_t *>(at.m + o + 128 * j);
-            v[j] = *reinterpret_cast<const uint32_t *>(at.v + o + 128 * j);
-        }
+        g.load(at.g + o);
+        x.load(at.x + o);
+        m = *reinterpret_cast<const uint2 *>(at.m + o);
+        v = *reinterpret_cast<const uint2 *>(at.v + o);
         u = at.scales[o / BLOCK];
     }
 };
 
+// 256 values with 8-bit states, whole and aligned.  False, and nothing done, when the block wants block()'s exact steps: a
+// gradient that is not finite, roots so small that the fast root of a subnormal v, 0, would not get the same code (below
+// 2^-46 of the largest all do: code 1), or a root next to a border between two codes.  The fast root is within 2^-23 of
+// the correctly rounded one, its product with the block's factor within 3 last places: eight of 2^19 to either side of a
+// border are left to the exact steps (8 blocks of 1,000), so that the codes are theirs in every case.  The largest root
+// is the rounded root of the largest v, since rounding keeps the order.
 template <class G, class X>
 __device__ __forceinline__ bool block8(const Common &c, const At<G, X> &at, const Scalars &s, int o, int lane, const Held8<G, X> &raw)
 {
     float x[8], m[8], v[8], r[8];
     const float2 u = raw.u;
-    float odd = 0.f, top_m = 0.f, top_v = 0.f;
+    float odd = 0.f, top_m = 0.f, top_v = 0.f, g[8];
+    raw.g.unpack(g);
+    raw.x.unpack(x);
+    e4m3_values(raw.m.x, m);
+    e4m3_values(raw.m.y, m + 4);
 #pragma unroll
-    for (int j = 0; j < 2; j++) {
-        float g[4];
-        Four<G>::unpack(raw.g[j], g);
-        Four<X>::unpack(raw.x[j], x + 4 * j);
-        e4m3_values(raw.m[j], m + 4 * j);
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            const int i = 4 * j + e;
-            const float gi = g[e] * s.scale, g2 = __fmul_rn(gi, gi), root = __fmul_rn(root_value(raw.v[j] >> (8 * e) & 255u), u.y);
-            odd = fmaf(g2, 0.f, odd);  // NaN when a square is not finite
-            m[i] = __fadd_rn(__fmul_rn(__fmul_rn(m[i], u.x), c.b1), __fmul_rn(gi, c.o1));
-            v[i] = __fadd_rn(__fmul_rn(__fmul_rn(root, root), c.b2), __fmul_rn(g2, c.o2));
-            top_m = fmaxf(top_m, fabsf(m[i]));
-            top_v = fmaxf(top_v, v[i]);
-        }
+    for (int i = 0; i < 8; i++) {
+        const uint32_t code = (i < 4 ? raw.v.x : raw.v.y) >> (8 * (i & 3)) & 255u;
+        const float gi = g[i] * s.scale, g2 = __fmul_rn(gi, gi), root = __fmul_rn(root_value(code), u.y);
+        odd = fmaf(g2, 0.f, odd);  // NaN when a square is not finite
+        m[i] = __fadd_rn(__fmul_rn(__fmul_rn(m[i], u.x), c.b1), __fmul_rn(gi, c.o1));
+        v[i] = __fadd_rn(__fmul_rn(__fmul_rn(root, root), c.b2), __fmul_rn(g2, c.o2));
+        top_m = fmaxf(top_m, fabsf(m[i]));
+        top_v = fmaxf(top_v, v[i]);
     }
     top_m = warp_top(top_m);
     top_v = warp_top(top_v);
@@ -413,7 +427,7 @@ __device__ __forceinline__ bool block8(const Common &c, const At<G, X> &at, cons
     uint32_t close = ~0u, codes[2];
 #pragma unroll
     for (int j = 0; j < 2; j++) {
-        codes[j] = 0;
+        uint32_t code[4];
 #pragma unroll
         for (int e = 0; e < 4; e++) {
             const int i = 4 * j + e;
@@ -421,8 +435,9 @@ __device__ __forceinline__ bool block8(const Common &c, const At<G, X> &at, cons
             const uint32_t b = __float_as_uint(fmaxf(__fmul_rn(r[i], ir), 17.f / 524288.f));  // code 1 at least
             close = min(close, (b + (8u - 0x40000u)) & 0x7FFFFu);
             const uint32_t near = (b + (0x40000u - (112u << 23))) >> 19;  // (no ties here: they are close)
-            codes[j] |= (v[i] > 0.f ? near : 0u) << (8 * e);
+            code[e] = min(near, __float_as_uint(v[i]));  // (0 for a v of 0, whose root counted as code 1's)
         }
+        codes[j] = __byte_perm(__byte_perm(code[0], code[1], 0x0040), __byte_perm(code[2], code[3], 0x0040), 0x5410);
     }
     if (__any_sync(0xffffffffu, close <= 16u)) return false;
     if (lane == 0) at.scales[o / BLOCK] = held;
@@ -436,11 +451,15 @@ __device__ __forceinline__ bool block8(const Common &c, const At<G, X> &at, cons
             x[i] = fmaf(x[i], s.shrink, -(m[i] * s.rate * inv));
             m[i] = __fmul_rn(m[i], im);
         }
-        X::store4(at.x + o + 128 * j, x + 4 * j);
-        if (X::kBytes == 4 && at.p) store4(at.p, o + 128 * j, at.pt, x + 4 * j);
-        *reinterpret_cast<uint32_t *>(at.m + o + 128 * j) = e4m3_codes(m + 4 * j);
-        *reinterpret_cast<uint32_t *>(at.v + o + 128 * j) = codes[j];
     }
+    store_eight<X>(at.x + o, x);
+    if (X::kBytes == 4 && at.p) {
+        if (at.pt == MOE_F32) store_eight<F32>(static_cast<float *>(at.p) + o, x);
+        else if (at.pt == MOE_BF16) Bf16::store8(static_cast<uint16_t *>(at.p) + o, x);
+        else Fp16::store8(static_cast<uint16_t *>(at.p) + o, x);
+    }
+    *reinterpret_cast<uint2 *>(at.m + o) = make_uint2(e4m3_codes(m), e4m3_codes(m + 4));
+    *reinterpret_cast<uint2 *>(at.v + o) = make_uint2(codes[0], codes[1]);
     return true;
 }
 
@@ -706,8 +725,10 @@ extern "C" moe_status moe_adamw_step(const moe_adamw_tensor *tensors, int n_tens
     const cudaStream_t s = to_cuda(stream);
     auto one = [&](int i, Tensor &t) {
         const moe_adamw_tensor &a = tensors[i];
-        t.vec = t.vec && aligned_to(a.param, 4 * dtype_bytes((moe_dtype)a.param_dtype)) &&
-                aligned_to(a.grad, 4 * dtype_bytes((moe_dtype)a.grad_dtype)) && aligned16(a.master);
+        const int n = a.scales ? 8 : 4;  // values that a lane takes at once
+        t.vec = aligned_to(a.m, a.scales ? 8 : 16) && aligned_to(a.v, a.scales ? 8 : 16) &&
+                aligned_to(a.param, n * dtype_bytes((moe_dtype)a.param_dtype)) &&
+                aligned_to(a.grad, n * dtype_bytes((moe_dtype)a.grad_dtype)) && aligned_to(a.master, n * 4);
     };
     bool kinds[2] = {false, false};
     for (int i = 0; i < n_tensors; i++)
