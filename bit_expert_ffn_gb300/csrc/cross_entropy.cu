@@ -30,10 +30,10 @@
 //
 // Measured on one GB300 (bf16, H = 2,048): 4,096 tokens against 65,536 words 519
 // us (2.1 PFLOP/s; by single CTAs 563), with both gradients 2.44 ms (1.8 PFLOP/s,
-// power-bound; by single CTAs 2.69); four tokens against 100,003 words 80 us (410
-// MB of W, 5.1 TB/s); 1,111 tokens, H = 1,056, 8,191 words with gradients 70 us.
-// Tried without gain: W on its way to L2 in boxes of 512 bytes a row (four tokens
-// 79 -> 89 us), results straight from the registers, the next columns loaded from
+// power-bound; by single CTAs 2.69); four tokens against 100,003 words 69 us (410
+// MB of W, 6.0 TB/s); 1,111 tokens, H = 1,056, 8,191 words with gradients 70 us.
+// Tried without gain: W on its way to L2 in boxes of 512 bytes a row (four tokens,
+// 10 us more), results straight from the registers, the next columns loaded from
 // tensor memory ahead, four blocks of results on their way instead of two.
 //
 // Every wait is bounded: after about 2 s the CTA records MOE_ERR_TIMEOUT and
@@ -79,6 +79,10 @@ struct Job {
     int b_y0, out_y0;          // added to B's and the output's row coordinates
     int part_rows;             // rows of the output from one part to the next
     int add, out_f32;
+    // Rows of the operands' boxes: as many as there are tokens, where they are few.  (Rows past the end that TMA has to fill
+    // with zeros take their time: four tokens against 100,003 x 2,048 82 us with boxes of 128, 69 with boxes of 8.)  Past
+    // a box of A with K inner lies what was there: rows of the result that nobody takes.
+    int a_rows, b_rows;
 };
 
 // Which items a CTA or pair takes: of the first job every G-th (G of them in all), then of the
@@ -328,7 +332,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
         for (int i = 0; ok && item_of<C>(p, i, m); i++) {
             const Job &g = p.job[m.j];
             const int half = g.bn / C, boxes = (half + 63) / 64;
-            const uint32_t bytes = A_BYTES + (K == PROD ? boxes * (BK * 128) : half * 128);
+            const uint32_t bytes = (K == PROD && g.mn_a ? ROWS / 64 : 1) * g.a_rows * 128 + (K == PROD ? boxes * g.b_rows : half) * 128;
             for (int kb = m.kb0; kb < m.kb1; kb++, it++) {
                 if (it >= STAGES) ok = warp_wait(S, &S.empty[s], phase);
                 if (!ok) break;
@@ -663,6 +667,9 @@ static int piece_columns(int T, int V)
 
 static int round_up(int n, int b) { return tiles(n, b) * b; }
 
+// Rows of a box of tokens: a single CTA's first tile has them all, where there are few.
+static int box_rows(int T, int C) { return C == 1 && T < ROWS ? round_up(T, 8) : ROWS; }
+
 // Columns of a tile: equal ones over all n.
 static int tile_columns(int n) { return round_up(tiles(n, tiles(n, BN)), 32); }
 
@@ -852,12 +859,12 @@ extern "C" moe_status moe_cross_entropy(const void *h, moe_dtype dtype, int T, i
     Maps maps = {};
     const Cut cut = cut_logits(T, V, sm_count());
     const int n_tiles = tiles(V, cut.bn);
-    p.job[0] = {tiles(T, ROWS * cut.C), n_tiles, cut.bn, H, 1, 0, 0, 0, 0, 0, 0};
+    p.job[0] = {tiles(T, ROWS * cut.C), n_tiles, cut.bn, H, 1, 0, 0, 0, 0, 0, 0, box_rows(T, cut.C), 0};
     p.idesc = tc::idesc_f16_f32(ROWS * cut.C, 0, dtype == MOE_BF16);
     p.T = T, p.V = V, p.labels = labels, p.status = dev_status;
     p.label_z = static_cast<float *>(ws);
     p.stats = reinterpret_cast<float2 *>(static_cast<char *>(ws) + align256((size_t)T * 4));
-    st = make_tmap_2d(&maps.a[0], h, map_type(dtype), 2, T, H, BK, ROWS);
+    st = make_tmap_2d(&maps.a[0], h, map_type(dtype), 2, T, H, BK, box_rows(T, cut.C));
     if (st == MOE_OK) st = make_tmap_2d(&maps.b[0], w, map_type(dtype), 2, V, H, BK, cut.bn / cut.C);
     if (st != MOE_OK) return st;
     const cudaStream_t s = to_cuda(stream);
@@ -915,15 +922,16 @@ extern "C" moe_status moe_cross_entropy_backward(const void *h, moe_dtype dtype,
     gp.status = pp.status = dev_status;
     gp.f16 = pp.f16 = f16;
     const bool direct = l.pieces == 1 && l.parts == 1;  // dh leaves as it is: no sums of pieces or parts
+    const int k_rows = std::min(BK, round_up(T, 16));   // of a step over the tokens
     const auto half = CU_TENSOR_MAP_SWIZZLE_64B;        // boxes of 32 16-bit columns
-    st = make_tmap_2d(&gm.a[0], h, map_type(dtype), 2, T, H, BK, ROWS);
+    st = make_tmap_2d(&gm.a[0], h, map_type(dtype), 2, T, H, BK, box_rows(T, cut.C));
     if (st == MOE_OK) st = make_tmap_2d(&gm.b[0], w, map_type(dtype), 2, V, H, BK, cut.bn / cut.C);
     if (st == MOE_OK) st = make_tmap_2d(&gm.out[0], d, map_type(dtype), 2, T, l.columns, 32, 32, half);
     CUtensorMap d_k, d_m, w_n, h_n, out_h, out_w;
-    if (st == MOE_OK) st = make_tmap_2d(&d_k, d, map_type(dtype), 2, T, l.columns, BK, ROWS);
-    if (st == MOE_OK) st = make_tmap_2d(&d_m, d, map_type(dtype), 2, T, l.columns, 64, BK);
+    if (st == MOE_OK) st = make_tmap_2d(&d_k, d, map_type(dtype), 2, T, l.columns, BK, box_rows(T, l.C));
+    if (st == MOE_OK) st = make_tmap_2d(&d_m, d, map_type(dtype), 2, T, l.columns, 64, k_rows);
     if (st == MOE_OK) st = make_tmap_2d(&w_n, w, map_type(dtype), 2, V, H, 64, BK);
-    if (st == MOE_OK) st = make_tmap_2d(&h_n, h, map_type(dtype), 2, T, H, 64, BK);
+    if (st == MOE_OK) st = make_tmap_2d(&h_n, h, map_type(dtype), 2, T, H, 64, k_rows);
     if (st == MOE_OK && dh)
         st = direct ? make_tmap_2d(&out_h, dh, map_type(dtype), 2, T, H, 32, 32, half)
                     : make_tmap_2d(&out_h, sums, map_type(MOE_F32), 4, l.parts * l.part_rows, H, 32, 32);
@@ -936,17 +944,17 @@ extern "C" moe_status moe_cross_entropy_backward(const void *h, moe_dtype dtype,
         const int v0 = i * l.columns, n = std::min(l.columns, V - v0);
         gp.v0 = v0;
         gp.V = n;
-        gp.job[0] = {tiles(T, ROWS * cut.C), tiles(n, cut.bn), cut.bn, H, 1, 0, v0, 0, 0, 0, 0};
+        gp.job[0] = {tiles(T, ROWS * cut.C), tiles(n, cut.bn), cut.bn, H, 1, 0, v0, 0, 0, 0, 0, box_rows(T, cut.C), 0};
         st = product<GRAD>(cut.C, gp, gm, s);
         if (st != MOE_OK) return st;
         int j = 0;
         if (dh) {
-            pp.job[j] = {tiles(T, ROWS * l.C), nt, bn, n, l.parts, 0, v0, 0, (int)l.part_rows, !direct && i > 0, !direct};
+            pp.job[j] = {tiles(T, ROWS * l.C), nt, bn, n, l.parts, 0, v0, 0, (int)l.part_rows, !direct && i > 0, !direct, box_rows(T, l.C), BK};
             pm.a[j] = d_k, pm.b[j] = w_n, pm.out[j] = out_h;
             j++;
         }
         if (dw) {
-            pp.job[j] = {tiles(n, ROWS * l.C), nt, bn, T, 1, 1, 0, v0, 0, accumulate != 0, dw_dtype == MOE_F32};
+            pp.job[j] = {tiles(n, ROWS * l.C), nt, bn, T, 1, 1, 0, v0, 0, accumulate != 0, dw_dtype == MOE_F32, k_rows, k_rows};
             pm.a[j] = d_m, pm.b[j] = h_n, pm.out[j] = out_w;
             j++;
         }

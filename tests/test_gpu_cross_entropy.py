@@ -44,7 +44,8 @@ def backward(h, w, labels, dtype, lse, dloss, dlse=None, want=(True, True), dw_d
 
 
 SIZES = [(1, 8, 1), (1, 64, 7), (2, 72, 255), (3, 256, 256), (31, 264, 257), (4, 2048, 5003), (129, 64, 1000), (128, 128, 512),
-         (300, 1056, 4099), (257, 8, 70), (513, 520, 2049), (1111, 200, 3001)]
+         (300, 1056, 4099), (257, 8, 70), (513, 520, 2049), (1111, 200, 3001),
+         (16, 136, 5000), (17, 64, 4865), (33, 320, 20011), (63, 72, 9001), (64, 128, 31), (65, 128, 5001)]
 
 
 @pytest.mark.parametrize("dtype", [m.MOE_BF16, m.MOE_F16])
