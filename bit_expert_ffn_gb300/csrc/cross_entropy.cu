@@ -141,16 +141,24 @@ __device__ __forceinline__ bool item_of(const Params &p, int i, Item &it)
         if (t >= p.items1) return false;
     }
     const Job &g = p.job[it.j];
-    const int whole = g.m_tiles * g.n_tiles;
-    it.part = t / whole;
-    t -= it.part * whole;
-    const int band = t / (BAND * g.n_tiles), m0 = band * BAND, rows = min(BAND, g.m_tiles - m0);
-    t -= band * BAND * g.n_tiles;
-    it.n = t / rows;
+    it.part = it.kb0 = 0;
+    it.kb1 = (g.K + BK - 1) / BK;
+    if (g.parts > 1) {  // (quotients take some hundred cycles each, of every warp and tile: only where there is need)
+        const uint32_t whole = g.m_tiles * g.n_tiles, nk = it.kb1;
+        it.part = (uint32_t)t / whole;
+        t -= it.part * whole;
+        it.kb0 = nk * it.part / (uint32_t)g.parts;
+        it.kb1 = nk * (it.part + 1) / (uint32_t)g.parts;
+    }
+    int m0 = 0, rows = g.m_tiles;
+    if (rows > BAND) {
+        const uint32_t band = (uint32_t)t / (uint32_t)(BAND * g.n_tiles);
+        m0 = band * BAND;
+        rows = min(BAND, g.m_tiles - m0);
+        t -= m0 * g.n_tiles;
+    }
+    it.n = (uint32_t)t / (uint32_t)rows;
     it.m = m0 + t - it.n * rows;
-    const int nk = (g.K + BK - 1) / BK;
-    it.kb0 = (int)((int64_t)nk * it.part / g.parts);
-    it.kb1 = (int)((int64_t)nk * (it.part + 1) / g.parts);
     return true;
 }
 
