@@ -107,6 +107,12 @@ struct Maps {
     CUtensorMap a[2], b[2], out[2];
 };
 
+// What a row of the logits' gradient needs.
+struct Row {
+    int label;
+    float lse, dloss, dlse;
+};
+
 struct Shared {
     uint64_t full[MAX_STAGES], empty[MAX_STAGES];
     uint64_t acc_full[2], acc_empty[2];
@@ -456,23 +462,40 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
         }
         const float up = K == PROD ? (p.f16 ? top / F16_ROOM : top) : 0.f;
         const float down = K == GRAD && top > 0.f ? (p.f16 ? F16_ROOM : 1.f) : 0.f;
-        Item m;
-        for (int i = 0; item_of<C>(p, i, m); i++) {
+        // what a row needs comes while the tile before is on its way out
+        Item m, next;
+        Row in = {}, ahead = {};
+        auto row_of = [&](const Item &m) { return m.m * BM + rank * ROWS + q * 32 + lane; };
+        auto fetch = [&](const Item &m, Row &r) {
+            const int row = row_of(m);
+            r.label = -1;
+            if (K == PROD || row >= p.T) return;
+            r.label = p.labels[row];
+            if (K == GRAD) {
+                r.lse = p.lse[row];
+                r.dloss = p.dloss[row];
+                if (p.dlse) r.dlse = p.dlse[row];
+            }
+        };
+        bool more = item_of<C>(p, 0, m);
+        if (more) fetch(m, in);
+        for (int i = 1; more; i++, m = next, in = ahead) {
+            more = item_of<C>(p, i, next);
+            if (more) fetch(next, ahead);
             const Job &g = p.job[m.j];
             if (m.kb0 == m.kb1) continue;
             const int acc = j & 1, v = j >> 1;
             j++;
-            const int row = m.m * BM + rank * ROWS + q * 32 + lane, n0 = m.n * g.bn;
-            int label = -1;
+            const int row = row_of(m), n0 = m.n * g.bn;
+            int label = in.label;
             float lse = 0.f, nl = 0.f, a = 0.f, b = 0.f;
-            if (K != PROD && row < p.T) label = p.labels[row];
             if (K == GRAD && row < p.T) {
                 const bool there = label >= 0 && label < p.all;
-                b = there ? p.dloss[row] : 0.f;
-                a = b + (p.dlse ? p.dlse[row] : 0.f);
+                b = there ? in.dloss : 0.f;
+                a = b + (p.dlse ? in.dlse : 0.f);
                 a = down > 0.f ? a / top * down : 0.f;
                 b = down > 0.f ? b / top * down : 0.f;
-                lse = p.lse[row];
+                lse = in.lse;
                 nl = -lse * LOG2E;
                 if (fabsf(lse) < FUSED) a *= ex2(-fmaf(lse, LOG2E, nl));  // (what the product's rounding left out)
                 label -= p.v0;
