@@ -44,7 +44,7 @@ DLOSS = (0.3, 0.07)
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 512, 10), (2, 2, 2), (7, 61, 4), (32, 512, 10), (33, 100, 3), (129, 128, 16),
-                                   (300, 256, 8), (1024, 60, 4), (1025, 64, 6), (4099, 513, 10), (2500, 1024, 16), (1500, 1021, 1)])
+                                   (300, 256, 8), (384, 1024, 2), (385, 512, 10), (1024, 60, 4), (1025, 64, 6), (4099, 513, 10), (2500, 1024, 16), (1500, 1021, 1)])
 def test_sizes(moe, T, E, k, dtype):
     logits, ids, w, dw = inputs(T, E, k, dtype, T)
     d = torch.tensor(DLOSS, device=DEV)

@@ -38,7 +38,7 @@ def test_router_loss():
                      (dict(counts=A + 1), "aligned"), (dict(dev_status=A + 2), "aligned")):
         refused(BAD, word, f, **loss(**kw))
     need = m.moe_router_loss_workspace_size(5000, 8)
-    assert need > 0 and m.moe_router_loss_workspace_size(1024, 1024) == 0
+    assert need > 0 and m.moe_router_loss_workspace_size(384, 1024) == 0
     refused(m.MOE_ERR_WORKSPACE, str(need), f, **loss(T=5000), ws=A, ws_bytes=need - 1)
     refused(m.MOE_ERR_WORKSPACE, str(need), f, **loss(T=5000))
     refused(BAD, "16-byte", f, **loss(T=5000), ws=A + 4, ws_bytes=need)
