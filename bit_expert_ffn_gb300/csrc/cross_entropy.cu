@@ -63,7 +63,7 @@ struct Tile {
 constexpr int MAX_STAGES = 6;
 constexpr int EPI_WARP0 = 2, EPI_WARPS = 8;  // two per quarter of the lanes: every other 32 columns each
 constexpr int THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
-constexpr int OUT_BYTES = 32 * 128;  // a warp's 32 rows of 32 values on their way out, two in turn
+constexpr int OUT_BYTES = 32 * 128;  // a warp's 32 rows of 32 fp32 values on their way out, or two blocks of 16-bit ones in turn
 constexpr size_t SMEM = 192 * 1024 + EPI_WARPS * OUT_BYTES + 1024;
 constexpr int BAND_ROWS = 4096;  // rows that pass over the columns together
 constexpr unsigned long long kWaitNs = 2000000000ull;
