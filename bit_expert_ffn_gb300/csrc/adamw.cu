@@ -22,8 +22,8 @@
 //
 // Measured on one GB300: 50 M fp32 values with fp32 states in 192 tensors 207 us
 // (6.8 TB/s: memory); 189 M values, 8-bit states, 16-bit gradient and parameter
-// and an fp32 copy 512 us (5.9 TB/s; 74 instructions a value, two thirds of the
-// issue slots), their states' values in fp32 283 us (6.7 TB/s).
+// and an fp32 copy 490 us (6.2 TB/s; some 70 instructions a value, 60% of the issue
+// slots), their states' values in fp32 283 us (6.7 TB/s).
 #include <new>
 
 #include "rows.cuh"
@@ -179,6 +179,7 @@ __device__ __forceinline__ void load8(const void *p, int64_t base, int64_t left,
 
 struct Scalars {
     float scale, shrink, rate, root2;
+    float root2_rate, eps_rate;  // root2 and eps over the rate (a product less a value); a rate of 0: 0 and infinity
 };
 
 // 256 values: with fp32 states (kVec: aligned for fours), or, k8, with 8-bit ones, value by value.
@@ -401,13 +402,17 @@ __device__ __forceinline__ bool block8(const Common &c, const At<G, X> &at, cons
     const float2 u = raw.u;
     float odd = 0.f, top_m = 0.f, top_v = 0.f, g[8];
     raw.g.unpack(g);
+    if (c.grad_scale) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) g[i] *= s.scale;
+    }
     raw.x.unpack(x);
     e4m3_values(raw.m.x, m);
     e4m3_values(raw.m.y, m + 4);
 #pragma unroll
     for (int i = 0; i < 8; i++) {
         const uint32_t code = (i < 4 ? raw.v.x : raw.v.y) >> (8 * (i & 3)) & 255u;
-        const float gi = g[i] * s.scale, g2 = __fmul_rn(gi, gi), root = __fmul_rn(root_value(code), u.y);
+        const float gi = g[i], g2 = __fmul_rn(gi, gi), root = __fmul_rn(root_value(code), u.y);
         odd = fmaf(g2, 0.f, odd);  // NaN when a square is not finite
         m[i] = __fadd_rn(__fmul_rn(__fmul_rn(m[i], u.x), c.b1), __fmul_rn(gi, c.o1));
         v[i] = __fadd_rn(__fmul_rn(__fmul_rn(root, root), c.b2), __fmul_rn(g2, c.o2));
@@ -433,13 +438,13 @@ __device__ __forceinline__ bool block8(const Common &c, const At<G, X> &at, cons
             const int i = 4 * j + e;
             asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r[i]) : "f"(v[i]));
             const uint32_t b = __float_as_uint(fmaxf(__fmul_rn(r[i], ir), 17.f / 524288.f));  // code 1 at least
-            close = min(close, (b + (8u - 0x40000u)) & 0x7FFFFu);
-            const uint32_t near = (b + (0x40000u - (112u << 23))) >> 19;  // (no ties here: they are close)
-            code[e] = min(near, __float_as_uint(v[i]));  // (0 for a v of 0, whose root counted as code 1's)
+            const uint32_t near = b + (0x40000u - (112u << 23));  // its code in the upper bits (no ties here: they are close)
+            close = min(close, near * 8192u + (8u << 13));        // how far its lower 19 bits are from -8, as the upper ones
+            code[e] = min(near >> 19, __float_as_uint(v[i]));  // (0 for a v of 0, whose root counted as code 1's)
         }
         codes[j] = __byte_perm(__byte_perm(code[0], code[1], 0x0040), __byte_perm(code[2], code[3], 0x0040), 0x5410);
     }
-    if (__any_sync(0xffffffffu, close <= 16u)) return false;
+    if (__any_sync(0xffffffffu, close <= 16u << 13)) return false;
     if (lane == 0) at.scales[o / BLOCK] = held;
 #pragma unroll
     for (int j = 0; j < 2; j++) {
@@ -447,8 +452,8 @@ __device__ __forceinline__ bool block8(const Common &c, const At<G, X> &at, cons
         for (int e = 0; e < 4; e++) {
             const int i = 4 * j + e;
             float inv;
-            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(r[i], s.root2, c.eps)));
-            x[i] = fmaf(x[i], s.shrink, -(m[i] * s.rate * inv));
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(r[i], s.root2_rate, s.eps_rate)));
+            x[i] = fmaf(x[i], s.shrink, -(m[i] * inv));
             m[i] = __fmul_rn(m[i], im);
         }
     }
@@ -509,6 +514,9 @@ __global__ void __launch_bounds__(THREADS, 3) step_kernel(const __grid_constant_
     lr *= t.lr_factor;
     s.rate = lr * rate1;
     s.shrink = 1.f - lr * t.decay;
+    const bool moves = fabsf(s.rate) >= 1e-35f;  // (below that the quotients could leave fp32)
+    s.root2_rate = moves ? s.root2 / s.rate : 0.f;
+    s.eps_rate = moves ? c.eps / s.rate : INFINITY;
     const int lane = lane_id();
     const int64_t begin = (int64_t)(blockIdx.x - p.first[which]) * c.chunk, end = min(begin + c.chunk, t.n);
     const int64_t first = begin + warp_id() * BLOCK;

@@ -175,6 +175,22 @@ def test_zero_tiny_and_huge_states(moe, bits):
     verify(d, want)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("lr", [0.0, 1e-38, 1e-30, -1e-3, 100.0])
+def test_rates_of_any_size(moe, bits, lr):
+    d = tensor(5000, 8, T32, T32, False, bits, weight_decay=0.01)
+    if bits == 32:
+        d["m"][:256].zero_(), d["v"][:256].zero_()
+    else:
+        d["scales"][0].zero_()
+    d["grad"][:256].zero_()  # 0 / eps
+    want = expected(d, lr=lr)
+    before = d["param"].clone()
+    step([d], lr=lr)
+    verify(d, want)
+    assert lr != 0 or torch.equal(d["param"], before)
+
+
 def test_scalars_on_the_device_and_a_replayed_step(moe):
     ds = [tensor(5000, 6, BF, BF, True, 8, weight_decay=0.1), tensor(777, 7, T32, T32, False, 32, lr_factor=0.5)]
     lr = torch.tensor([1.0], device=DEV)
