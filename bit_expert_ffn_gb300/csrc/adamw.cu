@@ -400,7 +400,8 @@ __device__ __forceinline__ bool block8(const Common &c, const At<G, X> &at, cons
 {
     float x[8], m[8], v[8], r[8];
     const float2 u = raw.u;
-    float odd = 0.f, top_m = 0.f, top_v = 0.f, g[8];
+    float top_m = 0.f, g[8];
+    uint32_t most = 0;  // the largest v's bits (of what is not negative, bits are in order; a NaN's are above all)
     raw.g.unpack(g);
     if (c.grad_scale) {
 #pragma unroll
@@ -413,17 +414,18 @@ __device__ __forceinline__ bool block8(const Common &c, const At<G, X> &at, cons
     for (int i = 0; i < 8; i++) {
         const uint32_t code = (i < 4 ? raw.v.x : raw.v.y) >> (8 * (i & 3)) & 255u;
         const float gi = g[i], g2 = __fmul_rn(gi, gi), root = __fmul_rn(root_value(code), u.y);
-        odd = fmaf(g2, 0.f, odd);  // NaN when a square is not finite
         m[i] = __fadd_rn(__fmul_rn(__fmul_rn(m[i], u.x), c.b1), __fmul_rn(gi, c.o1));
         v[i] = __fadd_rn(__fmul_rn(__fmul_rn(root, root), c.b2), __fmul_rn(g2, c.o2));
         top_m = fmaxf(top_m, fabsf(m[i]));
-        top_v = fmaxf(top_v, v[i]);
+        most = max(most, __float_as_uint(v[i]));
     }
     top_m = warp_top(top_m);
-    top_v = warp_top(top_v);
+    most = __reduce_max_sync(0xffffffffu, most);
+    const float top_v = __uint_as_float(most);
     if (top_m < SMALLEST) top_m = 0.f;
     const float top_r = __fsqrt_rn(top_v);
-    if (__any_sync(0xffffffffu, odd != 0.f) || (top_v > 0.f && top_r < 1.4210855e-14f)) return false;  // (2^-46)
+    // (a square that is not finite leaves v so)
+    if (most >= 0x7f800000u || (top_v > 0.f && top_r < 1.4210855e-14f)) return false;  // (2^-46)
     // the four quotients in four lanes at once: 448 / top, top / 448 and the root's
     const float top = lane & 1 ? top_r : top_m, full = lane & 1 ? 1.9375f : 448.f;
     const float q = top > 0.f ? __fdiv_rn(lane & 2 ? top : full, lane & 2 ? full : top) : 0.f;
