@@ -22,7 +22,7 @@
 //
 // Measured on one GB300: 50 M fp32 values with fp32 states in 192 tensors 207 us
 // (6.8 TB/s: memory); 189 M values, 8-bit states, 16-bit gradient and parameter
-// and an fp32 copy 490 us (6.2 TB/s; some 70 instructions a value, 60% of the issue
+// and an fp32 copy 485 us (6.2 TB/s; some 70 instructions a value, 60% of the issue
 // slots), their states' values in fp32 283 us (6.7 TB/s).
 #include <new>
 
