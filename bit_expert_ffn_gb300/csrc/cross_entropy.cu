@@ -12,9 +12,10 @@
 //   GRAD   z's tiles again, for a piece of the vocabulary; d leaves in 16 bits
 //   PROD   both gradients of a piece in one launch: dh (K over the piece's
 //          columns) and dW (K over the tokens)
-// d is divided by the call's largest |dloss| or |dlse| before its rounding (so
-// fp16 holds it, and the usual equal weights leave no rounding of their own) and
-// the gradients are multiplied by it.
+// d is divided by the call's largest |dloss| or |dlse| that is finite before its
+// rounding (so fp16 holds it, and the usual equal weights leave no rounding of
+// their own) and the gradients are multiplied by it.  A weight that is not finite
+// so stays in what its token reaches.
 //
 // d is row-major [T][piece]: for dh it is the A operand as it lies (K inner), for
 // dW it is A with M inner, and W and h are B with N inner: the tensor cores take
@@ -99,7 +100,7 @@ struct Params {
     float2 *stats;      // [T][n tiles][2]
     float *label_z;
     const float *lse, *dloss, *dlse;
-    float *top;         // the largest |dloss| or |dlse|: written by GRAD, for PROD
+    float *top;         // the largest finite |dloss| or |dlse|, 1 where there is none above zero: written by GRAD, for PROD
     int32_t *status;
 };
 
@@ -444,24 +445,26 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
         char *out = sO + (warp - EPI_WARP0) * OUT_BYTES;
         int j = 0, turn = 0;
         bool was32 = false;
-        // the largest |dloss| or |dlse| of the tokens that count, by every CTA for itself, under its first tile's products
+        // the largest finite |dloss| or |dlse| of the tokens that count, by every CTA for itself, under its first tile's products
         float top = K == PROD ? *p.top : 0.f;
+        auto raise = [&](float x) { top = fabsf(x) < INFINITY ? fmaxf(top, fabsf(x)) : top; };
         if (K == GRAD) {
 #pragma unroll 4
             for (int t = threadIdx.x - EPI_WARP0 * 32; t < p.T; t += EPI_WARPS * 32) {
                 const int label = p.labels[t];
-                if (label >= 0 && label < p.all) top = fmaxf(top, fabsf(p.dloss[t]));
-                if (p.dlse) top = fmaxf(top, fabsf(p.dlse[t]));
+                if (label >= 0 && label < p.all) raise(p.dloss[t]);
+                if (p.dlse) raise(p.dlse[t]);
             }
             top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
             if (lane == 0) S.top[warp - EPI_WARP0] = top;
             tc::named_sync(1, EPI_WARPS * 32);
 #pragma unroll
             for (int w = 0; w < EPI_WARPS; w++) top = fmaxf(top, S.top[w]);
+            if (top == 0.f) top = 1.f;
             if (blockIdx.x == 0 && threadIdx.x == EPI_WARP0 * 32) *p.top = top;
         }
         const float up = K == PROD ? (p.f16 ? top / F16_ROOM : top) : 0.f;
-        const float down = K == GRAD && top > 0.f ? (p.f16 ? F16_ROOM : 1.f) : 0.f;
+        const float down = p.f16 ? F16_ROOM : 1.f;
         // what a row needs comes while the tile before is on its way out
         Item m, next;
         Row in = {}, ahead = {};
@@ -493,8 +496,8 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                 const bool there = label >= 0 && label < p.all;
                 b = there ? in.dloss : 0.f;
                 a = b + (p.dlse ? in.dlse : 0.f);
-                a = down > 0.f ? a / top * down : 0.f;
-                b = down > 0.f ? b / top * down : 0.f;
+                a = a / top * down;
+                b = b / top * down;
                 lse = in.lse;
                 nl = -lse * LOG2E;
                 if (fabsf(lse) < FUSED) a *= ex2(-fmaf(lse, LOG2E, nl));  // (what the product's rounding left out)

@@ -693,11 +693,12 @@ moe_status moe_router_loss_backward(const void *logits, moe_dtype dtype, int T, 
  * either of which may be NULL.  accumulate adds to dw as it is (MOE_F32 only;
  * one addition per value and call).  The products are computed again, in
  * pieces of the vocabulary: d enters the two gradients rounded to h's type,
- * relative to the largest |dloss| or |dlse| of the call, and is held for one
- * piece at a time (at most 256 MiB of the workspace, at least 256 columns of
- * the vocabulary); a product over the whole of T or V is summed in fp32 and
- * rounded once.  dh and dw must not overlap h and w.  With T = 0 dw is set to
- * zero unless it is accumulated.
+ * relative to the largest finite |dloss| or |dlse| of the call, and is held for
+ * one piece at a time (at most 256 MiB of the workspace, at least 256 columns
+ * of the vocabulary); a product over the whole of T or V is summed in fp32 and
+ * rounded once.  A dloss or dlse that is not finite makes its token's dh, and
+ * dw, so too, and no other token's dh.  dh and dw must not overlap h and w.
+ * With T = 0 dw is set to zero unless it is accumulated.
  * A wait that runs out (about 2 s) sets MOE_ERR_TIMEOUT.
  */
 moe_status moe_cross_entropy_workspace_size(int T, int H, int V, size_t *bytes);
