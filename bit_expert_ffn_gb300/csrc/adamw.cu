@@ -179,7 +179,17 @@ __device__ __forceinline__ void load8(const void *p, int64_t base, int64_t left,
 
 struct Scalars {
     float scale, shrink, rate, root2;
-    float root2_rate, eps_rate;  // root2 and eps over the rate (a product less a value); a rate of 0: 0 and infinity
+    float before, after;  // block: the rate multiplies m, or, where that could leave fp32's normal range, the quotient
+    float root2_rate, eps_rate;  // for block8: root2 and eps over the rate (a product less a value); a rate of 0: 0 and infinity
+
+    // Whether block8's steps are the exact ones to 2^-22: its roots of v below 2^-126 are 0, which counts for nothing beside eps
+    // where root2 2^-63 is below eps 2^-24; and its reciprocals keep no number below 2^-126, so that root2 r / rate (r below
+    // 2^64, since squares are finite) and eps / rate stay between 2^-79 and 2^125.
+    __device__ bool fast(float eps) const
+    {
+        return eps >= root2 * 1.8189894e-12f && eps <= 1.2089258e24f && root2 <= 1048576.f &&  // (2^-39, 2^80, 2^20)
+               (rate == 0.f || (fabsf(rate) >= 9.0949470e-13f && fabsf(rate) <= 1.0995116e12f));  // (2^-40, 2^40)
+    }
 };
 
 // 256 values: with fp32 states (kVec: aligned for fours), or, k8, with 8-bit ones, value by value.
@@ -252,7 +262,7 @@ __device__ __forceinline__ void block(const Common &c, const Tensor &t, const Sc
         v[i] = ok ? vn : v[i];
         if (k8) r[i] = __fsqrt_rn(v[i]);
         else asm("sqrt.approx.f32 %0, %1;" : "=f"(r[i]) : "f"(v[i]));
-        const float to = __fdividef(m[i] * s.rate, fmaf(r[i], s.root2, c.eps));
+        const float to = __fdividef(m[i] * s.before, fmaf(r[i], s.root2, c.eps)) * s.after;
         x[i] = ok ? fmaf(x[i], s.shrink, -to) : x[i];
         bad += !ok;
         if (k8) top_m = fmaxf(top_m, fabsf(m[i])), top_r = fmaxf(top_r, r[i]);
@@ -516,15 +526,17 @@ __global__ void __launch_bounds__(THREADS, 3) step_kernel(const __grid_constant_
     lr *= t.lr_factor;
     s.rate = lr * rate1;
     s.shrink = 1.f - lr * t.decay;
-    const bool moves = fabsf(s.rate) >= 1e-35f;  // (below that the quotients could leave fp32)
-    s.root2_rate = moves ? s.root2 / s.rate : 0.f;
-    s.eps_rate = moves ? c.eps / s.rate : INFINITY;
+    const bool tiny = s.rate != 0.f && fabsf(s.rate) < 9.0949470e-13f;  // (2^-40)
+    s.before = tiny ? 1.f : s.rate;
+    s.after = tiny ? s.rate : 1.f;
+    s.root2_rate = s.rate == 0.f ? 0.f : s.root2 / s.rate;
+    s.eps_rate = s.rate == 0.f ? INFINITY : c.eps / s.rate;
     const int lane = lane_id();
     const int64_t begin = (int64_t)(blockIdx.x - p.first[which]) * c.chunk, end = min(begin + c.chunk, t.n);
     const int64_t first = begin + warp_id() * BLOCK;
     if (k8) {
         uint32_t left = ~0u;
-        if (t.vec && first < end)
+        if (t.vec && first < end && s.fast(c.eps))
             on_type(t.gt, [&](auto g) {
                 on_type(t.master ? (int)MOE_F32 : t.pt,
                         [&](auto x) { left = blocks8<decltype(g), decltype(x)>(c, t, s, first, (int)(end - first), lane); });
