@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
             S.abort = 1;
         }
         if (rank == 0 && elect_one()) commit<C>(&S.mma_done);
-        if (!tc::mbar_wait(&S.mma_done, 0, kWaitNs) && lane == 0) set_status(p.status, MOE_ERR_TIMEOUT);
+        if (rank == 0 && !tc::mbar_wait(&S.mma_done, 0, kWaitNs) && lane == 0) set_status(p.status, MOE_ERR_TIMEOUT);
     } else {
         // ---------------- sums out
         const int q = warp & 3, side = (warp - EPI_WARP0) >> 2;
@@ -613,6 +613,8 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
             if (lane == 0) arrive_leader<C>(&S.acc_empty[acc]);
         }
         if (K != LOSS && lane == 0) tc::bulk_wait_all();
+        // the pair's second CTA issues no products: its wait for their end, and with it the limit, begins where its last tile is out
+        if (rank == 1 && warp == EPI_WARP0 && !tc::mbar_wait(&S.mma_done, 0, kWaitNs) && lane == 0) set_status(p.status, MOE_ERR_TIMEOUT);
     }
     tc::tc_fence_before();
     tile_sync<C>();  // neither CTA leaves while the other's products read its operands or write its sums
