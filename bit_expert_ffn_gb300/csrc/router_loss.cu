@@ -20,6 +20,7 @@
 // (201 MB, part of the logits still in L2); 32 x 512 5.2 us, one launch (device
 // times).  Twelve warps a CTA and two CTAs an SM: with 16 the two rows spill.
 #include "cluster.cuh"
+#include "router_loss_deal.cuh"
 #include "rows.cuh"
 
 namespace moe {
@@ -114,7 +115,8 @@ __device__ __forceinline__ void finish(const Params &p, int parts, G get, float 
     const int C = gridDim.x, r = C > 1 ? (int)cluster_rank() : 0, tid = threadIdx.x;
     const int E = p.E, units = (E + V - 1) / V;
     const int e0 = (int)((int64_t)units * r / C) * V, w = (int)((int64_t)units * (r + 1) / C) - e0 / V;
-    const int per = min(w, kThreads), groups = max(1, min(kThreads / max(per, 1), parts));
+    const Deal d = deal(w, kThreads, parts, V);
+    const int per = d.per, groups = d.groups;
     const int g = per ? tid / per : groups, c0 = per ? tid % per : 0;
     __shared__ float s_n, s_z, s_dot[kThreads / 32];
     __shared__ int s_tok;
@@ -159,8 +161,8 @@ __device__ __forceinline__ void finish(const Params &p, int parts, G get, float 
             if ((tid & 31) == 0) s_tok = n, s_n = n > 0 ? (float)n : 1.f, s_z = z;
         }
         __syncthreads();
-        const int values = 2 * V * per, turns = kThreads / values;
-        const bool twice = groups >= 16 && turns >= 2;  // many groups: their sums by all threads, then the threads'
+        const int values = d.values, turns = d.turns;
+        const bool twice = d.twice;
         if (twice) {
             float f = 0.f;
             int k = 0;
