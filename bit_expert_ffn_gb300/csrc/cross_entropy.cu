@@ -40,6 +40,8 @@
 // Every wait is bounded: after about 2 s the CTA records MOE_ERR_TIMEOUT and
 // stops.
 #include "cluster.cuh"
+#include "common.cuh"
+#include "cross_entropy_plan.cuh"
 #include "dense_tc.cuh"
 #include "rows.cuh"
 #include "tc.cuh"
@@ -53,7 +55,6 @@ using tc::uniform;
 
 enum Kind { LOSS, GRAD, PROD };
 
-constexpr int ROWS = 128, BN = 256, BK = 64;  // a CTA's rows of a tile, its most columns, K of a step
 constexpr int A_BYTES = ROWS * BK * 2;
 
 // A tile is one CTA's (C = 1: 128 rows) or a pair's (C = 2: 256 rows), each with its rows of A and its half of B's columns.
@@ -70,7 +71,6 @@ constexpr int BAND_ROWS = 4096;  // rows that pass over the columns together
 constexpr unsigned long long kWaitNs = 2000000000ull;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float FUSED = 1e6f;  // below it x log2 e is rounded by at most 1/16
-constexpr size_t PIECE_BYTES = 256u << 20;
 constexpr float F16_ROOM = 16384.f;  // |d| <= 1 after the division: as fp16, 2^14 times that
 
 struct Job {
@@ -691,109 +691,6 @@ __global__ void __launch_bounds__(256) round_kernel(const float *in, int parts, 
     }
 }
 
-static int tiles(int n, int b) { return (n + b - 1) / b; }
-
-// Columns of a piece: what 256 MiB hold, in whole tiles, and pieces of nearly equal size.
-static int piece_columns(int T, int V)
-{
-    const int64_t most = std::max<int64_t>(BN, (int64_t)(PIECE_BYTES / 2 / std::max(T, 1)) / BN * BN);
-    const int64_t pieces = (V + most - 1) / most;
-    return (int)((V + pieces - 1) / pieces + BN - 1) / BN * BN;
-}
-
-static int round_up(int n, int b) { return tiles(n, b) * b; }
-
-// Rows of a box of tokens: a single CTA's first tile has them all, where there are few.
-static int box_rows(int T, int C) { return C == 1 && T < ROWS ? round_up(T, 8) : ROWS; }
-
-// Columns of a tile: equal ones over all n.
-static int tile_columns(int n) { return round_up(tiles(n, tiles(n, BN)), 32); }
-
-// Measured time of a step (K = 64) of 256 columns in us: pairs read and store less through shared memory per product and
-// have two more steps on their way (4,096 x 2,048 against 65,536: 563 us by single CTAs, 516 by pairs).
-static double step_us(int C) { return C == 1 ? 0.325 : 0.298; }
-
-// Tiles of the logits: by single CTAs or pairs, as wide as they go unless narrower ones fill the last round better
-// (100,003 columns for one row tile on 152 SMs: three rounds of 224 instead of 256).  A tile costs its steps and some 16
-// columns' worth besides.
-struct Cut {
-    int C, bn;
-};
-
-static Cut cut_logits(int rows, int V, int sms)
-{
-    Cut best = {1, BN};
-    double least = 1e300;
-    for (int C = 1; C <= 2; C++)
-        for (int bn = BN; bn >= 128; bn -= 32) {
-            const int64_t items = (int64_t)tiles(rows, ROWS * C) * tiles(V, bn), at_once = sms / C;
-            const double cost = (double)((items + at_once - 1) / at_once) * (bn + 16) * step_us(C);
-            if (cost < least) least = cost, best = {C, bn};
-        }
-    return best;
-}
-
-// What a CTA of the gradients takes, in steps of BK: dh's items (nk0 each) dealt out first, dW's (nk1 each) so that the
-// longest CTA is as short as it gets.
-struct Deal {
-    int longer, long_items, short_items;
-    int64_t steps;
-};
-
-static Deal deal(int64_t items0, int64_t nk0, int64_t items1, int64_t nk1, int64_t G)
-{
-    // a tile's way out takes as long as some six steps, under the next tile's steps where those are more
-    nk0 = std::max<int64_t>(nk0, 6);
-    nk1 = std::max<int64_t>(nk1, 6);
-    Deal best = {0, 0, 0, INT64_MAX};
-    const int64_t q = items0 / G, r = items0 % G;
-    auto with = [&](int64_t s) {  // s items of the second job for a CTA without an extra one of the first
-        const int64_t rest = std::max<int64_t>(0, items1 - (G - r) * s);
-        if (s < 0 || (r == 0 && rest > 0)) return;
-        const int64_t l = r ? (rest + r - 1) / r : s;
-        const int64_t steps = std::max(r ? (q + 1) * nk0 + l * nk1 : 0, q * nk0 + s * nk1);
-        if (steps < best.steps) best = {(int)r, (int)l, (int)s, steps};
-    };
-    with((items1 + G - r - 1) / (G - r));
-    if (items1 > 0) {  // about where all have the same
-        const int64_t s = ((items0 * nk0 + items1 * nk1) / G - q * nk0) / nk1;
-        for (int64_t i = s - 1; i <= s + 2; i++) with(i);
-    }
-    return best;
-}
-
-struct Layout {
-    int columns, pieces, parts, C;  // dh's sums over a piece are split into parts; by CTAs or pairs
-    int64_t part_rows;
-    size_t d, sums, total;  // bytes: d after the top value, fp32 sums of dh when there are several pieces or parts
-};
-
-// Splitting dh's sums pays where its few, long items would leave the other CTAs waiting: the steps' time is weighed
-// against a part's sums, written and read (8 bytes a value at 6 TB/s), and a launch for them.
-static Layout layout(int T, int H, int V)
-{
-    Layout l;
-    const int sms = sm_count();
-    l.columns = piece_columns(T, V);
-    l.pieces = tiles(V, l.columns);
-    const int n = std::min(V, l.columns), nk0 = tiles(n, BK), nk1 = tiles(T, BK), nt = tiles(H, BN);
-    double least = 1e300;
-    for (int C = 1; C <= 2; C++) {
-        const int64_t items0 = (int64_t)tiles(T, ROWS * C) * nt, items1 = (int64_t)tiles(n, ROWS * C) * nt;
-        for (int s = 1; s <= 32 && s <= nk0; s++) {
-            const Deal d = deal(items0 * s, tiles(nk0, s), items1, nk1, std::min<int64_t>(items0 * s + items1, sms / C));
-            const double us = step_us(C) * tile_columns(H) / BN * d.steps +
-                              (s > 1 || l.pieces > 1 ? 3.0 / l.pieces + 1.3e-6 * s * T * H * (l.pieces > 1 ? 2 : 1) : 0);
-            if (us < least) least = us, l.parts = s, l.C = C;
-        }
-    }
-    l.part_rows = round_up(T, ROWS * l.C);
-    l.d = 256;
-    l.sums = l.d + align256((size_t)T * l.columns * 2);
-    l.total = l.sums + (l.pieces > 1 || l.parts > 1 ? align256((size_t)l.parts * l.part_rows * H * 4) : 0);
-    return l;
-}
-
 static moe_status check(int T, int H, int V)
 {
     MOE_REQUIRE(T >= 0 && T <= (1 << 24), "T must be in [0, 2^24] (got %d)", T);
@@ -871,7 +768,7 @@ extern "C" moe_status moe_cross_entropy_workspace_size(int T, int H, int V, size
     MOE_REQUIRE(bytes, "bytes must not be NULL");
     moe_status st = check(T, H, V);
     if (st != MOE_OK) return st;
-    *bytes = align256((size_t)T * 4) + align256((size_t)tiles(V, cut_logits(T, V, sm_count()).bn) * T * 16);
+    *bytes = align256((size_t)T * 4) + stats_bytes(T, V, sm_count());
     return MOE_OK;
 }
 
@@ -916,7 +813,7 @@ extern "C" moe_status moe_cross_entropy_backward_workspace_size(int T, int H, in
     MOE_REQUIRE(bytes, "bytes must not be NULL");
     moe_status st = check(T, H, V);
     if (st != MOE_OK) return st;
-    *bytes = T ? layout(T, H, V).total : 0;
+    *bytes = T ? layout_bytes(T, H, V) : 0;
     return MOE_OK;
 }
 
@@ -939,7 +836,7 @@ extern "C" moe_status moe_cross_entropy_backward(const void *h, moe_dtype dtype,
     if (!dh && !dw) return MOE_OK;
     MOE_REQUIRE(lse && dloss, "NULL pointer");
     MOE_REQUIRE(aligned_to(lse, 4) && aligned_to(dloss, 4) && aligned_to(dlse, 4), "lse, dloss and dlse must be 4-byte aligned");
-    const Layout l = layout(T, H, V);
+    const Layout l = layout(T, H, V, sm_count());
     if (ws_bytes < l.total || !ws)
         return fail(MOE_ERR_WORKSPACE, "moe_cross_entropy_backward needs %zu bytes of workspace (got %zu)", l.total,
                     ws ? ws_bytes : (size_t)0);

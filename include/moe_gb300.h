@@ -700,6 +700,9 @@ moe_status moe_router_loss_backward(const void *logits, moe_dtype dtype, int T, 
  * dw, so too, and no other token's dh.  dh and dw must not overlap h and w.
  * With T = 0 dw is set to zero unless it is accumulated.
  * A wait that runs out (about 2 s) sets MOE_ERR_TIMEOUT.
+ *
+ * Both sizes grow with T: a workspace of the largest batch's size is enough
+ * for every smaller one of the same H and V.
  */
 moe_status moe_cross_entropy_workspace_size(int T, int H, int V, size_t *bytes);
 moe_status moe_cross_entropy(const void *h, moe_dtype dtype, int T, int H, const void *w, int V,
