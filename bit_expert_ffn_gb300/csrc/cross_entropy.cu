@@ -447,13 +447,23 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
         bool was32 = false;
         // the largest finite |dloss| or |dlse| of the tokens that count, by every CTA for itself, under its first tile's products
         float top = K == PROD ? *p.top : 0.f;
-        auto raise = [&](float x) { top = fabsf(x) < INFINITY ? fmaxf(top, fabsf(x)) : top; };
+        auto finite = [](float x, bool there) { return there && fabsf(x) < INFINITY ? fabsf(x) : 0.f; };
         if (K == GRAD) {
-#pragma unroll 4
-            for (int t = threadIdx.x - EPI_WARP0 * 32; t < p.T; t += EPI_WARPS * 32) {
-                const int label = p.labels[t];
-                if (label >= 0 && label < p.all) raise(p.dloss[t]);
-                if (p.dlse) raise(p.dlse[t]);
+            // (all loads of a turn before the first use, and none that waits for a label)
+            constexpr int AT_ONCE = 8, STEP = EPI_WARPS * 32;
+            for (int t0 = threadIdx.x - EPI_WARP0 * 32; t0 < p.T; t0 += AT_ONCE * STEP) {
+                int label[AT_ONCE];
+                float b[AT_ONCE], e[AT_ONCE];
+#pragma unroll
+                for (int i = 0; i < AT_ONCE; i++) {
+                    const int t = t0 + i * STEP;
+                    label[i] = t < p.T ? p.labels[t] : -1;
+                    b[i] = t < p.T ? p.dloss[t] : 0.f;
+                    e[i] = t < p.T && p.dlse ? p.dlse[t] : 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < AT_ONCE; i++)
+                    top = fmaxf(top, fmaxf(finite(b[i], label[i] >= 0 && label[i] < p.all), finite(e[i], true)));
             }
             top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
             if (lane == 0) S.top[warp - EPI_WARP0] = top;

@@ -57,3 +57,18 @@ def test_a_weight_of_no_token(moe):
         dloss[1] = bad
         got = backward(h, w, labels, m.MOE_BF16, lse, dloss)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("at", [0, 255, 256, 2047, 2048, 4095, 4999])
+@pytest.mark.parametrize("which", ["dloss", "dlse"])
+def test_the_largest_weight_in_any_place(moe, which, at):
+    """In fp16 a weight 10,000 times the others' would leave the range, were it not found."""
+    T, H, V = 5000, 64, 300
+    h, w, labels, dloss, lse = setup(T, H, V, m.MOE_F16, 13)
+    dloss[:] = 1e-4
+    dlse = torch.full((T,), 1e-4, device=DEV)
+    {"dloss": dloss, "dlse": dlse}[which][at] = -1.0
+    want = cross_entropy(h, w, labels, dloss, dlse)
+    dh, dw = backward(h, w, labels, m.MOE_F16, lse, dloss, dlse)
+    check(dh, want["dh"], want["dh_tol"], "dh")
+    check(dw, want["dw"], want["dw_tol"], "dw")
