@@ -681,9 +681,11 @@ moe_status moe_router_loss_backward(const void *logits, moe_dtype dtype, int T, 
  *   z_t = w h_t,  lse[t] = log sum_v exp(z_tv),  loss[t] = lse[t] - z_t,labels[t]
  * A negative label leaves its token out (loss 0; lse is given all the same);
  * one of V or more does too and sets *dev_status = MOE_ERR_BOUNDS.  Products
- * are exact, sums fp32.  A value that is not finite makes the losses of the
- * tokens that it reaches so too.  H a multiple of 8, V >= 1; h and w 16-byte
- * aligned.  T = 0 is a no-op.
+ * are exact, sums fp32.  A logit of NaN or +inf (values of h or w that are not
+ * finite, sums beyond fp32) makes its token's lse and loss NaN; one of -inf is
+ * a probability of zero (as a label's, its loss is infinite).  No status tells
+ * of either.  H a multiple of 8, V >= 1; h and w 16-byte aligned.  T = 0 is a
+ * no-op.
  *
  * moe_cross_entropy_backward: with dloss [T] and dlse [T] (NULL: zero) the
  * gradients of loss and lse, and d_tv = exp(z_tv - lse[t]) (dloss[t] + dlse[t])
@@ -697,8 +699,11 @@ moe_status moe_router_loss_backward(const void *logits, moe_dtype dtype, int T, 
  * one piece at a time (at most 256 MiB of the workspace, at least 256 columns
  * of the vocabulary); a product over the whole of T or V is summed in fp32 and
  * rounded once.  A dloss or dlse that is not finite makes its token's dh, and
- * dw, so too, and no other token's dh.  dh and dw must not overlap h and w.
- * With T = 0 dw is set to zero unless it is accumulated.
+ * dw, so too, and no other token's dh; so does a lse that is not finite, of a
+ * token whose weights are not zero.  A value w[v][j] (or h[t][j]) that is not
+ * finite leaves no finite value in column j of dh (or dw): a d of zero times it
+ * is NaN.  dh and dw must not overlap h and w.  With T = 0 dw is set to zero
+ * unless it is accumulated.
  * A wait that runs out (about 2 s) sets MOE_ERR_TIMEOUT.
  *
  * Both sizes grow with T: a workspace of the largest batch's size is enough
