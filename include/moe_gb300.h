@@ -771,8 +771,12 @@ typedef struct moe_adamw_options {
  * above (no product is fused with a sum), so that the codes do not depend on a
  * machine's or compiler's choices.  x is updated from m and v before they are
  * rounded to 8 bits.  A v that changes by less than half a step of its code
- * (some 3 to 6 percent) keeps it: with beta2 near 1, a small change of the
- * gradients' size is followed late.
+ * (some 3 to 6 percent) keeps it, and the change is lost.  With beta2 up to some
+ * 0.97 v is followed all the same.  With 0.999 a v that falls is NOT followed: a
+ * step takes a thousandth of it, and where the gradients become ten times
+ * smaller the root stays up to ten times, and the steps so much too small, for
+ * good (a growing v is followed only from gradients whose squares are 30 to 60
+ * times v).  Such a beta2 wants fp32 states.
  *
  * moe_adamw_states: the values that the states stand for, in fp32, tensor i's
  * to m_values[i] and v_values[i] (host arrays of device pointers, NULL entries
