@@ -6,6 +6,7 @@
 //   d = exp(z - lse) (dloss + dlse) - onehot dloss
 //   dh = d W, dW = d^T h
 //
+// How they are cut into tiles, pieces and parts is cross_entropy_plan.cuh's.
 // Three kinds of product share one kernel:
 //   LOSS   z's tiles; each row's maximum and sum of exponentials over the
 //          tile's columns leave (8 bytes a warp's half of them), and its label's z
@@ -29,10 +30,11 @@
 // that all CTAs end together; dh's long sums are split into parts where they are
 // too few for that.
 //
-// Measured on one GB300 (bf16, H = 2,048): 4,096 tokens against 65,536 words 519
-// us (2.1 PFLOP/s; by single CTAs 563), with both gradients 2.44 ms (1.8 PFLOP/s,
-// power-bound; by single CTAs 2.69); four tokens against 100,003 words 69 us (410
-// MB of W, 6.0 TB/s); 1,111 tokens, H = 1,056, 8,191 words with gradients 70 us.
+// Measured on one GB300 (bf16, H = 2,048): 4,096 tokens against 65,536 words 612
+// to 622 us in a long run (1.8 PFLOP/s, power-bound), 523 while the clocks are
+// still up (by single CTAs 557); with both gradients 2.57 to 2.64 ms (1.7 PFLOP/s),
+// 2.44 at first (by single CTAs 2.61); four tokens against 100,003 words 67 us (410
+// MB of W, 6.1 TB/s); 1,111 tokens, H = 1,056, 8,191 words with gradients 71 us.
 // Tried without gain: W on its way to L2 in boxes of 512 bytes a row (four tokens,
 // 10 us more), results straight from the registers, the next columns loaded from
 // tensor memory ahead, four blocks of results on their way instead of two.

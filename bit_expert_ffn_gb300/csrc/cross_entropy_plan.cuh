@@ -32,7 +32,10 @@ inline int box_rows(int T, int C) { return C == 1 && T < ROWS ? round_up(T, 8) :
 inline int tile_columns(int n) { return round_up(tiles(n, tiles(n, BN)), 32); }
 
 // Measured time of a step (K = 64) of 256 columns in us: pairs read and store less through shared memory per product and
-// have two more steps on their way (4,096 x 2,048 against 65,536: 563 us by single CTAs, 516 by pairs).
+// have two more steps on their way.  Forward pass by single CTAs and by pairs, us: 4,096 x 65,536 and H = 2,048 557 and
+// 523, 2,048 x 32,768 176 and 144, 512 x 32,000 49 and 42, 2,500 x 20,000 with H = 4,096 241 and 227.  The rule holds
+// where a tile's steps cover its way out: with H = 512 and below pairs are taken too often (4,096 x 16,384 48 and 60,
+// 1,500 x 30,000 with H = 256 25 and 32).
 inline double step_us(int C) { return C == 1 ? 0.325 : 0.298; }
 
 // Tiles of the logits: by single CTAs or pairs, as wide as they go unless narrower ones fill the last round better

@@ -29,7 +29,9 @@ namespace rl {
 constexpr int MAX_E = 1024, MAX_K = 16;
 constexpr int WARPS = 12, THREADS = WARPS * 32;
 constexpr int MAX_CLUSTER = 8;
-constexpr int CLUSTER_ROWS = 384;  // up to this many tokens are one cluster's (512 columns, device time: 7.5 us at 384 both ways, at 512 8.5 against 7.5)
+// Up to this many tokens are one cluster's.  Device times by one cluster and by two launches, us: 384 tokens of 64 columns
+// 5.9 and 6.1, of 512 7.5 and 7.8, of 1,024 8.4 and 8.9; 512 tokens 6.6 and 6.2, 8.6 and 7.7, 9.8 and 9.1.
+constexpr int CLUSTER_ROWS = 384;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float FUSED = 1e6f;  // below it x log2 e is rounded by at most 1/16
 
